@@ -293,6 +293,102 @@ sketchssm_status sketchssm_rmw_step(const sketchssm_shape* shape, float* S, cons
                                     const void* k, const void* v, const float* a,
                                     const float* beta, float* y, void* stream);
 
+/*
+ * Ragged batches.  The two calls below run n_seqs sequences of different
+ * lengths, packed one behind the other in one token axis, through the exact
+ * state update S <- M S + beta k v^T, y = S^T q.  Per sequence they read a first
+ * state, output y for each of its tokens and write its last state.
+ *   S0      device [n_rows0,H,K,V] fp32, the first states (e.g. a cache of
+ *           prompt prefixes); may be S itself; NULL: every sequence starts from
+ *           zero (n_rows0 is then not used)
+ *   rows0   device [n_seqs] int32: row of S0 that sequence i starts from, a
+ *           negative value for zero; several sequences may share a row.  NULL:
+ *           the same rows as `rows`; must be NULL without S0
+ *   S       device [B,H,K,V] fp32: row rows[i] receives sequence i's last state
+ *           (the first state unchanged if the sequence is empty)
+ *   rows    device [n_seqs] int32, each row at most once per call; NULL:
+ *           sequence i is row i
+ *   offsets device [n_seqs + 1] int32: sequence i is tokens offsets[i] ..
+ *           offsets[i+1]-1
+ *   n_seqs  >= 0; 0 does nothing
+ *   total_tokens  tokens in the arrays below (at least offsets[n_seqs]); tokens
+ *           outside every sequence are not read and their y is left as it was
+ *   max_len >= 0: the caller's bound on the sequences' lengths
+ *   q, k    device [total_tokens,Hk,K] qkv dtype
+ *   v       device [total_tokens,H,V] qkv dtype
+ *   a       device [total_tokens,H] fp32 (Mamba-2, GDN) or [total_tokens,H,K] (KDA)
+ *   beta    device [total_tokens,H] fp32 (GDN, KDA); NULL for Mamba-2
+ *   y       device [total_tokens,H,V] fp32, out
+ * The lists are read on the device, so bad values are not reported: a sequence
+ * whose row is outside 0 .. B-1, whose first row is n_rows0 or more, whose
+ * offsets decrease or leave 0 .. total_tokens, or which is longer than max_len
+ * is idle (nothing of it is read or written).  Where S0 is S (or overlaps it),
+ * a sequence must start from its own row, from zero, or from a row that no
+ * sequence of the call writes.  No window, plan, sketch or basis is involved:
+ * form a written row's sketch with sketchssm_flush_seq (0 tokens) before its
+ * first decode read.
+ */
+
+/*
+ * The recurrent form, for a few tokens of each sequence (one decode token,
+ * drafted tokens, a prompt's tail): token by token on a state held in
+ * registers, so the state moves once whatever the number of tokens.
+ */
+sketchssm_status sketchssm_rmw_seq(const sketchssm_shape* shape, const float* S0, int32_t n_rows0,
+                                   const int32_t* rows0, float* S, const int32_t* rows,
+                                   const int32_t* offsets, int32_t n_seqs, int32_t total_tokens,
+                                   int32_t max_len, const void* q, const void* k, const void* v,
+                                   const float* a, const float* beta, float* y, void* stream);
+
+/*
+ * The chunked form, for prompts: the same outputs up to rounding, in chunks of
+ * tokens whose products run on the matrix cores.
+ *   workspace  device scratch of at least sketchssm_prefill_workspace bytes
+ *           (its contents need not be kept between calls; calls that may run at
+ *           the same time need one each); NULL if that is 0
+ *   workspace_bytes  its size; SKSSM_ESHAPE if too small
+ */
+sketchssm_status sketchssm_prefill(const sketchssm_shape* shape, const float* S0, int32_t n_rows0,
+                                   const int32_t* rows0, float* S, const int32_t* rows,
+                                   const int32_t* offsets, int32_t n_seqs, int32_t total_tokens,
+                                   int32_t max_len, const void* q, const void* k, const void* v,
+                                   const float* a, const float* beta, float* y, void* workspace,
+                                   size_t workspace_bytes, void* stream);
+
+/* Host only.  Bytes of workspace of a sketchssm_prefill call with these sizes;
+ * 0 also for arguments that the call refuses. */
+size_t sketchssm_prefill_workspace(const sketchssm_shape* shape, int32_t n_seqs, int32_t total_tokens,
+                                   int32_t max_len);
+
+typedef enum {
+    SKSSM_GATE_NONE = 0,       /* out = norm(x) w */
+    SKSSM_GATE_SILU_FIRST = 1, /* out = norm(x silu(z)) w   (a Mamba-2 layer) */
+    SKSSM_GATE_SILU = 2,       /* out = norm(x) w silu(z)   (a Gated DeltaNet layer) */
+    SKSSM_GATE_SIGMOID = 3     /* out = norm(x) w sigmoid(z)   (a KDA layer) */
+} sketchssm_gate;
+
+/*
+ * The gated norm between a layer's y (of any read, step or prefill) and its
+ * output projection: x = y + D skip, then one of the forms above, with
+ * norm(x) = x / sqrt(mean(x^2) + eps) over groups of norm_heads consecutive heads.
+ * Sums and products in fp32, one rounding to the qkv dtype at the end.
+ *   y       device [n_tokens,H,V] fp32
+ *   skip    device [n_tokens,H,V] qkv dtype or NULL (a Mamba-2 layer's D skip
+ *           adds its v); D device [H] fp32, NULL without skip
+ *   z       device [n_tokens,H,V] qkv dtype; NULL for SKSSM_GATE_NONE
+ *   weight  device [H,V] fp32 (weight_heads = H) or [V] (weight_heads = 1, every
+ *           head the same)
+ *   norm_heads  must divide H (1: a norm per head)
+ *   gate    sketchssm_gate;  eps >= 0
+ *   n_tokens >= 0; 0 does nothing
+ *   out     device [n_tokens,H,V] qkv dtype
+ * Of the shape, H, V and qkv are used.
+ */
+sketchssm_status sketchssm_gated_norm(const sketchssm_shape* shape, const float* y, const void* skip,
+                                      const float* D, const void* z, const float* weight,
+                                      int32_t weight_heads, int32_t norm_heads, int32_t gate, float eps,
+                                      int32_t n_tokens, void* out, void* stream);
+
 /* Static English text for a status code. */
 const char* sketchssm_status_string(sketchssm_status status);
 

@@ -5,6 +5,7 @@ arguments.  Import fails loudly at first use if the library is not built.
 """
 from .binding import (  # noqa: F401
     DTYPE,
+    GATE,
     KIND,
     LIB_PATH,
     Plan,
@@ -18,6 +19,10 @@ from .binding import (  # noqa: F401
     sketchssm_dense_read,
     sketchssm_flush,
     sketchssm_flush_seq,
+    sketchssm_gated_norm,
+    sketchssm_prefill,
+    sketchssm_prefill_workspace,
+    sketchssm_rmw_seq,
     sketchssm_rmw_step,
     sketchssm_stream_probe,
     status_string,

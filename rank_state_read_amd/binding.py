@@ -18,6 +18,7 @@ LIB_PATH = os.path.join(_HERE, "libsketchssm.so")
 
 KIND = {"mamba2": 0, "gdn": 1, "kda": 2}
 DTYPE = {"bf16": 0, "f32": 1}
+GATE = {"none": 0, "silu_first": 1, "silu": 2, "sigmoid": 3}
 STATUS = {0: "SKSSM_OK", 1: "SKSSM_EINVAL", 2: "SKSSM_ESHAPE", 3: "SKSSM_EALIGN",
           4: "SKSSM_ENOMEM", 5: "SKSSM_EDEVICE", 6: "SKSSM_ELAUNCH"}
 
@@ -55,6 +56,12 @@ _PROTOS = {
     "sketchssm_decode_read_seq": (c_i32, [c_vp] * 16),
     "sketchssm_flush_seq": (c_i32, [c_vp] * 10 + [c_i32, c_vp]),
     "sketchssm_decode_read_flush": (c_i32, [c_vp] * 16),
+    "sketchssm_rmw_seq": (c_i32, [ctypes.POINTER(Shape), c_vp, c_i32] + [c_vp] * 4 + [c_i32] * 3 + [c_vp] * 7),
+    "sketchssm_prefill": (c_i32, [ctypes.POINTER(Shape), c_vp, c_i32] + [c_vp] * 4 + [c_i32] * 3 + [c_vp] * 7
+                          + [ctypes.c_size_t, c_vp]),
+    "sketchssm_prefill_workspace": (ctypes.c_size_t, [ctypes.POINTER(Shape)] + [c_i32] * 3),
+    "sketchssm_gated_norm": (c_i32, [ctypes.POINTER(Shape)] + [c_vp] * 5 + [c_i32] * 3 + [ctypes.c_float, c_i32]
+                             + [c_vp] * 2),
     "sketchssm_status_string": (ctypes.c_char_p, [c_i32]),
     "sketchssm_stream_probe": (c_i32, [c_vp, ctypes.c_size_t, c_vp, ctypes.c_size_t, c_i32, c_i32, c_i32, c_vp]),
 }
@@ -221,6 +228,114 @@ def sketchssm_decode_read_flush(plan: Plan, S, Z, frames, basis, q, k, v, a, bet
            lib().sketchssm_decode_read_flush(plan.handle, _ptr(S), _ptr(Z), _ptr(frames), _ptr(basis), _ptr(q),
                                              _ptr(k), _ptr(v), _ptr(a), _ptr(beta), _ptr(kbuf), _ptr(vbuf),
                                              _ptr(abuf), _ptr(bbuf), _ptr(y), _stream(stream)))
+
+
+def _want(name, x, dtype, shape, device):
+    """Refuse a tensor whose type, shape or device is not what the call takes (addresses pass through)."""
+    if x is None or isinstance(x, int):
+        return
+    if x.dtype != dtype or tuple(x.shape) != shape or x.device != device:
+        raise ValueError(f"{name}: expected {dtype} {list(shape)} on {device}, "
+                         f"got {x.dtype} {list(x.shape)} on {x.device}")
+
+
+def _on_device(device, stream):
+    """The context in which a call on tensors of `device` is made: that device current, if it is not."""
+    import contextlib
+
+    import torch
+    if device.index is None or device.index == torch.cuda.current_device():
+        return contextlib.nullcontext()
+    if stream is not None and not isinstance(stream, int) and stream.device != device:
+        raise ValueError(f"the stream is on {stream.device}, the tensors are on {device}")
+    return torch.cuda.device(device)
+
+
+def owned_by(stream, device):
+    """The context in which a tensor for calls on `stream` is allocated: it belongs to that stream, so torch's
+    allocator gives its memory to nothing else before the work queued there is done."""
+    import contextlib
+
+    import torch
+    if stream is None:
+        return contextlib.nullcontext()
+    return torch.cuda.stream(torch.cuda.ExternalStream(stream, device=device) if isinstance(stream, int) else stream)
+
+
+def _ragged(shape, S0, rows0, S, rows, offsets, max_len, q, k, v, a, beta, y):
+    """Checks of the ragged calls' tensors; the arguments both entry points begin with."""
+    import torch
+    dev, i32, f32 = S.device, torch.int32, torch.float32
+    H, K, V, Hk, T = shape.H, shape.K, shape.V, shape.kq_heads or shape.H, v.shape[0]
+    qkv = torch.bfloat16 if shape.qkv == 0 else f32
+    if offsets.dim() != 1 or offsets.numel() < 1:
+        raise ValueError("offsets: expected n_seqs + 1 entries")
+    n = offsets.numel() - 1
+    _want("S", S, f32, (shape.B, H, K, V), dev)
+    if S0 is not None:
+        _want("S0", S0, f32, (S0.shape[0], H, K, V), dev)
+    for name, x in (("rows0", rows0), ("rows", rows)):
+        _want(name, x, i32, (n,), dev)
+    if rows is None and n > shape.B:
+        raise ValueError(f"rows: {n} sequences and {shape.B} state rows")
+    _want("offsets", offsets, i32, (n + 1,), dev)
+    _want("q", q, qkv, (T, Hk, K), dev)
+    _want("k", k, qkv, (T, Hk, K), dev)
+    _want("v", v, qkv, (T, H, V), dev)
+    _want("a", a, f32, (T, H, K) if shape.kind == KIND["kda"] else (T, H), dev)
+    _want("beta", beta, f32, (T, H), dev)
+    _want("y", y, f32, (T, H, V), dev)
+    if S0 is None:
+        rows0 = None
+    return [ctypes.byref(shape), _ptr(S0), 0 if S0 is None else S0.shape[0], _ptr(rows0), _ptr(S), _ptr(rows),
+            _ptr(offsets), n, T, int(max_len), _ptr(q), _ptr(k), _ptr(v), _ptr(a), _ptr(beta), _ptr(y)]
+
+
+def sketchssm_rmw_seq(shape: Shape, S0, rows0, S, rows, offsets, max_len: int, q, k, v, a, beta, y, stream=None):
+    """The recurrent form for a few tokens of each listed sequence."""
+    args = _ragged(shape, S0, rows0, S, rows, offsets, max_len, q, k, v, a, beta, y)
+    with _on_device(S.device, stream):
+        _check("sketchssm_rmw_seq", lib().sketchssm_rmw_seq(*args, _stream(stream)))
+
+
+def sketchssm_prefill(shape: Shape, S0, rows0, S, rows, offsets, max_len: int, q, k, v, a, beta, y, workspace=None,
+                      stream=None):
+    """The chunked form for ragged prompts.  `workspace`: a uint8 tensor of at least
+    ``sketchssm_prefill_workspace`` bytes; None takes one from torch's allocator for this call."""
+    import torch
+    args = _ragged(shape, S0, rows0, S, rows, offsets, max_len, q, k, v, a, beta, y)
+    with _on_device(S.device, stream):
+        st = _stream(stream)
+        if workspace is None:
+            need = sketchssm_prefill_workspace(shape, args[7], args[8], max_len)
+            if need:
+                with owned_by(stream, S.device):
+                    workspace = torch.empty(need, dtype=torch.uint8, device=S.device)
+        size = 0 if workspace is None else workspace.numel() * workspace.element_size()
+        _check("sketchssm_prefill", lib().sketchssm_prefill(*args, _ptr(workspace), size, st))
+
+
+def sketchssm_prefill_workspace(shape: Shape, n_seqs: int, total_tokens: int, max_len: int) -> int:
+    return int(lib().sketchssm_prefill_workspace(ctypes.byref(shape), int(n_seqs), int(total_tokens), int(max_len)))
+
+
+def sketchssm_gated_norm(shape: Shape, y, skip, D, z, weight, norm_heads: int, gate, eps: float, out, stream=None):
+    """The gated norm behind a layer's output (``gate``: a key of ``GATE`` or its value)."""
+    import torch
+    dev, f32 = y.device, torch.float32
+    qkv = torch.bfloat16 if shape.qkv == 0 else f32
+    full = (y.shape[0], shape.H, shape.V)
+    _want("y", y, f32, full, dev)
+    for name, x in (("skip", skip), ("z", z), ("out", out)):
+        _want(name, x, qkv, full, dev)
+    _want("D", D, f32, (shape.H,), dev)
+    w_heads = 1 if weight.dim() == 1 else weight.shape[0]
+    _want("weight", weight, f32, (shape.V,) if weight.dim() == 1 else (w_heads, shape.V), dev)
+    with _on_device(dev, stream):
+        _check("sketchssm_gated_norm",
+               lib().sketchssm_gated_norm(ctypes.byref(shape), _ptr(y), _ptr(skip), _ptr(D), _ptr(z), _ptr(weight),
+                                          w_heads, int(norm_heads), GATE[gate] if isinstance(gate, str) else int(gate),
+                                          float(eps), full[0], _ptr(out), _stream(stream)))
 
 
 def sketchssm_stream_probe(src, read_bytes: int, dst, write_bytes: int, unroll: int = 8, blocks: int = 0,

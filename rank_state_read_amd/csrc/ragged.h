@@ -1,0 +1,58 @@
+// Ragged batches: which state rows and tokens a sequence of a call stands for.
+#pragma once
+
+#include <hip/hip_runtime.h>
+
+#include "device_common.h"
+#include "sketchssm_internal.h"
+
+namespace skssm {
+
+// What the ragged entry points (sketchssm_rmw_seq, sketchssm_prefill) share.
+struct RaggedArgs {
+    const float* S0;         // first states, or null: every sequence starts from zero
+    float* S;                // last states
+    const int32_t* rows0;    // state row of S0 per sequence (negative: zero), or null: as rows
+    const int32_t* rows;     // state row of S per sequence, or null: sequence i is row i
+    const int32_t* offsets;  // [n_seqs + 1] first token of each sequence
+    const void* q;
+    const void* k;
+    const void* v;
+    const float* a;
+    const float* beta;
+    float* y;
+    int B0, B, n_seqs, total, max_len;
+    int H, Hk, share;  // key/query heads; each serves `share` consecutive heads
+};
+
+struct SeqSpan {
+    int row, row0;  // row0 < 0: start from zero
+    int t0, len;
+    bool live;
+};
+
+// Sequence i of the call.  The lists live on the device, so what they hold is
+// checked here: a sequence with a row, a first token or a length out of range
+// is idle, nothing of it is read or written.
+__device__ __forceinline__ SeqSpan seq_span(const RaggedArgs& A, int i) {
+    SeqSpan s;
+    const int t1 = A.offsets[i + 1];
+    s.t0 = A.offsets[i];
+    s.row = A.rows ? A.rows[i] : i;
+    s.row0 = !A.S0 ? -1 : A.rows0 ? A.rows0[i] : s.row;
+    s.live = s.t0 >= 0 && t1 >= s.t0 && t1 <= A.total && s.row >= 0 && s.row < A.B && s.row0 < A.B0;
+    s.len = s.live ? t1 - s.t0 : 0;
+    if (s.len > A.max_len) s.live = false;
+    return s;
+}
+
+// Checks the arguments of a ragged entry point (host) and fills `out`.
+sketchssm_status ragged_args(const sketchssm_shape* shape, const float* S0, int32_t n_rows0, const int32_t* rows0,
+                             float* S, const int32_t* rows, const int32_t* offsets, int32_t n_seqs,
+                             int32_t total_tokens, int32_t max_len, const void* q, const void* k, const void* v,
+                             const float* a, const float* beta, float* y, RaggedArgs* out);
+
+// The recurrent form's launch (recur.hip).
+hipError_t launch_recur(const sketchssm_shape& sh, const RaggedArgs& a, hipStream_t s);
+
+}  // namespace skssm

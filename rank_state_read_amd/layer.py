@@ -72,6 +72,11 @@ class SketchLayer:
         self.abuf = torch.zeros((W, H, B, K) if kind == "kda" else (W, H, B), dtype=torch.float32, device=dev)
         self.bbuf = torch.zeros((W, H, B), dtype=torch.float32, device=dev) if kind != "mamba2" else None
         self.y = torch.empty((B, H, V), dtype=torch.float32, device=dev)
+        self.norm = None  # the gated norm behind y, see set_norm
+
+    def _new(self, shape, dtype, stream):
+        with _b.owned_by(stream, self.device):
+            return torch.empty(shape, dtype=dtype, device=self.device)
 
     # -- inputs ------------------------------------------------------------
     def upload_step(self, st: dict) -> dict:
@@ -132,6 +137,43 @@ class SketchLayer:
         y = self.y if y is None else y
         _b.sketchssm_rmw_step(self.shape, self.S, q, k, v, a, beta, y, stream)
         return y
+
+    def rmw_seq(self, offsets, max_len: int, q, k, v, a, beta=None, rows=None, S0=None, rows0=None, y=None,
+                stream=None) -> torch.Tensor:
+        """A few tokens of each listed row, token by token on this layer's state (no window, no sketch).
+        The rows go on from their own states, or from rows0 of S0 (negative: zero)."""
+        y = self._new(v.shape, torch.float32, stream) if y is None else y
+        _b.sketchssm_rmw_seq(self.shape, self.S if S0 is None else S0, rows0, self.S, rows, offsets, max_len, q, k, v,
+                            a, beta, y, stream)
+        return y
+
+    def prefill(self, offsets, max_len: int, q, k, v, a, beta=None, rows=None, S0=None, rows0=None, fresh: bool = True,
+                y=None, workspace=None, stream=None) -> torch.Tensor:
+        """Prompts of the listed rows (device int32; None: sequence i is row i), packed in one token axis:
+        writes each row's state after its prompt and returns y of every token.  The rows start from zero
+        (``fresh``), go on from their own states, or start from rows0 of S0 (negative: zero)."""
+        y = self._new(v.shape, torch.float32, stream) if y is None else y
+        if S0 is None and not fresh:
+            S0 = self.S
+        _b.sketchssm_prefill(self.shape, S0, rows0, self.S, rows, offsets, max_len, q, k, v, a, beta, y, workspace,
+                            stream)
+        return y
+
+    def set_norm(self, weight, norm_heads: int, gate: str, eps: float = 1e-5, D=None):
+        """The gated norm behind this layer's output: weight [H, V] or [V], D [H] the skip of v (Mamba-2) or None."""
+        f32 = torch.float32
+        self.norm = (_to_device(weight, f32, self.device), int(norm_heads), gate, float(eps),
+                     None if D is None else _to_device(D, f32, self.device))
+
+    def gated_norm(self, y, z, v=None, out=None, stream=None) -> torch.Tensor:
+        """The output that goes to the layer's projection: y [n, H, V] through ``set_norm``'s gated norm,
+        with the tokens' gate z and, where the layer has a skip, their values v."""
+        if self.norm is None:
+            raise ValueError("the layer has no norm: call set_norm first")
+        weight, heads, gate, eps, D = self.norm
+        out = self._new(y.shape, self.qdtype, stream) if out is None else out
+        _b.sketchssm_gated_norm(self.shape, y, None if D is None else v, D, z, weight, heads, gate, eps, out, stream)
+        return out
 
     # -- views ---------------------------------------------------------------
     def z_item(self, b: int, h: int) -> Optional[torch.Tensor]:

@@ -9,7 +9,9 @@ turn.  ``SketchModel`` holds those layers (``SketchLayer`` objects, one per
 recurrent layer, all with the same window length) and runs that loop over the
 C entry points: at window position 0 .. W-2 each layer's read, at W-1 each
 layer's last read fused into its flush.  All layers share one window phase,
-since every layer sees every token.
+since every layer sees every token.  ``prefill`` runs the sequences' prompts
+through the layers first.  Where a layer has a gated norm (``set_norm``) and its
+token inputs hold a gate ``z``, its output is the normed one.
 
 Only the recurrent part of a layer is here: the projections that produce a
 layer's q, k, v, decay and beta from the previous layer's output are not part of
@@ -46,19 +48,41 @@ class SketchModel:
             L.flush(0, stream=stream)
         self.pos = 0
 
+    def prefill(self, tokens: Sequence[Dict[str, Optional[torch.Tensor]]], offsets: torch.Tensor, max_len: int,
+                stream=None) -> List[torch.Tensor]:
+        """The prompts of all sequences through every layer, from empty states:
+        tokens offsets[b] .. offsets[b+1]-1 of layer i's packed inputs
+        ``tokens[i]`` are sequence b's.  Writes every state and first sketch,
+        restarts the window and returns the layers' outputs for all tokens."""
+        if len(tokens) != len(self.layers):
+            raise ValueError("one token input per layer")
+        if offsets.numel() != self.layers[0].B + 1:
+            raise ValueError("one prompt per sequence")
+        out = []
+        for L, d in zip(self.layers, tokens):
+            y = L.prefill(offsets, max_len, d["q"], d["k"], d["v"], d["a"], d.get("beta"), stream=stream)
+            out.append(self._normed(L, y, d, stream))
+        self.start(stream)
+        return out
+
+    @staticmethod
+    def _normed(L, y, d, stream):
+        return y if d.get("z") is None else L.gated_norm(y, d["z"], d["v"], stream=stream)
+
     def decode_step(self, tokens: Sequence[Dict[str, Optional[torch.Tensor]]], stream=None) -> List[torch.Tensor]:
         """One token through every layer.  ``tokens[i]`` holds layer i's device
         inputs (``q``, ``k``, ``v``, ``a`` and, for the delta rule, ``beta``);
         returns the layers' output buffers (each layer's ``y``, overwritten by
-        the next step)."""
+        the next step; with a gate ``z``, a new tensor of the normed output)."""
         if len(tokens) != len(self.layers):
             raise ValueError("one token input per layer")
         last = self.pos == self.W - 1
         out = []
         for L, d in zip(self.layers, tokens):
             if last:
-                out.append(L.read_flush(d["q"], d["k"], d["v"], d["a"], d.get("beta"), stream=stream))
+                y = L.read_flush(d["q"], d["k"], d["v"], d["a"], d.get("beta"), stream=stream)
             else:
-                out.append(L.read(self.pos, d["q"], d["k"], d["v"], d["a"], d.get("beta"), stream=stream))
+                y = L.read(self.pos, d["q"], d["k"], d["v"], d["a"], d.get("beta"), stream=stream)
+            out.append(self._normed(L, y, d, stream))
         self.pos = (self.pos + 1) % self.W
         return out
