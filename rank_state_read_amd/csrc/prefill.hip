@@ -1,130 +1,53 @@
-// Prefill of ragged prompts for gfx950: the state update in chunks of C = 64
-// tokens on the matrix cores.
+// Prefill of ragged prompts for gfx950 (see prefill_common.h for the chunked form).
 //
-// Per sequence and head, within a chunk that starts at state S, with gamma_i the
-// decays' product up to token i, gamma_ij that after j up to i and sigma_j that
-// after j to the chunk's end:
-//   A_ij = beta_i gamma_ij (k_i . k_j)  (j < i),   P_ij = gamma_ij (q_i . k_j)  (j <= i)
-//   T    = (I + A)^-1 diag(beta)                    (Mamba-2: w = v instead)
-//   w    = T (v - gamma K S),   y = gamma Q S + P w,   S <- gamma_C S + K^T (sigma w)
-//
-// Two launches.  T and P depend on a chunk's own tokens alone, so the first
-// forms them for all chunks of all heads at once and leaves them in the
+// Two launches for the delta rule: T depends on a chunk's own tokens alone, so
+// the first forms it for all chunks of all heads at once and leaves it in the
 // workspace; the second walks a sequence's chunks in order with the state in
-// registers.  Value columns are independent of each other: a block owns 16 of
-// them, so that a single sequence fills the chip.  Its four waves share a
-// chunk's work by rows -- 16 tokens each for K S, Q S, T and P, 32 key channels
-// each for the state -- and hand each other their results through LDS as B
-// operands.
-//
-// Products run on the bf16 matrix instruction (16x16x32, fp32 sums) and keep
-// fp32 precision: an fp32 operand x is written as hi + mid + lo, three bf16
-// numbers of 8 significant bits each.  q, k, v in bf16 are exact operands, so
-// their products with an fp32 operand take three instructions, products of two
-// fp32 operands six (the terms below 2^-24 are left out).  The fp32 matrix
-// instruction has 1/16 of the bf16 rate.
+// registers.  Mamba-2 needs the walk only.
 #include <hip/hip_runtime.h>
 
+#include <cstdlib>
 #include <type_traits>
 
-#include "device_common.h"
-#include "ragged.h"
-#include "sketchssm_internal.h"
+#include "prefill_common.h"
 
 namespace skssm {
 
+// ---------------------------------------------------------------------------
+// T of every chunk and head: one wave per (slot, head).
+// ---------------------------------------------------------------------------
 namespace {
 
-typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
-typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
-typedef float f32x2 __attribute__((ext_vector_type(2)));
-typedef short s16x4 __attribute__((ext_vector_type(4)));
-typedef unsigned u32x2 __attribute__((ext_vector_type(2)));
-
-constexpr int kC = 64;              // tokens per chunk
-constexpr int kFrag = 64 * 16;      // one operand of a wave, bytes
-constexpr int kTri = 6 * 3 * kFrag; // T or P: six (row tile, 32-column) operands of three terms
-
-__device__ __forceinline__ f32x4 mfma_bf16(u32x4 a, u32x4 b, f32x4 c) {
-    return __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, a), __builtin_bit_cast(bf16x8, b), c, 0,
-                                                   0, 0);
-}
-
-// x = t[0] + t[1] + t[2] for 2 N consecutive values, each term rounded to bf16.
-template <int N>
-__device__ __forceinline__ void split3(const float* f, uint32_t (&u)[3][N]) {
-#pragma unroll
-    for (int i = 0; i < N; ++i) {
-        float x0 = f[2 * i], x1 = f[2 * i + 1];
-#pragma unroll
-        for (int p = 0; p < 3; ++p) {
-            const uint32_t h = __builtin_bit_cast(uint32_t, __builtin_convertvector((f32x2{x0, x1}), bf16x2));
-            u[p][i] = h;
-            x0 -= __uint_as_float(h << 16);
-            x1 -= __uint_as_float(h & 0xffff0000u);
-        }
-    }
-}
-
-// Operand (row tile m, 32-column step s <= m / 2) of a C x C triangle.
-__device__ __forceinline__ int tri_frag(int m, int s) { return (m < 2 ? m : 2 * m - 2) + s; }
-
-// A workspace record: P, then T (delta rule), then gamma and sigma.
-template <int KIND>
-struct Record {
-    static constexpr bool delta = KIND != SKSSM_MAMBA2;
-    static constexpr int p = 0;
-    static constexpr int t = kTri;
-    static constexpr int g = delta ? 2 * kTri : kTri;
-    static constexpr int bytes = g + 2 * kC * 4;
-};
-
-inline long prefill_slots(long total, int n_seqs) { return total / kC + n_seqs; }
-
-// Chunk c of a sequence has slot off / C + seq + c of the workspace: a sequence
-// of len tokens has at most (off + len) / C - off / C + 1 chunks, so sequences
-// that do not overlap never share a slot.
-__device__ __forceinline__ long first_slot(int t0, int seq) { return long(t0) / kC + seq; }
-
-}  // namespace
-
-// ---------------------------------------------------------------------------
-// T and P of every chunk and head: a block of four waves per (slot, head).
-// ---------------------------------------------------------------------------
+constexpr int kPrepWaves = 4;
 constexpr int kGS = kC + 4;  // row stride of a C x C matrix in LDS, floats
 
-// Product of two 16 x 16 blocks in LDS, added to c.
-__device__ __forceinline__ f32x4 block_mul(const float* a, const float* b, f32x4 c, int lr, int lq) {
+// Product of two 16 x 16 blocks in LDS.
+__device__ __forceinline__ f32x4 block_mul(const float* a, const float* b, int lr, int lq) {
+    f32x4 c = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
     for (int s = 0; s < 4; ++s) c = mfma_16x16x4(a[lr * kGS + 4 * s + lq], b[(4 * s + lq) * kGS + lr], c);
     return c;
 }
 // The same with the second block in the accumulator layout.
-__device__ __forceinline__ f32x4 block_mul(const float* a, f32x4 b, f32x4 c, int lr, int lq) {
+__device__ __forceinline__ f32x4 block_mul(const float* a, f32x4 b, int lr, int lq) {
+    f32x4 c = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
     for (int s = 0; s < 4; ++s) c = mfma_16x16x4(a[lr * kGS + 4 * lq + s], b[s], c);
     return c;
 }
-__device__ __forceinline__ void block_put(float* d, f32x4 c, int lr, int lq) {
-#pragma unroll
-    for (int r = 0; r < 4; ++r) d[(4 * lq + r) * kGS + lr] = c[r];
+
+__device__ __forceinline__ void wave_sync() {
+    __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+    __builtin_amdgcn_wave_barrier();
 }
 
-template <int KIND>
-__global__ __launch_bounds__(256) void prep_kernel(RaggedArgs A, char* ws) {
-    constexpr bool DELTA = KIND != SKSSM_MAMBA2;
-    typedef Record<KIND> R;
-    __shared__ __align__(16) float gq[kC * kGS];
-    __shared__ __align__(16) float gk[DELTA ? kC * kGS : 4];
-    __shared__ __align__(16) float bs[kC];
-    const int w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-    const int lane = threadIdx.x & 63, lr = lane & 15, lq = lane >> 4;
-    const long slot = blockIdx.x / A.H;
-    const int h = int(blockIdx.x - slot * A.H), hk = h / A.share;
+__device__ __forceinline__ float lane_value(float x, int i) {
+    return __uint_as_float(__builtin_amdgcn_readlane(__float_as_uint(x), i));
+}
 
-    // the sequence and chunk of this slot, if any (every wave looks on its own)
-    int seq = -1, t0 = 0, clen = 0;
-    for (int s0 = 0; s0 < A.n_seqs && seq < 0; s0 += 64) {
+// The sequence and chunk of a workspace slot: first token and tokens, none: 0.
+__device__ __forceinline__ int slot_chunk(const RaggedArgs& A, long slot, int lane, int& t0) {
+    for (int s0 = 0; s0 < A.n_seqs; s0 += 64) {
         const int s = s0 + lane;
         bool hit = false;
         int tc = 0, cl = 0;
@@ -138,482 +61,616 @@ __global__ __launch_bounds__(256) void prep_kernel(RaggedArgs A, char* ws) {
         const unsigned long long m = __ballot(hit);
         if (m) {
             const int f = __ffsll(m) - 1;
-            seq = s0 + f;
             t0 = __shfl(tc, f, 64);
-            clen = __shfl(cl, f, 64);
+            return __shfl(cl, f, 64);
         }
     }
-    if (seq < 0) return;  // the whole block
+    return 0;
+}
 
-    // k_i . k_j and q_i . k_j, row tile w: exact products of bf16 values, fp32 sums
+}  // namespace
+
+__global__ __launch_bounds__(kPrepWaves * 64) void prep_gdn_kernel(RaggedArgs A, char* ws) {
+    typedef Record<SKSSM_GDN> R;
+    __shared__ __align__(16) float tiles[kPrepWaves][2][kC * kGS];
+    const int w = threadIdx.x >> 6, lane = threadIdx.x & 63, lr = lane & 15, lq = lane >> 4;
+    const long task = long(blockIdx.x) * kPrepWaves + w;
+    const long slot = task / A.H;
+    const int h = int(task - slot * A.H), hk = h / A.share;
+    int t0 = 0;
+    const int clen = slot_chunk(A, slot, lane, t0);
+    if (clen == 0) return;  // no wave waits for another one below
+
+    // k_i . k_j and q_i . k_j: exact products of bf16 values, fp32 sums
+    float* g = tiles[w][0];
+    float* gq = tiles[w][1];
+    const int j = lane & 31;
+    const bool valid = j < clen;
+    const size_t tj = size_t(t0) + (valid ? j : 0);
+    const float aj = valid ? A.a[tj * A.H + h] : 1.f;
+    const float bj = valid ? A.beta[tj * A.H + h] : 0.f;
     {
-        auto row = [&](const void* base, int tile, u32x4 (&f)[4]) {
-            const size_t r = (size_t(t0) + min(16 * tile + lr, clen - 1)) * A.Hk + hk;
+        u32x4 kf[2][4];
+        auto row = [&](const void* base, int m, u32x4 (&f)[4]) {
+            const size_t r = (size_t(t0) + min(16 * m + lr, clen - 1)) * A.Hk + hk;
             const char* src = static_cast<const char*>(base) + (r * kK + 8 * lq) * 2;
 #pragma unroll
             for (int s = 0; s < 4; ++s) f[s] = *reinterpret_cast<const u32x4*>(src + 64 * s);
         };
-        u32x4 kf[4], qf[4];
-        if (DELTA) row(A.k, w, kf);
-        row(A.q, w, qf);
-        for (int n = 0; n <= w; ++n) {
-            u32x4 nf[4];
-            row(A.k, n, nf);
-            f32x4 dk = {0.f, 0.f, 0.f, 0.f}, dq = dk;
+        row(A.k, 0, kf[0]);
+        row(A.k, 1, kf[1]);
 #pragma unroll
-            for (int s = 0; s < 4; ++s) {
-                if (DELTA) dk = mfma_bf16(kf[s], nf[s], dk);
-                dq = mfma_bf16(qf[s], nf[s], dq);
-            }
-            if (DELTA) block_put(gk + 16 * w * kGS + 16 * n, dk, lr, lq);
-            block_put(gq + 16 * w * kGS + 16 * n, dq, lr, lq);
-        }
-    }
-    const bool valid = lane < clen;
-    const size_t tj = size_t(t0) + (valid ? lane : 0);
-    const float aj = valid ? A.a[tj * A.H + h] : 1.f;
-    const float bj = !DELTA ? 1.f : valid ? A.beta[tj * A.H + h] : 0.f;
-    if (w == 0) bs[lane] = bj;
-    __syncthreads();
-
-    // column j = lane: the decays' products after token j, one factor at a time (a
-    // decay may be 0, so nothing is divided).  Delta rule: two waves write -A, two
-    // P, 32 rows each; Mamba-2: 16 rows of P each.
-    char* rec = ws + size_t(blockIdx.x) * R::bytes;
-    {
-        const bool isA = DELTA && (w & 1) == 0;
-        const int rows = DELTA ? 32 : 16, r0 = DELTA ? 32 * (w >> 1) : 16 * w;
-        float* gt = isA ? gk : gq;
-        float d = 0.f, gam = 0.f, run = 1.f;
-        for (int i = 0; i < r0; ++i) {
-            const float ai = __uint_as_float(__builtin_amdgcn_readlane(__float_as_uint(aj), i));
-            d = i == lane ? 1.f : d * ai;
-            run *= ai;
-            gam = i == lane ? run : gam;
-        }
-#pragma unroll 8
-        for (int i = r0; i < r0 + rows; ++i) {
-            const float ai = __uint_as_float(__builtin_amdgcn_readlane(__float_as_uint(aj), i));
-            const float bi = __uint_as_float(__builtin_amdgcn_readlane(__float_as_uint(bj), i));
-            d = i == lane ? 1.f : d * ai;
-            run *= ai;
-            gam = i == lane ? run : gam;
-            const float g = gt[i * kGS + lane] * d;
-            const bool in = isA ? i > lane : i >= lane && valid;
-            gt[i * kGS + lane] = in ? (isA ? -bi * g : g) : 0.f;
-        }
-        if (w == 3) {  // the waves that have walked to the end
-            float* g = reinterpret_cast<float*>(rec + R::g);
-            g[lane] = gam;
-            g[kC + lane] = valid ? d : 0.f;
-        }
-    }
-    __syncthreads();
-
-    if (DELTA) {
-        // (I + A)^-1 by blocks of 16: the diagonal blocks by forward substitution,
-        // one lane per column, then M_ba = M_bb (-A_ba) M_aa for 16 and 32 rows
-        if (lane < 16) {
-            float* g = gk + 16 * w * kGS + 16 * w;
-            float x[16];
+        for (int m = 0; m < 2; ++m) {
+            u32x4 qf[4];
+            row(A.q, m, qf);
 #pragma unroll
-            for (int i = 0; i < 16; ++i) {
-                float s0 = i == lane ? 1.f : 0.f, s1 = 0.f;
+            for (int n = 0; n <= m; ++n) {
+                f32x4 d = {0.f, 0.f, 0.f, 0.f}, dq = d;
 #pragma unroll
-                for (int m = 0; m < i; m += 4) {
-                    const f32x4 n4 = *reinterpret_cast<const f32x4*>(g + i * kGS + m);
-#pragma unroll
-                    for (int e = 0; e < 4; ++e)
-                        if (m + e < i) {
-                            if (e & 1) s1 = fmaf(n4[e], x[m + e], s1);
-                            else s0 = fmaf(n4[e], x[m + e], s0);
-                        }
+                for (int s = 0; s < 4; ++s) {
+                    d = mfma_bf16(kf[m][s], kf[n][s], d);
+                    dq = mfma_bf16(qf[s], kf[n][s], dq);
                 }
-                x[i] = s0 + s1;
+#pragma unroll
+                for (int r = 0; r < 4; ++r) {
+                    const int at = (16 * m + 4 * lq + r) * kGS + 16 * n + lr;
+                    g[at] = d[r];
+                    gq[at] = dq[r];
+                }
             }
-            __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
-            __builtin_amdgcn_wave_barrier();
-#pragma unroll
-            for (int i = 0; i < 16; ++i) g[i * kGS + lane] = x[i];
         }
-        __syncthreads();
-        const f32x4 zero = {0.f, 0.f, 0.f, 0.f};
-        auto blk = [&](int i, int j) { return gk + 16 * i * kGS + 16 * j; };
-        if (w < 2) {  // blocks (1, 0) and (3, 2)
-            const f32x4 r = block_mul(blk(2 * w + 1, 2 * w), blk(2 * w, 2 * w), zero, lr, lq);
-            const f32x4 m = block_mul(blk(2 * w + 1, 2 * w + 1), r, zero, lr, lq);
-            __builtin_amdgcn_wave_barrier();
-            block_put(blk(2 * w + 1, 2 * w), m, lr, lq);
-        }
-        __syncthreads();
-        const int ca = w & 1, rb = 2 + (w >> 1);  // block (rb, ca)
-        f32x4 m = zero;
-        for (int b = 2; b <= rb; ++b) {
-            f32x4 r = zero;
-            for (int x = ca; x < 2; ++x) r = block_mul(blk(b, x), blk(x, ca), r, lr, lq);
-            m = block_mul(blk(rb, b), r, m, lr, lq);
-        }
-        __syncthreads();
-        block_put(blk(rb, ca), m, lr, lq);
-        __syncthreads();
     }
+    wave_sync();
 
-    // row tile w of both as A operands
-    for (int s = 0; s <= w / 2; ++s) {
-        const int at = (16 * w + lr) * kGS + 32 * s + 8 * lq;
-        char* out = rec + tri_frag(w, s) * 3 * kFrag + lane * 16;
+    // column j: the decays' products after token j one factor at a time (a decay may
+    // be 0, so nothing is divided); lanes 0 .. 31 take -A, lanes 32 .. 63 take P
+    char* rec = ws + task * R::bytes;
+    {
+        float* gt = lane < 32 ? g : gq;
+        float d = 0.f, run = 1.f, gam = 0.f;
+#pragma unroll
+        for (int i = 0; i < kC; ++i) {
+            const float ai = lane_value(aj, i), bi = lane_value(bj, i);
+            d = i == j ? 1.f : d * ai;
+            run *= ai;
+            gam = i == j ? run : gam;
+            const float x = d * gt[i * kGS + j];
+            gt[i * kGS + j] = lane < 32 ? (i > j ? -bi * x : 0.f) : (i >= j && valid ? x : 0.f);
+        }
+        reinterpret_cast<float*>(rec + R::g)[lane] = lane < 32 ? gam : (valid ? d : 0.f);
+    }
+    wave_sync();
+    // (I + A)^-1: the diagonal blocks of 16 by forward substitution, one lane per
+    // column, then M_10 = M_11 (-A_10) M_00
+    if (lane < 32) {
+        float* b = g + (lane & 16) * (kGS + 1);
+        const int l = lane & 15;
+        float x[16];
+#pragma unroll
+        for (int i = 0; i < 16; ++i) {
+            float s0 = i == l ? 1.f : 0.f, s1 = 0.f;
+#pragma unroll
+            for (int m = 0; m < i; m += 4) {
+                const f32x4 n4 = *reinterpret_cast<const f32x4*>(b + i * kGS + m);
+#pragma unroll
+                for (int e = 0; e < 4; ++e)
+                    if (m + e < i) {
+                        if (e & 1) s1 = fmaf(n4[e], x[m + e], s1);
+                        else s0 = fmaf(n4[e], x[m + e], s0);
+                    }
+            }
+            x[i] = s0 + s1;
+        }
+        wave_sync();
+#pragma unroll
+        for (int i = 0; i < 16; ++i) b[i * kGS + l] = x[i];
+    }
+    wave_sync();
+    const f32x4 r10 = block_mul(g + 16 * kGS, g, lr, lq);
+    const f32x4 m10 = block_mul(g + 16 * kGS + 16, r10, lr, lq);
+    wave_sync();
+#pragma unroll
+    for (int r = 0; r < 4; ++r) g[(16 + 4 * lq + r) * kGS + lr] = m10[r];
+    wave_sync();
+
+    // P and T = (I + A)^-1 diag(beta) as A operands
+    float b[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) b[i] = __shfl(bj, 8 * lq + i, 64);
+#pragma unroll
+    for (int m = 0; m < 2; ++m) {
         float f[8];
-        uint32_t u[3][4];
+        const int at = tile_row(m, lr) * kGS + 8 * lq;
+        load8f(g + at, f);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) f[i] *= b[i];
+        const Split t = split8(f);
         load8f(gq + at, f);
-        split3<4>(f, u);
+        const Split p = split8(f);
 #pragma unroll
-        for (int e = 0; e < 3; ++e)
-            *reinterpret_cast<u32x4*>(out + R::p + e * kFrag) = u32x4{u[e][0], u[e][1], u[e][2], u[e][3]};
-        if (DELTA) {
-            float b[8];
-            load8f(gk + at, f);
-            load8f(bs + 32 * s + 8 * lq, b);
-#pragma unroll
-            for (int i = 0; i < 8; ++i) f[i] *= b[i];
-            split3<4>(f, u);
-#pragma unroll
-            for (int e = 0; e < 3; ++e)
-                *reinterpret_cast<u32x4*>(out + R::t + e * kFrag) = u32x4{u[e][0], u[e][1], u[e][2], u[e][3]};
+        for (int e = 0; e < 3; ++e) {
+            *reinterpret_cast<u32x4*>(rec + R::t + (2 * e + m) * kFrag + lane * 16) = t.t[e];
+            *reinterpret_cast<u32x4*>(rec + R::p + (2 * e + m) * kFrag + lane * 16) = p.t[e];
         }
     }
 }
 
 // ---------------------------------------------------------------------------
-// The walk over a sequence's chunks.
+// The walk over a sequence's chunks, bf16 keys and queries, one decay per token:
+// NW waves of 16 value columns, V / (16 NW) blocks per sequence and head.
+//
+// One barrier per chunk.  While chunk c is computed, the next chunk's keys,
+// queries, values and record come from memory to registers, and then to the
+// other LDS buffer.  Mamba-2 has no record: P of chunk c + 1 is formed from its
+// keys and queries, so those are fetched two chunks ahead.
 // ---------------------------------------------------------------------------
-struct ScanLds {  // bytes
-    static constexpr int k = 0;                         // keys of two chunks [2][C][K], swizzled
-    static constexpr int s = k + 2 * kC * kK * 2;       // the state's B operands: [buffer][4 steps][3 terms]
-    static constexpr int sbuf = 12 * kFrag;
-    // delta rule: v - gamma K S, w and sigma w, each [2 steps][3 terms]
-    static constexpr int r = s + sbuf;
-    static constexpr int w = r + 6 * kFrag;
-    static constexpr int u = w + 6 * kFrag;
-    static constexpr int bytes_delta = u + 6 * kFrag;
-    // Mamba-2: two buffers of the state, of v [2 steps] and of sigma v
-    static constexpr int v2 = s + 2 * sbuf;
-    static constexpr int u2 = v2 + 2 * 2 * kFrag;
-    static constexpr int bytes_mamba = u2 + 2 * 6 * kFrag;
+template <int KIND, int NW>
+struct WalkLds {  // bytes
+    static constexpr bool delta = KIND != SKSSM_MAMBA2;
+    static constexpr int v = NW * kFrag;                       // a chunk's values [C][16 NW] in bf16
+    static constexpr int kqbuf = 2 * kPlane;                   // keys, queries
+    static constexpr int kq = 0;
+    static constexpr int nkq = delta ? 2 : 3;
+    static constexpr int vals = kq + nkq * kqbuf;              // two chunks
+    static constexpr int rec = vals + 2 * v;                   // delta rule: records of two chunks
+    static constexpr int p = rec;                              // Mamba-2: P of two chunks,
+    static constexpr int f = p + 2 * kTri;                     // decays' products of two chunks [8][C], then a [C],
+    static constexpr int fbuf = 9 * kC * 4;
+    static constexpr int g = f + 2 * fbuf;                     // gamma, sigma of three chunks
+    static constexpr int gbuf = 2 * kC * 4;
+    static constexpr int bytes = delta ? rec + 2 * Record<SKSSM_GDN>::bytes : g + 3 * gbuf;
 };
 
-// Granule of 16 bytes g of token row r sits at granule g ^ row_swizzle(r): the 16
-// rows of a tile start in different banks, and so do the four rows and four
-// granules of a transposed read.
-__device__ __forceinline__ int row_swizzle(int r) { return ((r & 3) << 2) | ((r >> 2) & 3); }
+// A buffer resource whose first address moves on by a step per chunk; it covers
+// `rows` rows of `row` bytes at a stride, so that tokens behind the sequence read
+// as 0 and are not written.
+struct Cursor {
+    uint64_t at;
+    uint32_t stride, row;
+    __device__ __forceinline__ __amdgpu_buffer_rsrc_t rsrc(int rows) const {
+        return buffer_rsrc(reinterpret_cast<const void*>(at), rows > 0 ? uint32_t(min(rows, kC) - 1) * stride + row : 0u);
+    }
+    __device__ __forceinline__ void next() { at += uint64_t(kC) * stride; }
+};
 
-template <int KIND>
-__global__ __launch_bounds__(256) void scan_kernel(RaggedArgs A, const char* ws, int V) {
+template <int KIND, int NW>
+__global__ __launch_bounds__(NW * 64) __attribute__((amdgpu_waves_per_eu(2)))
+void walk_kernel(RaggedArgs A, const char* ws, int V) {
     constexpr bool DELTA = KIND != SKSSM_MAMBA2;
-    typedef Record<KIND> R;
-    typedef ScanLds L;
+    typedef WalkLds<KIND, NW> L;
+    typedef Record<SKSSM_GDN> R;
     extern __shared__ __align__(16) char lds[];
     const int w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);  // the same in every lane
     const int lane = threadIdx.x & 63, lr = lane & 15, lq = lane >> 4;
-    // heads that share a key head sit on one XCD (blocks go round the eight by index)
-    const int per = (A.H + 7) / 8, slices = V / 16;
+    const int per = (A.H + 7) / 8;
+    const int slices = V / (16 * NW);
     const int xcd = blockIdx.x & 7;
     int rest = blockIdx.x >> 3;
     const int slice = rest % slices;
     rest /= slices;
-    const int un = rest % per, seq = rest / per;
-    const int h = A.Hk % 8 == 0 ? (xcd + 8 * (un / A.share)) * A.share + un % A.share : xcd + 8 * un;
+    const int seq = rest / per, h = head_of(A, xcd, rest % per);
     if (h >= A.H) return;
     const int hk = h / A.share;
     const SeqSpan sp = seq_span(A, seq);
     if (!sp.live) return;
-    const int col = slice * 16 + lr;
+    const int col = 16 * (slice * NW + w) + lr;
 
-    // the state, channels 32 w .. 32 w + 31: tile o, register r <-> channel
-    // 32 w + 8 lq + 4 o + r, so a lane holds 8 consecutive channels, one B operand
-    f32x4 S[2];
-    const int svo = ((32 * w + 8 * lq) * V + col) * 4;
+    // the state: tile 2 s + o, register r <-> channel 32 s + 8 lq + 4 o + r
+    f32x4 S[8];
+    const int svo = (8 * lq * V + col) * 4;
     if (sp.row0 >= 0) {
         const __amdgpu_buffer_rsrc_t s0 = buffer_rsrc(A.S0 + (size_t(sp.row0) * A.H + h) * (kK * V), kK * V * 4);
 #pragma unroll
-        for (int i = 0; i < 8; ++i) S[i / 4][i & 3] = buffer_load_f32(s0, svo, i * V * 4);
+        for (int t = 0; t < 8; ++t)
+#pragma unroll
+            for (int r = 0; r < 4; ++r)
+                S[t][r] = buffer_load_f32(s0, svo, (32 * (t >> 1) + 4 * (t & 1) + r) * V * 4);
     } else {
-        S[0] = S[1] = f32x4{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+        for (int t = 0; t < 8; ++t) S[t] = f32x4{0.f, 0.f, 0.f, 0.f};
     }
-    const int n_chunks = (sp.len + kC - 1) / kC;
 
-    const char* rec0 = ws + (first_slot(sp.t0, seq) * A.H + h) * R::bytes;
-    const size_t rec_step = size_t(A.H) * R::bytes;
-    const char* ksrc = static_cast<const char*>(A.k) + (size_t(sp.t0) * A.Hk + hk) * (kK * 2);
-    const char* qsrc = static_cast<const char*>(A.q) + (size_t(sp.t0) * A.Hk + hk) * (kK * 2);
-    const uint32_t qk_step = uint32_t(A.Hk) * kK * 2;
+    // ---- where a chunk's data come from ----
+    auto first = [&](const void* base, int heads, int head, int row) {
+        return reinterpret_cast<uint64_t>(base) + (uint64_t(sp.t0) * heads + head) * uint64_t(row);
+    };
+    const uint32_t krow = kK * 2, vrow = uint32_t(V) * 2;
+    Cursor ck{first(A.k, A.Hk, hk, krow), A.Hk * krow, krow};
+    Cursor cq{first(A.q, A.Hk, hk, krow), A.Hk * krow, krow};
+    Cursor cv{first(A.v, A.H, h, vrow), A.H * vrow, vrow};
+    Cursor cy{first(A.y, A.H, h, 2 * vrow), A.H * 2 * vrow, 2 * vrow};
+    uint64_t crec = reinterpret_cast<uint64_t>(ws) + (first_slot(sp.t0, seq) * A.H + h) * R::bytes;
 
-    // Loads of chunk c.  Rows behind the sequence repeat its last token: their
-    // columns of T and P and their sigma are 0.
-    u32x4 kreg[4], qf[4], tf[2][3], pf[2][3];
-    f32x4 gam, sig;
-    float gC;
-    uint32_t v[4];
-    auto load_k = [&](int c) {  // rows 16 j + 4 w + lane / 16 of the key tile
+    // keys and queries: 16 pieces of 1 KB (four rows), piece w + j NW by wave w;
+    // granules swizzled
+    constexpr int NKQ = (16 + NW - 1) / NW;
+    u32x4 kq[NKQ];
+    int kqoff[NKQ];
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
-            const int r = 16 * j + 4 * w + lq;
-            const size_t t = min(c * kC + r, sp.len - 1);
-            kreg[j] = *reinterpret_cast<const u32x4*>(ksrc + t * qk_step + (lr ^ row_swizzle(r)) * 16);
+    for (int j = 0; j < NKQ; ++j) {
+        const int r = 4 * ((w + j * NW) & 7) + lq;
+        kqoff[j] = int(r * ck.stride) + (lr ^ row_swizzle(r)) * 16;
+    }
+    auto load_kq = [&](int rows) {
+        const __amdgpu_buffer_rsrc_t rk = ck.rsrc(rows), rq = cq.rsrc(rows);
+#pragma unroll
+        for (int j = 0; j < NKQ; ++j)
+            kq[j] = __builtin_bit_cast(u32x4, __builtin_amdgcn_raw_buffer_load_b128(w + j * NW < 8 ? rk : rq, kqoff[j], 0, 0));
+        ck.next();
+        cq.next();
+    };
+    auto put_kq = [&](char* dst) {
+#pragma unroll
+        for (int j = 0; j < NKQ; ++j)
+            if ((j + 1) * NW <= 16 || w + j * NW < 16)
+                *reinterpret_cast<u32x4*>(dst + (w + j * NW) * kFrag + lane * 16) = kq[j];
+    };
+    // values: the block's columns, one piece per wave
+    u32x4 vp;
+    const int vat = w * kFrag + lane * 16;
+    const int voff = (vat / (32 * NW)) * int(cv.stride) + vat % (32 * NW) + slice * NW * 32;
+    auto load_v = [&](int rows) {
+        vp = __builtin_bit_cast(u32x4, __builtin_amdgcn_raw_buffer_load_b128(cv.rsrc(rows), voff, 0, 0));
+        cv.next();
+    };
+    auto put_v = [&](char* dst) { *reinterpret_cast<u32x4*>(dst + vat) = vp; };
+    // a record, piece w + j NW by wave w
+    constexpr int NR = R::bytes / kFrag, NRW = DELTA ? (NR + NW - 1) / NW : 1;
+    u32x4 rp[NRW];
+    auto load_rec = [&](int rows) {
+        const __amdgpu_buffer_rsrc_t rs = buffer_rsrc(reinterpret_cast<const void*>(crec), rows > 0 ? R::bytes : 0);
+#pragma unroll
+        for (int j = 0; j < NRW; ++j)
+            rp[j] = __builtin_bit_cast(u32x4, __builtin_amdgcn_raw_buffer_load_b128(rs, (w + j * NW) * kFrag + lane * 16, 0, 0));
+        crec += uint64_t(A.H) * R::bytes;
+    };
+    auto put_rec = [&](char* dst) {
+#pragma unroll
+        for (int j = 0; j < NRW; ++j)
+            if ((j + 1) * NW <= NR || w + j * NW < NR)
+                *reinterpret_cast<u32x4*>(dst + (w + j * NW) * kFrag + lane * 16) = rp[j];
+    };
+
+    // ---- Mamba-2: decays' products and P ----
+    float av = 1.f;
+    bool in = false;
+    auto load_a = [&](int c) {  // the decay of token lane % 32
+        const int t = c * kC + (lane & 31);
+        in = t < sp.len;
+        av = in ? A.a[(size_t(sp.t0) + t) * A.H + h] : 1.f;
+    };
+    // By one wave, lane i = token i: with groups of four tokens,
+    // F[b][i] = a_{4b+4} .. a_i (0 for i < 4b + 3), the decays themselves, gamma and
+    // sigma.  The two half-waves write the same.
+    auto put_decays = [&](char* dst, char* gs) {
+        const int i = lane & 31, q = i & 3, b = i >> 2;
+        // within the group: products up to token i, and after it
+        const float p1 = dpp_mov<0x90>(av);  // quad_perm [0,0,1,2]
+        float up = q >= 1 ? av * p1 : av;
+        const float p2 = dpp_mov<0x40>(up);  // quad_perm [0,0,0,1]
+        up = q >= 2 ? up * p2 : up;
+        const float n1 = dpp_mov<0xF9>(av);  // quad_perm [1,2,3,3]
+        const float s1 = q <= 2 ? n1 : 1.f;
+        const float n2 = dpp_mov<0xF9>(s1);
+        float down = q <= 1 ? s1 * n2 : s1;
+        const float n3 = dpp_mov<0xFF>(av);  // quad_perm [3,3,3,3]
+        down = q == 0 ? down * n3 : down;
+        float r = up, sg = down;
+        float* f = reinterpret_cast<float*>(dst) + i;
+        const float own = q == 3 ? 1.f : 0.f;
+#pragma unroll
+        for (int g = 7; g >= 0; --g) {
+            const float bg = lane_value(up, 4 * g + 3);
+            f[g * kC] = g > b ? 0.f : g == b ? own : r;
+            r = g < b ? r * bg : r;
+            sg = g > b ? sg * bg : sg;
         }
+        f[8 * kC] = av;
+        reinterpret_cast<float*>(gs)[i] = r;
+        reinterpret_cast<float*>(gs)[kC + i] = in ? sg : 0.f;
     };
-    auto put_k = [&](int c) {
-        char* dst = lds + L::k + (c & 1) * (kC * kK * 2) + (4 * w + lq) * (kK * 2) + lr * 16;
-#pragma unroll
-        for (int j = 0; j < 4; ++j) *reinterpret_cast<u32x4*>(dst + 16 * j * (kK * 2)) = kreg[j];
-    };
-    auto load_q = [&](int c) {
-        const size_t t = min(c * kC + 16 * w + lr, sp.len - 1);
-#pragma unroll
-        for (int s = 0; s < 4; ++s) qf[s] = *reinterpret_cast<const u32x4*>(qsrc + t * qk_step + 16 * lq + 64 * s);
-    };
-    auto load_tri = [&](int c, int what, u32x4 (&f)[2][3]) {
-        const char* src = rec0 + c * rec_step + what + lane * 16;
-#pragma unroll
-        for (int s = 0; s < 2; ++s)
-#pragma unroll
-            for (int e = 0; e < 3; ++e)  // waves 0 and 1 have one step only: it stands in for the second
-                f[s][e] = *reinterpret_cast<const u32x4*>(src + (tri_frag(w, min(s, w / 2)) * 3 + e) * kFrag);
-    };
-    auto load_gam = [&](int c) {
-        const float* g = reinterpret_cast<const float*>(rec0 + c * rec_step + R::g);
-        gam = *reinterpret_cast<const f32x4*>(g + 16 * w + 4 * lq);
-        sig = *reinterpret_cast<const f32x4*>(g + kC + 16 * w + 4 * lq);
-        gC = g[kC - 1];
-    };
-    const uint32_t vstep = uint32_t(A.H) * V * 2, ystep = 2 * vstep;
-    auto load_v = [&](int c) {  // tokens 16 w + 4 lq + r (0 behind the sequence)
-        const size_t base = ((size_t(sp.t0) + c * kC) * A.H + h) * V;
-        const int left = min(kC, sp.len - c * kC);
-        const __amdgpu_buffer_rsrc_t rs =
-            buffer_rsrc(static_cast<const uint16_t*>(A.v) + base, uint32_t(left - 1) * vstep + V * 2);
-#pragma unroll
-        for (int r = 0; r < 4; ++r)
-            v[r] = uint16_t(__builtin_amdgcn_raw_buffer_load_b16(rs, int((16 * w + 4 * lq + r) * vstep) + col * 2, 0, 0));
-    };
-    auto store_y = [&](int c, f32x4 y) {
-        const size_t base = ((size_t(sp.t0) + c * kC) * A.H + h) * V;
-        const int left = min(kC, sp.len - c * kC);
-        const __amdgpu_buffer_rsrc_t rs = buffer_rsrc(A.y + base, uint32_t(left - 1) * ystep + V * 4);
-#pragma unroll
-        for (int r = 0; r < 4; ++r) buffer_store_f32(y[r], rs, int((16 * w + 4 * lq + r) * ystep) + col * 4, 0);
-    };
-
-    // Four values of tokens 16 w + 4 lq .. + 3 into B operands [2 steps][stride
-    // terms]: half a lane's 16 bytes
-    const int half = ((2 * (w & 1) + (lq >> 1)) * 16 + lr) * 16 + 8 * (lq & 1);
-    auto put_tokens = [&](char* dst, f32x4 x) {
-        const float f[4] = {x[0], x[1], x[2], x[3]};
-        uint32_t u[3][2];
-        split3<2>(f, u);
-#pragma unroll
-        for (int e = 0; e < 3; ++e)
-            *reinterpret_cast<u32x2*>(dst + ((w >> 1) * 3 + e) * kFrag + half) = u32x2{u[e][0], u[e][1]};
-    };
-    auto put_state = [&](char* dst) {
-        float f[8];
-        uint32_t u[3][4];
-#pragma unroll
-        for (int i = 0; i < 8; ++i) f[i] = S[i / 4][i & 3];
-        split3<4>(f, u);
-#pragma unroll
-        for (int e = 0; e < 3; ++e)
-            *reinterpret_cast<u32x4*>(dst + (w * 3 + e) * kFrag + lane * 16) = u32x4{u[e][0], u[e][1], u[e][2], u[e][3]};
-    };
-    // one 16 x 64 by 64 x 16 product of two three-term operands, small terms first
-    auto tri_mul = [&](const u32x4 (&a)[2][3], const char* b, f32x4 c) {
-        constexpr int ia[6] = {2, 0, 1, 1, 0, 0}, ib[6] = {0, 2, 1, 0, 1, 0};
+    // P of a chunk: four tasks (row tile m, half o of the columns), each 16 x 16
+    // values of Q K^T, formed transposed so that a lane holds four columns of a row
+    auto put_p = [&](int task, const char* keys, const char* dec, char* dst) {
+        const int m = task >> 1, o = task & 1;
+        const int ri = tile_row(m, lr), rj = tile_row(o, lr);
         f32x4 d = {0.f, 0.f, 0.f, 0.f};
-        u32x4 x[3];
-#pragma unroll
-        for (int e = 0; e < 3; ++e) x[e] = *reinterpret_cast<const u32x4*>(b + e * kFrag + lane * 16);
-        if (w >= 2) {
-            u32x4 z[3];
-#pragma unroll
-            for (int e = 0; e < 3; ++e) z[e] = *reinterpret_cast<const u32x4*>(b + (3 + e) * kFrag + lane * 16);
-#pragma unroll
-            for (int e = 0; e < 6; ++e) {
-                c = mfma_bf16(a[0][ia[e]], x[ib[e]], c);
-                d = mfma_bf16(a[1][ia[e]], z[ib[e]], d);
-            }
-            return c + d;
-        }
-#pragma unroll
-        for (int e = 0; e < 6; ++e) c = mfma_bf16(a[0][ia[e]], x[ib[e]], c);
-        return c;
-    };
-    // S <- gamma_C S + K^T u, u as B operands [2 steps][3 terms]
-    auto update = [&](int c, const char* u) {
-        const char* kt = lds + L::k + (c & 1) * (kC * kK * 2);
-        u32x4 b[2][3];
-#pragma unroll
-        for (int s = 0; s < 2; ++s)
-#pragma unroll
-            for (int e = 0; e < 3; ++e) b[s][e] = *reinterpret_cast<const u32x4*>(u + (3 * s + e) * kFrag + lane * 16);
-        u32x4 a[2][2];
-#pragma unroll
-        for (int s = 0; s < 2; ++s)
-#pragma unroll
-            for (int o = 0; o < 2; ++o)
-#pragma unroll
-                for (int x = 0; x < 2; ++x) {
-                    // transposed read: a quarter-wave's lane p points at four channels of
-                    // token 32 s + 8 lq + 4 x + p / 4, and lane i receives its row's
-                    // channel (tile o) of tokens 32 s + 8 lq + 4 x .. + 3
-                    const int row = 32 * s + 8 * lq + 4 * x + (lr >> 2);
-                    const char* p = kt + row * (kK * 2) + ((4 * w + (lr & 3)) ^ row_swizzle(row)) * 16 + 8 * o;
-                    const s16x4 q = __builtin_amdgcn_ds_read_tr16_b64_v4i16((__attribute__((address_space(3))) s16x4*)(p));
-                    const u32x2 q2 = __builtin_bit_cast(u32x2, q);
-                    a[s][o][2 * x] = q2[0];
-                    a[s][o][2 * x + 1] = q2[1];
-                }
-        S[0] *= gC;
-        S[1] *= gC;
-#pragma unroll
-        for (int e = 2; e >= 0; --e)
-#pragma unroll
-            for (int s = 0; s < 2; ++s)
-#pragma unroll
-                for (int o = 0; o < 2; ++o) S[o] = mfma_bf16(a[s][o], b[s][e], S[o]);
-    };
-    // K S and Q S of this wave's tokens
-    auto state_mul = [&](int c, const char* sb, f32x4& X, f32x4& Y) {
-        const char* kt = lds + L::k + (c & 1) * (kC * kK * 2);
-        const int row = 16 * w + lr;
-        u32x4 b[4][3], ka[4];
 #pragma unroll
         for (int s = 0; s < 4; ++s) {
-#pragma unroll
-            for (int e = 0; e < 3; ++e) b[s][e] = *reinterpret_cast<const u32x4*>(sb + (3 * s + e) * kFrag + lane * 16);
-            if (DELTA)
-                ka[s] = *reinterpret_cast<const u32x4*>(kt + row * (kK * 2) + ((4 * s + lq) ^ row_swizzle(row)) * 16);
+            const u32x4 ka = *reinterpret_cast<const u32x4*>(keys + rj * (kK * 2) + ((4 * s + lq) ^ row_swizzle(rj)) * 16);
+            const u32x4 qb = *reinterpret_cast<const u32x4*>(keys + kPlane + ri * (kK * 2) +
+                                                             ((4 * s + lq) ^ row_swizzle(ri)) * 16);
+            d = mfma_bf16(ka, qb, d);
         }
+        const float* f = reinterpret_cast<const float*>(dec);
+        const int b = 2 * lq + o, dist = ri - 4 * b;  // columns 4 b .. 4 b + 3
+        float x = f[b * kC + ri];
+        const f32x4 a4 = *reinterpret_cast<const f32x4*>(f + 8 * kC + 4 * b);
+        float z[4];
+        z[3] = d[3] * x;
 #pragma unroll
-        for (int e = 2; e >= 0; --e)
+        for (int r = 2; r >= 0; --r) {
+            x = dist == r ? 1.f : x * a4[r + 1];
+            z[r] = d[r] * x;
+        }
+        uint32_t u[3][2];
+        split3<2>(z, u);
 #pragma unroll
-            for (int s = 0; s < 4; ++s) {
-                if (DELTA) X = mfma_bf16(ka[s], b[s][e], X);
-                Y = mfma_bf16(qf[s], b[s][e], Y);
-            }
+        for (int e = 0; e < 3; ++e)
+            *reinterpret_cast<u32x2*>(dst + (2 * e + m) * kFrag + lane * 16 + 8 * o) = u32x2{u[e][0], u[e][1]};
     };
 
-    const f32x4 zero = {0.f, 0.f, 0.f, 0.f};
-    if (n_chunks > 0) {
-        const int last = n_chunks - 1;
-        load_k(0);
-        load_q(0);
-        load_gam(0);
-        load_v(0);
-        if constexpr (DELTA) {
-            load_tri(0, R::t, tf);
-            put_state(lds + L::s);
-            put_k(0);
-            f32x4 yp = zero;  // y of the chunk before, as far as it is formed
-            for (int c = 0; c < n_chunks; ++c) {
-                __syncthreads();  // keys and state of chunk c
-                const int cn = min(c + 1, last);  // the last chunk loads itself again
-                load_k(cn);
-                __builtin_amdgcn_sched_barrier(0);
-                f32x4 X = zero, Y = zero;
-                state_mul(c, lds + L::s, X, Y);
-                load_q(cn);
-                f32x4 x;
+    // this lane's places in a buffer of keys: row operands, step s at xor 64 s;
+    // transposed reads (a quarter-wave's lane p points at four channels of token
+    // 8 lq + 4 x + p / 4, and lane i receives its row's channel of tokens
+    // 8 lq + 4 x .. + 3), step s at xor 64 s, tile o at + 8 o; values likewise
+    int ra[2], ta[2], va[2];
 #pragma unroll
-                for (int r = 0; r < 4; ++r) {
-                    x[r] = fmaf(-gam[r], X[r], __uint_as_float(v[r] << 16));
-                    Y[r] *= gam[r];
-                }
-                put_tokens(lds + L::r, x);
-                if (c) store_y(c - 1, tri_mul(pf, lds + L::w, yp));
-                load_tri(c, R::p, pf);
-                yp = Y;
-                __syncthreads();  // v - gamma K S
-                x = tri_mul(tf, lds + L::r, zero);
-                load_tri(cn, R::t, tf);
-                put_tokens(lds + L::u, x * sig);
-                put_tokens(lds + L::w, x);
-                __syncthreads();  // w
-                update(c, lds + L::u);
-                load_gam(cn);
-                load_v(cn);
-                put_state(lds + L::s);
-                put_k(c + 1);
-            }
-            store_y(last, tri_mul(pf, lds + L::w, yp));
+    for (int m = 0; m < 2; ++m) {
+        const int row = tile_row(m, lr);
+        ra[m] = row * (kK * 2) + ((lq ^ row_swizzle(row)) * 16);
+        const int tk = 8 * lq + 4 * m + (lr >> 2);
+        ta[m] = tk * (kK * 2) + (((lr & 3) ^ row_swizzle(tk)) * 16);
+        va[m] = tk * (32 * NW) + 32 * w + 8 * (lr & 3);
+    }
+    auto tr_read = [&](const char* p) {
+        return __builtin_bit_cast(u32x2,
+                                  __builtin_amdgcn_ds_read_tr16_b64_v4i16((__attribute__((address_space(3))) s16x4*)(p)));
+    };
+    auto split_state = [&](int s) {
+        float f[8];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) f[i] = S[2 * s + i / 4][i & 3];
+        return split8(f);
+    };
+
+    int left = sp.len;  // tokens from chunk c on
+    if (left > 0) {
+        load_kq(left);
+        load_v(left);
+        if (DELTA) load_rec(left);
+        put_kq(lds + L::kq);
+        put_v(lds + L::vals);
+        if (DELTA) {
+            put_rec(lds + L::rec);
         } else {
-            auto put_v = [&](int c) {  // v and sigma v of chunk c
-                char* dst = lds + L::v2 + (c & 1) * 2 * kFrag + (w >> 1) * kFrag + half;
-                *reinterpret_cast<u32x2*>(dst) = u32x2{v[0] | v[1] << 16, v[2] | v[3] << 16};
-                f32x4 x;
-#pragma unroll
-                for (int r = 0; r < 4; ++r) x[r] = sig[r] * __uint_as_float(v[r] << 16);
-                put_tokens(lds + L::u2 + (c & 1) * 6 * kFrag, x);
-            };
-            load_tri(0, R::p, pf);
-            put_state(lds + L::s);
-            put_k(0);
-            put_v(0);
-            f32x4 g = gam;
-            float gc = gC;
-            for (int c = 0; c < n_chunks; ++c) {
-                __syncthreads();  // keys, values and state of chunk c; the other buffers are free
-                const int cn = min(c + 1, last);
-                load_k(cn);
-                load_v(cn);
-                load_gam(cn);
-                __builtin_amdgcn_sched_barrier(0);
-                f32x4 X = zero, Y = zero;
-                state_mul(c, lds + L::s + (c & 1) * L::sbuf, X, Y);
-                load_q(cn);
-                const float gnext = gC;
-                gC = gc;
-                update(c, lds + L::u2 + (c & 1) * 6 * kFrag);
-                gC = gc = gnext;
-                put_state(lds + L::s + ((c + 1) & 1) * L::sbuf);
-                Y *= g;
-                g = gam;
-                const char* vb = lds + L::v2 + (c & 1) * 2 * kFrag + lane * 16;
-                const u32x4 b0 = *reinterpret_cast<const u32x4*>(vb);
-#pragma unroll
-                for (int e = 2; e >= 0; --e) Y = mfma_bf16(pf[0][e], b0, Y);
-                if (w >= 2) {
-                    const u32x4 b1 = *reinterpret_cast<const u32x4*>(vb + kFrag);
-#pragma unroll
-                    for (int e = 2; e >= 0; --e) Y = mfma_bf16(pf[1][e], b1, Y);
-                }
-                load_tri(cn, R::p, pf);
-                store_y(c, Y);
-                put_k(c + 1);
-                put_v(c + 1);
+            load_kq(left - kC);
+            if (w == NW - 1) {
+                load_a(0);
+                put_decays(lds + L::f, lds + L::g);
+                load_a(1);
+                put_decays(lds + L::f + L::fbuf, lds + L::g + L::gbuf);
+                load_a(2);
             }
+            put_kq(lds + L::kq + L::kqbuf);
+            __syncthreads();
+            if (w < 4) put_p(w, lds + L::kq, lds + L::f, lds + L::p);
+        }
+        int b0 = 0, b1 = 1, b2 = 2;  // Mamba-2: buffers of chunks c, c + 1, c + 2
+        Split sb = split_state(0);
+        for (int c = 0; left > 0; ++c) {
+            __syncthreads();  // everything of chunk c is there, and nobody reads chunk c - 1 any more
+            const int cur = c & 1;
+            const char* keys = lds + L::kq + (DELTA ? cur : b0) * L::kqbuf;
+            const char* rec = lds + L::rec + cur * R::bytes;
+            const float* gam = reinterpret_cast<const float*>(DELTA ? rec + R::g : lds + L::g + b0 * L::gbuf);
+            const char* pf = (DELTA ? rec + R::p : lds + L::p + cur * kTri) + lane * 16;
+            const char* tf = rec + R::t + lane * 16;
+            const char* vals = lds + L::vals + cur * L::v;
+            load_kq(left - (DELTA ? 1 : 2) * kC);
+            load_v(left - kC);
+            if (DELTA) load_rec(left - kC);
+            __builtin_amdgcn_sched_barrier(0);  // the loads go out before the chunk is computed
+
+            // X = K S, Y = Q S: while a step's products run, the next step's state is
+            // split and the operands of the one after are read
+            f32x4 X[2] = {}, Y[2] = {};
+            u32x4 ka[2][2], qa[2][2], a[2][3];
+            auto read_rows = [&](int s) {
+#pragma unroll
+                for (int m = 0; m < 2; ++m) {
+                    const char* p = keys + (ra[m] ^ (64 * s));
+                    if (DELTA) ka[s & 1][m] = *reinterpret_cast<const u32x4*>(p);
+                    qa[s & 1][m] = *reinterpret_cast<const u32x4*>(p + kPlane);
+                }
+            };
+            auto read_tri = [&](const char* f) {
+#pragma unroll
+                for (int m = 0; m < 2; ++m)
+#pragma unroll
+                    for (int e = 0; e < 3; ++e) a[m][e] = *reinterpret_cast<const u32x4*>(f + (2 * e + m) * kFrag);
+            };
+            read_rows(0);
+            __builtin_amdgcn_sched_barrier(0);
+            float g[8], sg[8], wt[8], gC = 0.f;
+            u32x4 vb = {0, 0, 0, 0};  // values, tokens 8 lq .. 8 lq + 7: an exact B operand
+#pragma unroll
+            for (int s = 0; s < 4; ++s) {
+                if (s < 3) {
+                    read_rows(s + 1);
+                } else {
+                    if (DELTA) read_tri(tf);
+                    load8f(gam + 8 * lq, g);
+                    load8f(gam + kC + 8 * lq, sg);
+                    gC = gam[kC - 1];
+                }
+                if (s == 2) {
+                    const u32x2 lo = tr_read(vals + va[0]), hi = tr_read(vals + va[1]);
+                    vb = u32x4{lo[0], lo[1], hi[0], hi[1]};
+                }
+                Split nb;
+                if (s < 3) nb = split_state(s + 1);
+#pragma unroll
+                for (int e = 2; e >= 0; --e)
+#pragma unroll
+                    for (int m = 0; m < 2; ++m) {
+                        if (DELTA) X[m] = mfma_bf16(ka[s & 1][m], sb.t[e], X[m]);
+                        Y[m] = mfma_bf16(qa[s & 1][m], sb.t[e], Y[m]);
+                    }
+                if (s < 3) {
+                    sb = nb;
+                } else {
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        wt[2 * i] = __uint_as_float(vb[i] << 16);
+                        wt[2 * i + 1] = __uint_as_float(vb[i] & 0xffff0000u);
+                    }
+                }
+                __builtin_amdgcn_sched_group_barrier(0x100, 11, 0);
+#pragma unroll
+                for (int i = 0; i < (DELTA ? 12 : 6); ++i) {
+                    __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);
+                    __builtin_amdgcn_sched_group_barrier(0x002, DELTA ? 4 : 8, 0);
+                }
+                __builtin_amdgcn_sched_barrier(0);
+            }
+            Split wb, rb;
+            if (DELTA) {  // w = T (v - gamma X)
+#pragma unroll
+                for (int i = 0; i < 8; ++i) wt[i] = fmaf(-g[i], X[i / 4][i & 3], wt[i]);
+                rb = split8(wt);
+            }
+            // rows of K^T of step s
+            u32x4 kt[2][2];
+            auto read_kt = [&](int s) {
+#pragma unroll
+                for (int o = 0; o < 2; ++o)
+#pragma unroll
+                    for (int x = 0; x < 2; ++x) {
+                        const u32x2 q2 = tr_read(keys + (ta[x] ^ (64 * s)) + 8 * o);
+                        kt[s & 1][o][2 * x] = q2[0];
+                        kt[s & 1][o][2 * x + 1] = q2[1];
+                    }
+            };
+            read_kt(0);
+            f32x4 d[2] = {};
+            if (DELTA) {
+#pragma unroll
+                for (int e = 0; e < 6; ++e)
+#pragma unroll
+                    for (int m = 0; m < 2; ++m) d[m] = mfma_bf16(a[m][kTermA[e]], rb.t[kTermB[e]], d[m]);
+            }
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                S[i] *= gC;
+                Y[i / 4][i & 3] *= g[i];
+            }
+            if (DELTA) {
+#pragma unroll
+                for (int i = 0; i < 8; ++i) wt[i] = d[i / 4][i & 3];
+            }
+            // S <- gamma_C S + K^T (sigma w)
+            {
+                float f[8];
+#pragma unroll
+                for (int i = 0; i < 8; ++i) f[i] = sg[i] * wt[i];
+                rb = split8(f);
+            }
+            __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+            for (int s = 0; s < 4; ++s) {
+                if (s < 3) read_kt(s + 1);
+                if (s == 2) read_tri(pf);
+                if (DELTA && s == 0) wb = split8(wt);
+#pragma unroll
+                for (int e = 2; e >= 0; --e)
+#pragma unroll
+                    for (int o = 0; o < 2; ++o) S[2 * s + o] = mfma_bf16(kt[s & 1][o], rb.t[e], S[2 * s + o]);
+                __builtin_amdgcn_sched_group_barrier(0x100, 10, 0);
+#pragma unroll
+                for (int i = 0; i < 6; ++i) {
+                    __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);
+                    __builtin_amdgcn_sched_group_barrier(0x002, 8, 0);
+                }
+                __builtin_amdgcn_sched_barrier(0);
+            }
+            // y = gamma Y + P w, beside the next chunk's first split
+            sb = split_state(0);
+            if (DELTA) {
+#pragma unroll
+                for (int e = 0; e < 6; ++e)
+#pragma unroll
+                    for (int m = 0; m < 2; ++m) Y[m] = mfma_bf16(a[m][kTermA[e]], wb.t[kTermB[e]], Y[m]);
+            } else {
+#pragma unroll
+                for (int e = 2; e >= 0; --e)
+#pragma unroll
+                    for (int m = 0; m < 2; ++m) Y[m] = mfma_bf16(a[m][e], vb, Y[m]);
+            }
+#pragma unroll
+            for (int i = 0; i < (DELTA ? 12 : 6); ++i) {
+                __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);
+                __builtin_amdgcn_sched_group_barrier(0x002, DELTA ? 4 : 8, 0);
+            }
+            __builtin_amdgcn_sched_barrier(0);
+            {
+                const __amdgpu_buffer_rsrc_t rs = cy.rsrc(left);
+                const int at = 8 * lq * int(cy.stride) + col * 4;
+#pragma unroll
+                for (int i = 0; i < 8; ++i) buffer_store_f32(Y[i / 4][i & 3], rs, at + i * int(cy.stride), 0);
+                cy.next();
+            }
+            // the chunks to come
+            put_v(lds + L::vals + (cur ^ 1) * L::v);
+            if (DELTA) {
+                put_kq(lds + L::kq + (cur ^ 1) * L::kqbuf);
+                put_rec(lds + L::rec + (cur ^ 1) * R::bytes);
+            } else {
+                if (w < 4)
+                    put_p(w, lds + L::kq + b1 * L::kqbuf, lds + L::f + (cur ^ 1) * L::fbuf, lds + L::p + (cur ^ 1) * kTri);
+                put_kq(lds + L::kq + b2 * L::kqbuf);
+                if (w == NW - 1) {
+                    put_decays(lds + L::f + cur * L::fbuf, lds + L::g + b2 * L::gbuf);
+                    load_a(c + 3);
+                }
+                const int t = b0;
+                b0 = b1;
+                b1 = b2;
+                b2 = t;
+            }
+            left -= kC;
         }
     }
     const __amdgpu_buffer_rsrc_t so = buffer_rsrc(A.S + (size_t(sp.row) * A.H + h) * (kK * V), kK * V * 4);
 #pragma unroll
-    for (int i = 0; i < 8; ++i) buffer_store_f32(S[i / 4][i & 3], so, svo, i * V * 4);
+    for (int t = 0; t < 8; ++t)
+#pragma unroll
+        for (int r = 0; r < 4; ++r) buffer_store_f32(S[t][r], so, svo, (32 * (t >> 1) + 4 * (t & 1) + r) * V * 4);
 }
 
 namespace {
 
-template <int KIND>
-hipError_t launch_chunked(const RaggedArgs& a, char* ws, int V, hipStream_t s) {
-    constexpr int lds = KIND == SKSSM_MAMBA2 ? ScanLds::bytes_mamba : ScanLds::bytes_delta;
-    hipLaunchKernelGGL((prep_kernel<KIND>), dim3(uint32_t(prefill_slots(a.total, a.n_seqs) * a.H)), dim3(256), 0, s, a,
-                       ws);
-    hipError_t e = hipGetLastError();
-    if (e != hipSuccess) return e;
+template <int KIND, int NW>
+hipError_t launch_walk_t(const RaggedArgs& a, const char* ws, int V, hipStream_t s) {
+    constexpr int lds = WalkLds<KIND, NW>::bytes;
     if (lds > 64 * 1024) {
-        e = hipFuncSetAttribute(reinterpret_cast<const void*>(scan_kernel<KIND>),
-                                hipFuncAttributeMaxDynamicSharedMemorySize, lds);
+        const hipError_t e = hipFuncSetAttribute(reinterpret_cast<const void*>(walk_kernel<KIND, NW>),
+                                                 hipFuncAttributeMaxDynamicSharedMemorySize, lds);
         if (e != hipSuccess) return e;
     }
-    const long blocks = long(a.n_seqs) * ((a.H + 7) / 8) * 8 * (V / 16);
-    hipLaunchKernelGGL((scan_kernel<KIND>), dim3(uint32_t(blocks)), dim3(256), lds, s, a, ws, V);
+    const long blocks = long(a.n_seqs) * ((a.H + 7) / 8) * 8 * (V / (16 * NW));
+    hipLaunchKernelGGL((walk_kernel<KIND, NW>), dim3(uint32_t(blocks)), dim3(NW * 64), lds, s, a, ws, V);
     return hipGetLastError();
+}
+
+template <int KIND>
+hipError_t launch_walk(const RaggedArgs& a, const char* ws, int V, hipStream_t s) {
+    switch (V) {
+        case 64: return launch_walk_t<KIND, 4>(a, ws, V, s);
+        case 80: return launch_walk_t<KIND, 5>(a, ws, V, s);
+        case 96: return launch_walk_t<KIND, 6>(a, ws, V, s);
+        case 112: return launch_walk_t<KIND, 7>(a, ws, V, s);
+        case 128: return getenv("NW8") ? launch_walk_t<KIND, 8>(a, ws, V, s) : launch_walk_t<KIND, 4>(a, ws, V, s);
+    }
+    return hipErrorInvalidValue;
+}
+
+hipError_t launch_gdn(const RaggedArgs& a, char* ws, int V, hipStream_t s) {
+    const long tasks = prefill_slots(a.total, a.n_seqs) * a.H;
+    hipLaunchKernelGGL(prep_gdn_kernel, dim3(uint32_t((tasks + kPrepWaves - 1) / kPrepWaves)), dim3(kPrepWaves * 64), 0,
+                       s, a, ws);
+    const hipError_t e = hipGetLastError();
+    return e == hipSuccess ? launch_walk<SKSSM_GDN>(a, ws, V, s) : e;
 }
 
 // Whether a call takes the chunked kernels, else the recurrent one.
@@ -630,9 +687,8 @@ using namespace skssm;
 extern "C" size_t sketchssm_prefill_workspace(const sketchssm_shape* shape, int32_t n_seqs, int32_t total_tokens,
                                               int32_t max_len) {
     if (check_shape(shape) != SKSSM_OK || n_seqs <= 0 || total_tokens < 0 || max_len < 0) return 0;
-    if (!chunked(*shape, max_len)) return 0;
-    const size_t rec = shape->kind == SKSSM_MAMBA2 ? Record<SKSSM_MAMBA2>::bytes : Record<SKSSM_GDN>::bytes;
-    return size_t(prefill_slots(total_tokens, n_seqs)) * shape->H * rec;
+    if (!chunked(*shape, max_len) || shape->kind == SKSSM_MAMBA2) return 0;
+    return size_t(prefill_slots(total_tokens, n_seqs)) * shape->H * Record<SKSSM_GDN>::bytes;
 }
 
 extern "C" sketchssm_status sketchssm_prefill(const sketchssm_shape* shape, const float* S0, int32_t n_rows0,
@@ -657,10 +713,9 @@ extern "C" sketchssm_status sketchssm_prefill(const sketchssm_shape* shape, cons
     } else {
         // blocks of both launches stay below 2^31
         if (double(prefill_slots(total_tokens, n_seqs)) * shape->H >= 2147483648.0) return SKSSM_ESHAPE;
-        if (double(n_seqs) * (shape->H + 7) * (shape->V / 16) >= 2147483648.0) return SKSSM_ESHAPE;
+        if (double(n_seqs) * (shape->H + 7) >= 2147483648.0) return SKSSM_ESHAPE;
         char* ws = static_cast<char*>(workspace);
-        e = shape->kind == SKSSM_MAMBA2 ? launch_chunked<SKSSM_MAMBA2>(A, ws, shape->V, s)
-                                        : launch_chunked<SKSSM_GDN>(A, ws, shape->V, s);
+        e = shape->kind == SKSSM_MAMBA2 ? launch_walk<SKSSM_MAMBA2>(A, ws, shape->V, s) : launch_gdn(A, ws, shape->V, s);
     }
     return e == hipSuccess ? SKSSM_OK : SKSSM_ELAUNCH;
 }

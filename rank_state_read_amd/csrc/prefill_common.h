@@ -1,0 +1,121 @@
+// What the prefill kernels share: chunks of C = 32 tokens, operands of the bf16
+// matrix instruction with fp32 precision, and the walk's work on one chunk.
+//
+// Per sequence and head, within a chunk that starts at state S, with gamma_i the
+// decays' product up to token i, gamma_ij that after j up to i and sigma_j that
+// after j to the chunk's end (per key channel for KDA):
+//   A_ij = beta_i sum_c gamma_ij k_i k_j  (j < i),   P_ij = sum_c gamma_ij q_i k_j  (j <= i)
+//   T    = (I + A)^-1 diag(beta)                      (Mamba-2: w = v instead)
+//   w    = T (v - (gamma K) S),   y = (gamma Q) S + P w,   S <- gamma_C S + (sigma K)^T w
+//
+// Products run on the bf16 matrix instruction (16x16x32, fp32 sums) and keep
+// fp32 precision: an fp32 operand x is written as hi + mid + lo, three bf16
+// numbers of 8 significant bits each.  q, k, v in bf16 are exact operands, so
+// their products with an fp32 operand take three instructions, products of two
+// fp32 operands six (the terms below 2^-24 are left out).  The fp32 matrix
+// instruction has 1/16 of the bf16 rate.
+//
+// Value columns are independent of each other.  In the walk over a sequence's
+// chunks one wave owns 16 of them for all 128 key channels, so that nothing it
+// computes has to reach another wave: the accumulator layout (lane l, register r
+// <-> row 4 (l/16) + r, column l % 16) becomes the next product's B operand
+// (lane l <-> 8 consecutive rows from 8 (l/16), column l % 16) without leaving
+// the lane.  Rows 4 q + r of the two tiles of a 32-row group stand for group rows
+// 8 q + r and 8 q + 4 + r, which the A operand's rows follow.
+#pragma once
+
+#include <hip/hip_runtime.h>
+
+#include "device_common.h"
+#include "ragged.h"
+#include "sketchssm_internal.h"
+
+namespace skssm {
+
+typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
+typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
+typedef float f32x2 __attribute__((ext_vector_type(2)));
+typedef short s16x4 __attribute__((ext_vector_type(4)));
+typedef unsigned u32x2 __attribute__((ext_vector_type(2)));
+
+constexpr int kC = 32;                   // tokens per chunk
+constexpr int kFrag = 64 * 16;           // one operand of a wave, bytes
+constexpr int kTri = 3 * 2 * kFrag;      // T or P as A operands: three terms, two row tiles
+constexpr int kPlane = kC * kK * 2;      // a chunk's keys or queries in bf16
+
+__device__ __forceinline__ f32x4 mfma_bf16(u32x4 a, u32x4 b, f32x4 c) {
+    return __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, a), __builtin_bit_cast(bf16x8, b), c, 0,
+                                                   0, 0);
+}
+
+__device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
+    return __builtin_bit_cast(uint32_t, __builtin_convertvector((f32x2{lo, hi}), bf16x2));
+}
+
+// x = term 0 + term 1 + term 2 for 2 N consecutive values, each rounded to bf16.
+// (The bf16 dot product would subtract in one instruction, but it shares the
+// matrix unit: three of them beside a matrix instruction take 40 cycles, three
+// subtractions 21.)
+template <int N>
+__device__ __forceinline__ void split3(const float* f, uint32_t (&u)[3][N]) {
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+        float x0 = f[2 * i], x1 = f[2 * i + 1];
+#pragma unroll
+        for (int p = 0; p < 3; ++p) {
+            const uint32_t h = pack_bf16(x0, x1);
+            u[p][i] = h;
+            x0 -= __uint_as_float(h << 16);
+            x1 -= __uint_as_float(h & 0xffff0000u);
+        }
+    }
+}
+
+// Eight values as a B operand of three terms.
+struct Split {
+    u32x4 t[3];
+};
+__device__ __forceinline__ Split split8(const float* f) {
+    uint32_t u[3][4];
+    split3<4>(f, u);
+    Split s;
+#pragma unroll
+    for (int p = 0; p < 3; ++p) s.t[p] = u32x4{u[p][0], u[p][1], u[p][2], u[p][3]};
+    return s;
+}
+
+// Row i of row tile m of a 32-row group (see above).
+__device__ __forceinline__ int tile_row(int m, int i) { return 8 * (i >> 2) + 4 * m + (i & 3); }
+
+// Granule of 16 bytes g of a plane's token row r sits at granule g ^ row_swizzle(r):
+// the 16 rows of a tile start in different banks, and the 16 pieces that a
+// quarter-wave's transposed read collects lie in all of them.
+__device__ __forceinline__ int row_swizzle(int r) { return (r & 3) | (((r >> 3) & 3) << 2); }
+
+// The products of three-term operands that matter, small ones first.
+__device__ constexpr int kTermA[6] = {2, 0, 1, 1, 0, 0};
+__device__ constexpr int kTermB[6] = {0, 2, 1, 0, 1, 0};
+
+// A workspace record of a chunk and head: P, T (delta rule), gamma and sigma.
+template <int KIND>
+struct Record {
+    static constexpr bool delta = KIND != SKSSM_MAMBA2;
+    static constexpr int p = 0;
+    static constexpr int t = kTri;
+    static constexpr int g = delta ? 2 * kTri : kTri;
+    static constexpr int bytes = g + kFrag;  // whole pieces of 1 KB
+};
+
+// Chunk c of a sequence has slot off / C + seq + c of the workspace: a sequence
+// of len tokens has at most (off + len) / C - off / C + 1 chunks, so sequences
+// that do not overlap never share a slot.
+__host__ __device__ inline long first_slot(long t0, long seq) { return t0 / kC + seq; }
+inline long prefill_slots(long total, long n_seqs) { return total / kC + n_seqs; }
+
+// The heads' order over the blocks: those that share a key head sit on one XCD
+// (blocks go round the eight by index).  Head of unit u of XCD x, or >= H.
+__device__ __forceinline__ int head_of(const RaggedArgs& A, int x, int u) {
+    return A.Hk % 8 == 0 ? (x + 8 * (u / A.share)) * A.share + u % A.share : x + 8 * u;
+}
+
+}  // namespace skssm
