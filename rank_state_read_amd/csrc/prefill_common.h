@@ -38,10 +38,7 @@ typedef float f32x2 __attribute__((ext_vector_type(2)));
 typedef short s16x4 __attribute__((ext_vector_type(4)));
 typedef unsigned u32x2 __attribute__((ext_vector_type(2)));
 
-constexpr int kC = 32;                   // tokens per chunk
-constexpr int kFrag = 64 * 16;           // one operand of a wave, bytes
-constexpr int kTri = 3 * 2 * kFrag;      // T or P as A operands: three terms, two row tiles
-constexpr int kPlane = kC * kK * 2;      // a chunk's keys or queries in bf16
+constexpr int kFrag = 64 * 16;  // one operand of a wave, bytes
 
 __device__ __forceinline__ f32x4 mfma_bf16(u32x4 a, u32x4 b, f32x4 c) {
     return __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, a), __builtin_bit_cast(bf16x8, b), c, 0,
@@ -53,9 +50,9 @@ __device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
 }
 
 // x = term 0 + term 1 + term 2 for 2 N consecutive values, each rounded to bf16.
-// (The bf16 dot product would subtract in one instruction, but it shares the
-// matrix unit: three of them beside a matrix instruction take 40 cycles, three
-// subtractions 21.)
+// (The remainders could be bf16 dot products with (-1, 0) and (0, -1), one
+// instruction instead of two, but those share the matrix unit: three beside a
+// matrix instruction take 40 cycles, three subtractions 21.)
 template <int N>
 __device__ __forceinline__ void split3(const float* f, uint32_t (&u)[3][N]) {
 #pragma unroll
@@ -96,26 +93,76 @@ __device__ __forceinline__ int row_swizzle(int r) { return (r & 3) | (((r >> 3) 
 __device__ constexpr int kTermA[6] = {2, 0, 1, 1, 0, 0};
 __device__ constexpr int kTermB[6] = {0, 2, 1, 0, 1, 0};
 
-// A workspace record of a chunk and head: P, T (delta rule), gamma and sigma.
-template <int KIND>
-struct Record {
-    static constexpr bool delta = KIND != SKSSM_MAMBA2;
-    static constexpr int p = 0;
-    static constexpr int t = kTri;
-    static constexpr int g = delta ? 2 * kTri : kTri;
-    static constexpr int bytes = g + kFrag;  // whole pieces of 1 KB
-};
-
 // Chunk c of a sequence has slot off / C + seq + c of the workspace: a sequence
 // of len tokens has at most (off + len) / C - off / C + 1 chunks, so sequences
 // that do not overlap never share a slot.
-__host__ __device__ inline long first_slot(long t0, long seq) { return t0 / kC + seq; }
-inline long prefill_slots(long total, long n_seqs) { return total / kC + n_seqs; }
+template <int C>
+__host__ __device__ inline long first_slot(long t0, long seq) {
+    return t0 / C + seq;
+}
+template <int C>
+inline long prefill_slots(long total, long n_seqs) {
+    return total / C + n_seqs;
+}
+
+// The sequence and chunk of a workspace slot: first token and tokens, none: 0.
+template <int C>
+__device__ __forceinline__ int slot_chunk(const RaggedArgs& A, long slot, int lane, int& t0) {
+    for (int s0 = 0; s0 < A.n_seqs; s0 += 64) {
+        const int s = s0 + lane;
+        bool hit = false;
+        int tc = 0, cl = 0;
+        if (s < A.n_seqs) {
+            const SeqSpan sp = seq_span(A, s);
+            const long c = slot - first_slot<C>(sp.t0, s);
+            hit = sp.live && c >= 0 && c * C < sp.len;
+            tc = sp.t0 + int(c) * C;
+            cl = min(C, sp.len - int(c) * C);
+        }
+        const unsigned long long m = __ballot(hit);
+        if (m) {
+            const int f = __ffsll(m) - 1;
+            t0 = __shfl(tc, f, 64);
+            return __shfl(cl, f, 64);
+        }
+    }
+    return 0;
+}
+
+// The rows of one head over a sequence's chunks: a buffer resource whose first
+// address moves on by C tokens a time and which ends with the sequence, so that
+// what lies behind it reads as 0 and is not written.
+template <int C>
+struct Cursor {
+    uint64_t at;
+    uint32_t stride, row;
+    __device__ __forceinline__ Cursor(const void* base, int t0, int heads, int head, uint32_t row_bytes)
+        : at(reinterpret_cast<uint64_t>(base) + (uint64_t(t0) * heads + head) * row_bytes),
+          stride(heads * row_bytes),
+          row(row_bytes) {}
+    // `rows` tokens from here to the end of the sequence
+    __device__ __forceinline__ __amdgpu_buffer_rsrc_t rsrc(int rows) const {
+        return buffer_rsrc(reinterpret_cast<const void*>(at), rows > 0 ? uint32_t(min(rows, C) - 1) * stride + row : 0u);
+    }
+    __device__ __forceinline__ void next() { at += uint64_t(C) * stride; }
+};
+
+// Transposed LDS read: lane p of a quarter-wave points at four consecutive bf16
+// values; lane i receives value i % 4 of lanes i / 4, 4 + i / 4, 8 + i / 4, 12 + i / 4.
+__device__ __forceinline__ u32x2 tr_read(const char* p) {
+    return __builtin_bit_cast(u32x2,
+                              __builtin_amdgcn_ds_read_tr16_b64_v4i16((__attribute__((address_space(3))) s16x4*)(p)));
+}
 
 // The heads' order over the blocks: those that share a key head sit on one XCD
 // (blocks go round the eight by index).  Head of unit u of XCD x, or >= H.
 __device__ __forceinline__ int head_of(const RaggedArgs& A, int x, int u) {
     return A.Hk % 8 == 0 ? (x + 8 * (u / A.share)) * A.share + u % A.share : x + 8 * u;
 }
+
+// Launches of the chunked form (prefill_walk.hip, prefill_mamba2.hip).
+size_t walk_workspace(const sketchssm_shape& sh, long n_seqs, long total);
+hipError_t launch_walk(const sketchssm_shape& sh, const RaggedArgs& a, char* ws, hipStream_t s);
+hipError_t launch_mamba2(const RaggedArgs& a, int V, hipStream_t s);
 
 }  // namespace skssm

@@ -1,0 +1,890 @@
+// The chunked form for gfx950 (prefill_common.h) of the delta-rule layers, and of
+// Mamba-2 with float32 keys: chunks of C = 32 tokens.
+//
+// Two launches.  T and P depend on a chunk's own tokens alone, so the first
+// forms them for all chunks of all heads at once and leaves them in the
+// workspace; the second walks a sequence's chunks in order with the state in
+// registers.
+#include <hip/hip_runtime.h>
+
+#include <type_traits>
+
+#include "prefill_common.h"
+
+namespace skssm {
+
+namespace {
+
+constexpr int kC = 32;               // tokens per chunk
+constexpr int kTri = 3 * 2 * kFrag;  // T or P as A operands: three terms, two row tiles
+constexpr int kPlane = kC * kK * 2;  // one bf16 term of a chunk's keys or queries
+
+// A workspace record of a chunk and head: P, T, gamma and sigma.
+struct Record {
+    static constexpr int p = 0;
+    static constexpr int t = kTri;
+    static constexpr int g = 2 * kTri;
+    static constexpr int bytes = g + kFrag;  // whole pieces of 1 KB
+};
+
+constexpr int kGS = kC + 4;  // row stride of a C x C matrix in LDS, floats
+
+// Product of two 16 x 16 blocks in LDS.
+__device__ __forceinline__ f32x4 block_mul(const float* a, const float* b, int lr, int lq) {
+    f32x4 c = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+    for (int s = 0; s < 4; ++s) c = mfma_16x16x4(a[lr * kGS + 4 * s + lq], b[(4 * s + lq) * kGS + lr], c);
+    return c;
+}
+// The same with the second block in the accumulator layout.
+__device__ __forceinline__ f32x4 block_mul(const float* a, f32x4 b, int lr, int lq) {
+    f32x4 c = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+    for (int s = 0; s < 4; ++s) c = mfma_16x16x4(a[lr * kGS + 4 * lq + s], b[s], c);
+    return c;
+}
+
+__device__ __forceinline__ void wave_sync() {
+    __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+    __builtin_amdgcn_wave_barrier();
+}
+
+__device__ __forceinline__ float lane_value(float x, int i) {
+    return __uint_as_float(__builtin_amdgcn_readlane(__float_as_uint(x), i));
+}
+
+__device__ __forceinline__ u32x4 load16(__amdgpu_buffer_rsrc_t rs, int off) {
+    return __builtin_bit_cast(u32x4, __builtin_amdgcn_raw_buffer_load_b128(rs, off, 0, 0));
+}
+
+// ---------------------------------------------------------------------------
+// T and P of every chunk and head: one wave per (slot, head).
+// ---------------------------------------------------------------------------
+
+// A record from the wave's matrices in LDS: g = -A (strictly lower), gq = P;
+// lane j < 32 and j + 32 hold token j's beta (0 behind the sequence).
+template <bool DELTA>
+__device__ __forceinline__ void put_record(char* rec, float* g, const float* gq, float bj, int lane) {
+    typedef Record R;
+    const int lr = lane & 15, lq = lane >> 4;
+    float b[8];
+    if (DELTA) {
+        // (I + A)^-1: the diagonal blocks of 16 by forward substitution, one lane per
+        // column, then M_10 = M_11 (-A_10) M_00
+        if (lane < 32) {
+            float* d = g + (lane & 16) * (kGS + 1);
+            const int l = lane & 15;
+            float x[16];
+#pragma unroll
+            for (int i = 0; i < 16; ++i) {
+                float s0 = i == l ? 1.f : 0.f, s1 = 0.f;
+#pragma unroll
+                for (int m = 0; m < i; m += 4) {
+                    const f32x4 n4 = *reinterpret_cast<const f32x4*>(d + i * kGS + m);
+#pragma unroll
+                    for (int e = 0; e < 4; ++e)
+                        if (m + e < i) {
+                            if (e & 1) s1 = fmaf(n4[e], x[m + e], s1);
+                            else s0 = fmaf(n4[e], x[m + e], s0);
+                        }
+                }
+                x[i] = s0 + s1;
+            }
+            wave_sync();
+#pragma unroll
+            for (int i = 0; i < 16; ++i) d[i * kGS + l] = x[i];
+        }
+        wave_sync();
+        const f32x4 r10 = block_mul(g + 16 * kGS, g, lr, lq);
+        const f32x4 m10 = block_mul(g + 16 * kGS + 16, r10, lr, lq);
+        wave_sync();
+#pragma unroll
+        for (int r = 0; r < 4; ++r) g[(16 + 4 * lq + r) * kGS + lr] = m10[r];
+        wave_sync();
+#pragma unroll
+        for (int i = 0; i < 8; ++i) b[i] = __shfl(bj, 8 * lq + i, 64);
+    }
+    // P and T = (I + A)^-1 diag(beta) as A operands
+#pragma unroll
+    for (int m = 0; m < 2; ++m) {
+        float f[8];
+        const int at = tile_row(m, lr) * kGS + 8 * lq;
+        load8f(gq + at, f);
+        const Split p = split8(f);
+#pragma unroll
+        for (int e = 0; e < 3; ++e) *reinterpret_cast<u32x4*>(rec + R::p + (2 * e + m) * kFrag + lane * 16) = p.t[e];
+        if (DELTA) {
+            load8f(g + at, f);
+#pragma unroll
+            for (int i = 0; i < 8; ++i) f[i] *= b[i];
+            const Split t = split8(f);
+#pragma unroll
+            for (int e = 0; e < 3; ++e) *reinterpret_cast<u32x4*>(rec + R::t + (2 * e + m) * kFrag + lane * 16) = t.t[e];
+        }
+    }
+}
+
+// One decay per token.  k_i . k_j and q_i . k_j first (bf16: exact products on the
+// bf16 instruction; fp32: the fp32 instruction), then the decays' products.
+template <bool DELTA, typename QT>
+__global__ __launch_bounds__(256) void prep_scalar_kernel(RaggedArgs A, char* ws) {
+    constexpr bool BF = std::is_same<QT, Bf16Tag>::value;
+    typedef Record R;
+    __shared__ __align__(16) float tiles[4][2][kC * kGS];
+    const int w = threadIdx.x >> 6, lane = threadIdx.x & 63, lr = lane & 15, lq = lane >> 4;
+    const long task = long(blockIdx.x) * 4 + w;
+    const long slot = task / A.H;
+    const int h = int(task - slot * A.H), hk = h / A.share;
+    int t0 = 0;
+    const int clen = slot_chunk<kC>(A, slot, lane, t0);
+    if (clen == 0) return;  // no wave waits for another one below
+
+    float* g = tiles[w][0];
+    float* gq = tiles[w][1];
+    const int j = lane & 31;
+    const bool valid = j < clen;
+    const size_t tj = size_t(t0) + (valid ? j : 0);
+    const float aj = valid ? A.a[tj * A.H + h] : 1.f;
+    const float bj = !DELTA ? 1.f : valid ? A.beta[tj * A.H + h] : 0.f;
+    // operands of a row tile: bf16 steps of 32 channels, or fp32 steps of 4 (lane's
+    // channels 32 lq + s)
+    constexpr int NV = BF ? 4 : 8;
+    auto row = [&](const void* base, int m, u32x4 (&f)[NV]) {
+        const size_t r = (size_t(t0) + min(16 * m + lr, clen - 1)) * A.Hk + hk;
+        const char* src = static_cast<const char*>(base) + (BF ? (r * kK + 8 * lq) * 2 : (r * kK + 32 * lq) * 4);
+#pragma unroll
+        for (int s = 0; s < NV; ++s) f[s] = *reinterpret_cast<const u32x4*>(src + (BF ? 64 : 16) * s);
+    };
+    auto mul = [&](const u32x4 (&x)[NV], const u32x4 (&y)[NV]) {
+        f32x4 d = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+        for (int s = 0; s < NV; ++s) {
+            if (BF) {
+                d = mfma_bf16(x[s], y[s], d);
+            } else {
+#pragma unroll
+                for (int e = 0; e < 4; ++e) d = mfma_16x16x4(__uint_as_float(x[s][e]), __uint_as_float(y[s][e]), d);
+            }
+        }
+        return d;
+    };
+    {
+        u32x4 kf[2][NV], qf[NV];
+        row(A.k, 0, kf[0]);
+        row(A.k, 1, kf[1]);
+#pragma unroll
+        for (int m = 0; m < 2; ++m) {
+            row(A.q, m, qf);
+#pragma unroll
+            for (int n = 0; n <= m; ++n) {
+                f32x4 d = {0.f, 0.f, 0.f, 0.f};
+                if (DELTA) d = mul(kf[m], kf[n]);
+                const f32x4 dq = mul(qf, kf[n]);
+#pragma unroll
+                for (int r = 0; r < 4; ++r) {
+                    const int at = (16 * m + 4 * lq + r) * kGS + 16 * n + lr;
+                    if (DELTA) g[at] = d[r];
+                    gq[at] = dq[r];
+                }
+            }
+        }
+    }
+    wave_sync();
+
+    // column j: the decays' products after token j one factor at a time (a decay may
+    // be 0, so nothing is divided); lanes 0 .. 31 take -A, lanes 32 .. 63 take P
+    char* rec = ws + task * R::bytes;
+    {
+        float* gt = lane < 32 ? g : gq;
+        float d = 0.f, run = 1.f, gam = 0.f;
+#pragma unroll
+        for (int i = 0; i < kC; ++i) {
+            const float ai = lane_value(aj, i), bi = lane_value(bj, i);
+            d = i == j ? 1.f : d * ai;
+            run *= ai;
+            gam = i == j ? run : gam;
+            const float x = d * gt[i * kGS + j];
+            gt[i * kGS + j] = lane < 32 ? (i > j ? -bi * x : 0.f) : (i >= j && valid ? x : 0.f);
+        }
+        reinterpret_cast<float*>(rec + R::g)[lane] = lane < 32 ? gam : (valid ? d : 0.f);
+    }
+    wave_sync();
+    put_record<DELTA>(rec, g, gq, bj, lane);
+}
+
+// KDA: a decay per key channel, which does not leave the sums over channels and
+// must not be divided by.  For tokens j < i let b be the highest bit in which they
+// differ: all tokens with bit b set (U) against all with it clear (L), 16 each,
+//   A_ij ~ sum_c (k_i a_{m+1} .. a_i) (k_j a_{j+1} .. a_m),  m the last token of L
+// in the 2^{b+1}-block of i and j: one 16 x 16 product over the channels per bit,
+// used where i and j share their higher bits.  The partial products of decays
+// over 2^b-blocks follow from those over half blocks.  Lanes hold two channels
+// each; the scaled rows reach the fp32 matrix instruction through LDS.
+constexpr int kPS = kK + 4;  // row stride of the scaled rows, floats
+
+template <typename QT>
+__global__ __launch_bounds__(128) void prep_kda_kernel(RaggedArgs A, char* ws) {
+    constexpr bool BF = std::is_same<QT, Bf16Tag>::value;
+    typedef Record R;
+    __shared__ __align__(16) float tiles[2][2][kC * kGS];
+    __shared__ __align__(16) float rows[2][48 * kPS];
+    const int w = threadIdx.x >> 6, lane = threadIdx.x & 63, lr = lane & 15, lq = lane >> 4;
+    const long task = long(blockIdx.x) * 2 + w;
+    const long slot = task / A.H;
+    const int h = int(task - slot * A.H), hk = h / A.share;
+    int t0 = 0;
+    const int clen = slot_chunk<kC>(A, slot, lane, t0);
+    if (clen == 0) return;  // no wave waits for another one below
+    float* g = tiles[w][0];
+    float* gq = tiles[w][1];
+    float* sr = rows[w];
+
+    const int j = lane & 31;
+    const bool valid = j < clen;
+    const float bj = valid ? A.beta[(size_t(t0) + j) * A.H + h] : 0.f;
+    // this lane's two channels of every token; pre and suf: the decays' products over
+    // a token's 2^b-block up to it and after it
+    uint32_t kb[BF ? kC : 1], qb[BF ? kC : 1];
+    f32x2 pre[kC], suf[kC];
+#pragma unroll
+    for (int t = 0; t < kC; ++t) {
+        const bool in = t < clen;
+        const size_t tok = size_t(t0) + (in ? t : 0);
+        if constexpr (BF) {
+            const size_t e = (tok * A.Hk + hk) * kK + 2 * lane;
+            const uint32_t kx = *reinterpret_cast<const uint32_t*>(static_cast<const uint16_t*>(A.k) + e);
+            const uint32_t qx = *reinterpret_cast<const uint32_t*>(static_cast<const uint16_t*>(A.q) + e);
+            kb[t] = in ? kx : 0u;
+            qb[t] = in ? qx : 0u;
+        }
+        const f32x2 ax = *reinterpret_cast<const f32x2*>(A.a + (tok * A.H + h) * kK + 2 * lane);
+        pre[t] = in ? ax : f32x2{1.f, 1.f};
+        suf[t] = f32x2{1.f, 1.f};
+    }
+    auto value = [&](const void* base, const uint32_t* packed, int t) {
+        if constexpr (BF) {
+            return f32x2{__uint_as_float(packed[t] << 16), __uint_as_float(packed[t] & 0xffff0000u)};
+        } else {  // from memory again every time: registers are short
+            const size_t e = ((size_t(t0) + min(t, clen - 1)) * A.Hk + hk) * kK + 2 * lane;
+            const f32x2 x = *reinterpret_cast<const f32x2*>(static_cast<const float*>(base) + e);
+            return t < clen ? x : f32x2{0.f, 0.f};
+        }
+    };
+    auto key = [&](int t) { return value(A.k, kb, t); };
+    auto query = [&](int t) { return value(A.q, qb, t); };
+    // 16 x 16 products of rows x and y of the scaled rows
+    auto mul = [&](const float* x, const float* y) {
+        f32x4 d = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+        for (int s = 0; s < 8; ++s) {
+            const f32x4 xa = *reinterpret_cast<const f32x4*>(x + lr * kPS + 32 * lq + 4 * s);
+            const f32x4 ya = *reinterpret_cast<const f32x4*>(y + lr * kPS + 32 * lq + 4 * s);
+#pragma unroll
+            for (int e = 0; e < 4; ++e) d = mfma_16x16x4(xa[e], ya[e], d);
+        }
+        return d;
+    };
+    float* su = sr;
+    float* sq = sr + 16 * kPS;
+    float* sl = sr + 32 * kPS;
+    for (int i = lane; i < kC * kGS; i += 64) g[i] = gq[i] = 0.f;
+    // the diagonal of P: q_i . k_i
+#pragma unroll
+    for (int m = 0; m < 2; ++m) {
+#pragma unroll
+        for (int t = 0; t < 16; ++t) {
+            *reinterpret_cast<f32x2*>(sq + t * kPS + 2 * lane) = query(16 * m + t);
+            *reinterpret_cast<f32x2*>(sl + t * kPS + 2 * lane) = key(16 * m + t);
+        }
+        wave_sync();
+        const f32x4 d = mul(sq, sl);
+#pragma unroll
+        for (int r = 0; r < 4; ++r)
+            if (4 * lq + r == lr) gq[(16 * m + lr) * (kGS + 1)] = d[r];
+        wave_sync();
+    }
+#pragma unroll
+    for (int b = 0; b < 5; ++b) {
+        // pre, suf are over 2^b-blocks here
+#pragma unroll
+        for (int t = 0; t < 16; ++t) {
+            const int lo = ((t >> b) << (b + 1)) | (t & ((1 << b) - 1)), up = lo | (1 << b);
+            *reinterpret_cast<f32x2*>(su + t * kPS + 2 * lane) = key(up) * pre[up];
+            *reinterpret_cast<f32x2*>(sq + t * kPS + 2 * lane) = query(up) * pre[up];
+            *reinterpret_cast<f32x2*>(sl + t * kPS + 2 * lane) = key(lo) * suf[lo];
+        }
+        wave_sync();
+        const f32x4 d = mul(su, sl), dq = mul(sq, sl);
+        const int lj = ((lr >> b) << (b + 1)) | (lr & ((1 << b) - 1));
+#pragma unroll
+        for (int r = 0; r < 4; ++r) {
+            const int t = 4 * lq + r;
+            const int ui = ((t >> b) << (b + 1)) | (t & ((1 << b) - 1)) | (1 << b);
+            const float bi = __shfl(bj, ui, 64);
+            if ((t >> b) == (lr >> b)) {
+                g[ui * kGS + lj] = -bi * d[r];
+                gq[ui * kGS + lj] = dq[r];
+            }
+        }
+        wave_sync();
+#pragma unroll
+        for (int t = 0; t < kC; ++t)
+            if (!((t >> b) & 1)) suf[t] *= pre[t | ((2 << b) - 1)];
+#pragma unroll
+        for (int t = 0; t < kC; ++t)
+            if ((t >> b) & 1) pre[t] *= pre[(t & ~((2 << b) - 1)) | ((1 << b) - 1)];
+    }
+    put_record<true>(ws + task * R::bytes, g, gq, bj, lane);
+}
+
+}  // namespace
+
+// ---------------------------------------------------------------------------
+// The walk over a sequence's chunks: NW waves of 16 value columns each,
+// V / (16 NW) blocks per sequence and head.
+//
+// A chunk's operands pass through LDS: T and P as the first launch left them; keys
+// and queries as bf16 planes of one term (bf16 inputs, whose decays stay outside
+// the products) or of three -- float32 keys and queries, and for KDA gamma K,
+// gamma Q and sigma K, which are formed here from the inputs.
+//   one term:    one barrier a chunk; the next chunk is on its way from memory
+//                through registers to the other buffer meanwhile;
+//   three terms: one buffer of planes and two barriers, between which the waves
+//                form the next chunk's planes from inputs already in registers.
+// ---------------------------------------------------------------------------
+template <int KIND, typename QT, int NW>
+struct WalkLds {  // bytes
+    static constexpr bool bf = std::is_same<QT, Bf16Tag>::value, kda = KIND == SKSSM_KDA;
+    static constexpr int terms = bf && !kda ? 1 : 3;
+    static constexpr int v = NW * kFrag * (bf ? 1 : 2);        // a chunk's values [C][16 NW]
+    static constexpr int q = terms * kPlane;                   // queries' planes behind the keys'
+    static constexpr int kd = 2 * terms * kPlane;              // KDA: sigma K
+    static constexpr int kqbuf = (kda ? 3 : 2) * terms * kPlane;
+    static constexpr int kq = 0;
+    static constexpr int vals = kq + (terms == 1 ? 2 : 1) * kqbuf;  // two chunks
+    static constexpr int rec = vals + 2 * v;                   // two chunks
+    static constexpr int gp = rec + 2 * Record::bytes;         // KDA: decays' products of token groups [8][K],
+    static constexpr int gc = gp + (kda ? 8 * kK * 4 : 0);     // of the chunk [K]
+    static constexpr int bytes = gc + (kda ? kK * 4 : 0);
+};
+
+template <int KIND, typename QT, int NW>
+__global__ __launch_bounds__(NW * 64)
+__attribute__((amdgpu_waves_per_eu(WalkLds<KIND, QT, NW>::terms == 3 && NW <= 4 ? 1 : 2)))
+void walk_kernel(RaggedArgs A, const char* ws, int V) {
+    constexpr bool DELTA = KIND != SKSSM_MAMBA2, KDA = KIND == SKSSM_KDA;
+    constexpr bool BF = std::is_same<QT, Bf16Tag>::value;
+    typedef WalkLds<KIND, QT, NW> L;
+    typedef Record R;
+    constexpr int TERMS = L::terms;
+    extern __shared__ __align__(16) char lds[];
+    const int w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);  // the same in every lane
+    const int lane = threadIdx.x & 63, lr = lane & 15, lq = lane >> 4;
+    const int per = (A.H + 7) / 8;
+    const int slices = V / (16 * NW);
+    const int xcd = blockIdx.x & 7;
+    int rest = blockIdx.x >> 3;
+    const int slice = rest % slices;
+    rest /= slices;
+    const int seq = rest / per, h = head_of(A, xcd, rest % per);
+    if (h >= A.H) return;
+    const int hk = h / A.share;
+    const SeqSpan sp = seq_span(A, seq);
+    if (!sp.live) return;
+    const int col = 16 * (slice * NW + w) + lr;
+
+    // the state: tile 2 s + o, register r <-> channel 32 s + 8 lq + 4 o + r
+    f32x4 S[8];
+    const int svo = (8 * lq * V + col) * 4;
+    if (sp.row0 >= 0) {
+        const __amdgpu_buffer_rsrc_t s0 = buffer_rsrc(A.S0 + (size_t(sp.row0) * A.H + h) * (kK * V), kK * V * 4);
+#pragma unroll
+        for (int t = 0; t < 8; ++t)
+#pragma unroll
+            for (int r = 0; r < 4; ++r)
+                S[t][r] = buffer_load_f32(s0, svo, (32 * (t >> 1) + 4 * (t & 1) + r) * V * 4);
+    } else {
+#pragma unroll
+        for (int t = 0; t < 8; ++t) S[t] = f32x4{0.f, 0.f, 0.f, 0.f};
+    }
+
+    // ---- where a chunk's data come from ----
+    constexpr int E = Vec8<QT>::kElemBytes;
+    const uint32_t krow = kK * E, vrow = uint32_t(V) * E;
+    Cursor<kC> ck(A.k, sp.t0, A.Hk, hk, krow), cq(A.q, sp.t0, A.Hk, hk, krow);
+    Cursor<kC> cv(A.v, sp.t0, A.H, h, vrow), cy(A.y, sp.t0, A.H, h, uint32_t(V) * 4);
+    Cursor<kC> ca(A.a, sp.t0, A.H, h, kK * 4);  // KDA
+    uint64_t crec = reinterpret_cast<uint64_t>(ws) + (first_slot<kC>(sp.t0, seq) * A.H + h) * R::bytes;
+
+    // Pieces of 1 KB, on their way from memory to LDS through a wave's registers:
+    // those of the record, piece w + j NW by wave w; of the block's value columns; and
+    // (one term) 16 of keys and queries, four rows each, granules swizzled.
+    constexpr int NKQ = TERMS == 1 ? (16 + NW - 1) / NW : 0, NVP = BF ? 1 : 2;
+    constexpr int NR = R::bytes / kFrag, NRW = (NR + NW - 1) / NW;
+    constexpr int NP = NKQ + NVP + NRW;
+    u32x4 st[NP];
+    int kqoff[NKQ ? NKQ : 1], voff[NVP];
+#pragma unroll
+    for (int j = 0; j < NKQ; ++j) {
+        const int r = 4 * ((w + j * NW) & 7) + lq;
+        kqoff[j] = int(r * ck.stride) + (lr ^ row_swizzle(r)) * 16;
+    }
+#pragma unroll
+    for (int j = 0; j < NVP; ++j) {
+        const int at = (w + j * NW) * kFrag + lane * 16;
+        voff[j] = (at / (16 * E * NW)) * int(cv.stride) + at % (16 * E * NW) + slice * NW * 16 * E;
+    }
+    __amdgpu_buffer_rsrc_t rsk, rsq, rsv, rsr;
+    auto aim = [&](int rows) {  // the next chunk, `rows` tokens from its first on
+        if (TERMS == 1) {
+            rsk = ck.rsrc(rows);
+            rsq = cq.rsrc(rows);
+            ck.next();
+            cq.next();
+        }
+        rsv = cv.rsrc(rows);
+        cv.next();
+        rsr = buffer_rsrc(reinterpret_cast<const void*>(crec), rows > 0 ? R::bytes : 0);
+        crec += uint64_t(A.H) * R::bytes;
+    };
+    auto fetch = [&](int j) {
+        if (j < NKQ) st[j] = load16(w + j * NW < 8 ? rsk : rsq, kqoff[j]);
+        else if (j < NKQ + NVP) st[j] = load16(rsv, voff[j - NKQ]);
+        else st[j] = load16(rsr, (w + (j - NKQ - NVP) * NW) * kFrag + lane * 16);
+    };
+    auto put = [&](int j, char* kq, char* v, char* rec) {
+        const int o = lane * 16;
+        if (j < NKQ) {
+            if ((j + 1) * NW <= 16 || w + j * NW < 16) *reinterpret_cast<u32x4*>(kq + (w + j * NW) * kFrag + o) = st[j];
+        } else if (j < NKQ + NVP) {
+            *reinterpret_cast<u32x4*>(v + (w + (j - NKQ) * NW) * kFrag + o) = st[j];
+        } else {
+            const int i = w + (j - NKQ - NVP) * NW;
+            if ((j - NKQ - NVP + 1) * NW <= NR || i < NR) *reinterpret_cast<u32x4*>(rec + i * kFrag + o) = st[j];
+        }
+    };
+
+    // ---- three terms: planes from the inputs ----
+    // Lane = two channels, wave w = token groups w, w + NW, .. of four tokens.
+    constexpr int NG = (8 + NW - 1) / NW;
+    typedef typename std::conditional<BF, uint32_t, f32x2>::type pair_t;
+    pair_t kin[TERMS == 3 ? NG : 1][4], qin[TERMS == 3 ? NG : 1][4];
+    f32x2 ain[KDA ? NG : 1][4];
+    auto load_pair = [&](__amdgpu_buffer_rsrc_t rs, int off) {
+        if constexpr (BF) return uint32_t(__builtin_amdgcn_raw_buffer_load_b32(rs, off, 0, 0));
+        else return __builtin_bit_cast(f32x2, __builtin_amdgcn_raw_buffer_load_b64(rs, off, 0, 0));
+    };
+    auto unpack = [&](pair_t x) {
+        if constexpr (BF) return f32x2{__uint_as_float(x << 16), __uint_as_float(x & 0xffff0000u)};
+        else return x;
+    };
+    auto load_inputs = [&](int rows) {
+        const __amdgpu_buffer_rsrc_t rk = ck.rsrc(rows), rq = cq.rsrc(rows), ra = ca.rsrc(rows);
+#pragma unroll
+        for (int n = 0; n < NG; ++n)
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const int t = 4 * (w + n * NW) + i;  // beyond the chunk where NW does not divide 8: not used
+                kin[n][i] = load_pair(rk, t * int(ck.stride) + lane * 2 * E);
+                qin[n][i] = load_pair(rq, t * int(cq.stride) + lane * 2 * E);
+                if (KDA) {
+                    const f32x2 x = __builtin_bit_cast(
+                        f32x2, __builtin_amdgcn_raw_buffer_load_b64(ra, t * int(ca.stride) + lane * 8, 0, 0));
+                    ain[n][i] = t < rows ? x : f32x2{1.f, 1.f};
+                }
+            }
+        ck.next();
+        cq.next();
+        ca.next();
+    };
+    auto put_groups = [&]() {  // KDA: each token group's decays' product
+#pragma unroll
+        for (int n = 0; n < NG; ++n)
+            if ((n + 1) * NW <= 8 || w + n * NW < 8)
+                *reinterpret_cast<f32x2*>(lds + L::gp + ((w + n * NW) * kK + 2 * lane) * 4) =
+                    (ain[n][0] * ain[n][1]) * (ain[n][2] * ain[n][3]);
+    };
+    auto put_planes = [&]() {
+        f32x2 gprod[KDA ? 8 : 1];
+        if (KDA) {
+#pragma unroll
+            for (int g = 0; g < 8; ++g) gprod[g] = *reinterpret_cast<const f32x2*>(lds + L::gp + (g * kK + 2 * lane) * 4);
+            if (w == 0) {
+                f32x2 x = gprod[0];
+#pragma unroll
+                for (int g = 1; g < 8; ++g) x *= gprod[g];
+                *reinterpret_cast<f32x2*>(lds + L::gc + 2 * lane * 4) = x;
+            }
+        }
+#pragma unroll
+        for (int n = 0; n < NG; ++n) {
+            const int grp = w + n * NW;
+            if ((n + 1) * NW > 8 && grp >= 8) break;
+            f32x2 pre[4], suf[4];
+            if (KDA) {
+                f32x2 p = {1.f, 1.f}, q = p;
+#pragma unroll
+                for (int g = 0; g < 8; ++g) {
+                    if (g < grp) p *= gprod[g];
+                    if (7 - g > grp) q *= gprod[7 - g];
+                }
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    p *= ain[n][i];
+                    pre[i] = p;
+                    suf[3 - i] = q;
+                    q *= ain[n][3 - i];
+                }
+            }
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const int r = 4 * grp + i;
+                char* at = lds + L::kq + r * (kK * 2) + (((lane >> 2) ^ row_swizzle(r)) * 16) + (lane & 3) * 4;
+                auto three = [&](char* dst, f32x2 x) {
+                    const float f[2] = {x[0], x[1]};
+                    uint32_t u[3][1];
+                    split3<1>(f, u);
+#pragma unroll
+                    for (int e = 0; e < 3; ++e) *reinterpret_cast<uint32_t*>(dst + e * kPlane) = u[e][0];
+                };
+                const f32x2 kx = unpack(kin[n][i]), qx = unpack(qin[n][i]);
+                three(at, KDA ? kx * pre[i] : kx);
+                three(at + L::q, KDA ? qx * pre[i] : qx);
+                if (KDA) three(at + L::kd, kx * suf[i]);
+            }
+        }
+    };
+
+    // this lane's places in a plane: row operands, step s at xor 64 s; transposed
+    // reads (a quarter-wave's lane p points at four channels of token
+    // 8 lq + 4 x + p / 4, and lane i receives its row's channel of tokens
+    // 8 lq + 4 x .. + 3), step s at xor 64 s, tile o at + 8 o; bf16 values likewise
+    int ra[2], ta[2], va[2];
+#pragma unroll
+    for (int m = 0; m < 2; ++m) {
+        const int row = tile_row(m, lr);
+        ra[m] = row * (kK * 2) + ((lq ^ row_swizzle(row)) * 16);
+        const int tk = 8 * lq + 4 * m + (lr >> 2);
+        ta[m] = tk * (kK * 2) + (((lr & 3) ^ row_swizzle(tk)) * 16);
+        va[m] = tk * (32 * NW) + 32 * w + 8 * (lr & 3);
+    }
+    auto split_state = [&](int s) {
+        float f[8];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) f[i] = S[2 * s + i / 4][i & 3];
+        return split8(f);
+    };
+
+    int left = sp.len;  // tokens from chunk c on
+    if (left > 0) {
+        aim(left);
+#pragma unroll
+        for (int j = 0; j < NP; ++j) fetch(j);
+        if (TERMS == 3) {
+            load_inputs(left);
+            if (KDA) {
+                put_groups();
+                __syncthreads();
+            }
+            put_planes();
+            load_inputs(left - kC);
+        }
+#pragma unroll
+        for (int j = 0; j < NP; ++j) put(j, lds + L::kq, lds + L::vals, lds + L::rec);
+        aim(left - kC);
+#pragma unroll
+        for (int j = 0; j < NP; ++j) fetch(j);
+        Split sb = split_state(0);
+        for (int c = 0; left > 0; ++c) {
+            __syncthreads();  // everything of chunk c is there, and nobody reads chunk c - 1 any more
+            const int cur = c & 1;
+            const char* keys = lds + L::kq + (TERMS == 1 ? cur : 0) * L::kqbuf;
+            const char* rec = lds + L::rec + cur * R::bytes;
+            const float* gam = reinterpret_cast<const float*>(rec + R::g);
+            const char* pf = rec + R::p + lane * 16;
+            const char* tf = rec + R::t + lane * 16;
+            const char* vals = lds + L::vals + cur * L::v;
+            aim(left - 2 * kC);
+
+            // X = K S, Y = Q S: while a step's products run, the next step's state is
+            // split, the operands of the one after are read, and a quarter of the next
+            // chunk goes to LDS and of the one behind it leaves memory
+            f32x4 X[2] = {}, Y[2] = {};
+            constexpr int AB = TERMS == 1 ? 2 : 1;  // three terms: an operand is read where it is used
+            u32x4 ka[AB][2][TERMS], qa[AB][2][TERMS], a[2][3];
+            auto read_rows = [&](int s) {
+#pragma unroll
+                for (int m = 0; m < 2; ++m)
+#pragma unroll
+                    for (int e = 0; e < TERMS; ++e) {
+                        const char* p = keys + (ra[m] ^ (64 * s)) + e * kPlane;
+                        if (DELTA) ka[s % AB][m][e] = *reinterpret_cast<const u32x4*>(p);
+                        qa[s % AB][m][e] = *reinterpret_cast<const u32x4*>(p + L::q);
+                    }
+            };
+            auto read_tri = [&](const char* f) {
+#pragma unroll
+                for (int m = 0; m < 2; ++m)
+#pragma unroll
+                    for (int e = 0; e < 3; ++e) a[m][e] = *reinterpret_cast<const u32x4*>(f + (2 * e + m) * kFrag);
+            };
+            read_rows(0);
+            __builtin_amdgcn_sched_barrier(0);
+            float g[8], sg[8], wt[8], gC = 0.f;
+            u32x4 vb = {0, 0, 0, 0};  // values, tokens 8 lq .. 8 lq + 7
+#pragma unroll
+            for (int s = 0; s < 4; ++s) {
+                if (TERMS == 1 && s < 3) read_rows(s + 1);
+                if (s == 3) {
+                    if (DELTA) read_tri(tf);
+                    if (!KDA) {
+                        load8f(gam + 8 * lq, g);
+                        load8f(gam + kC + 8 * lq, sg);
+                        gC = gam[kC - 1];
+                    }
+                }
+                if (s == 2) {
+                    if constexpr (BF) {
+                        const u32x2 lo = tr_read(vals + va[0]), hi = tr_read(vals + va[1]);
+                        vb = u32x4{lo[0], lo[1], hi[0], hi[1]};
+                    } else {
+#pragma unroll
+                        for (int i = 0; i < 8; ++i)
+                            wt[i] = *reinterpret_cast<const float*>(vals + ((8 * lq + i) * 16 * NW + 16 * w + lr) * 4);
+                    }
+                }
+#pragma unroll
+                for (int j = NP * s / 4; j < NP * (s + 1) / 4; ++j) {
+                    put(j, lds + L::kq + (cur ^ 1) * L::kqbuf, lds + L::vals + (cur ^ 1) * L::v,
+                        lds + L::rec + (cur ^ 1) * R::bytes);
+                    fetch(j);
+                }
+                Split nb;
+                if (s < 3) nb = split_state(s + 1);
+                if constexpr (TERMS == 1) {
+#pragma unroll
+                    for (int e = 2; e >= 0; --e)
+#pragma unroll
+                        for (int m = 0; m < 2; ++m) {
+                            if (DELTA) X[m] = mfma_bf16(ka[s % AB][m][0], sb.t[e], X[m]);
+                            Y[m] = mfma_bf16(qa[s % AB][m][0], sb.t[e], Y[m]);
+                        }
+                } else {
+#pragma unroll
+                    for (int e = 0; e < 6; ++e)
+#pragma unroll
+                        for (int m = 0; m < 2; ++m) {
+                            if (DELTA) X[m] = mfma_bf16(ka[s % AB][m][kTermA[e]], sb.t[kTermB[e]], X[m]);
+                            Y[m] = mfma_bf16(qa[s % AB][m][kTermA[e]], sb.t[kTermB[e]], Y[m]);
+                        }
+                    if (s < 3) read_rows(s + 1);
+                }
+                if (s < 3) {
+                    sb = nb;
+                } else if constexpr (BF) {
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        wt[2 * i] = __uint_as_float(vb[i] << 16);
+                        wt[2 * i + 1] = __uint_as_float(vb[i] & 0xffff0000u);
+                    }
+                }
+                if (TERMS == 1) {
+                    __builtin_amdgcn_sched_group_barrier(0x100, 11, 0);
+#pragma unroll
+                    for (int i = 0; i < 12; ++i) {
+                        __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);
+                        __builtin_amdgcn_sched_group_barrier(0x002, 4, 0);
+                    }
+                } else {
+#pragma unroll
+                    for (int i = 0; i < (DELTA ? 24 : 12); ++i) {
+                        __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);
+                        __builtin_amdgcn_sched_group_barrier(0x002, DELTA ? 2 : 4, 0);
+                    }
+                }
+                __builtin_amdgcn_sched_barrier(0);
+            }
+            Split wb, rb;
+            if (DELTA) {  // w = T (v - gamma X)
+#pragma unroll
+                for (int i = 0; i < 8; ++i) wt[i] = KDA ? wt[i] - X[i / 4][i & 3] : fmaf(-g[i], X[i / 4][i & 3], wt[i]);
+                rb = split8(wt);
+            }
+            // rows of (sigma K)^T of step s
+            u32x4 kt[2][2][TERMS];
+            auto read_kt = [&](int s) {
+#pragma unroll
+                for (int o = 0; o < 2; ++o)
+#pragma unroll
+                    for (int e = 0; e < TERMS; ++e)
+#pragma unroll
+                        for (int x = 0; x < 2; ++x) {
+                            const u32x2 q2 = tr_read(keys + (KDA ? L::kd : 0) + e * kPlane + (ta[x] ^ (64 * s)) + 8 * o);
+                            kt[s & 1][o][e][2 * x] = q2[0];
+                            kt[s & 1][o][e][2 * x + 1] = q2[1];
+                        }
+            };
+            read_kt(0);
+            f32x4 d[2] = {};
+            if (DELTA) {
+#pragma unroll
+                for (int e = 0; e < 6; ++e)
+#pragma unroll
+                    for (int m = 0; m < 2; ++m) d[m] = mfma_bf16(a[m][kTermA[e]], rb.t[kTermB[e]], d[m]);
+            }
+            if (KDA) {
+#pragma unroll
+                for (int i = 0; i < 8; ++i)
+                    S[i] *= *reinterpret_cast<const f32x4*>(lds + L::gc + (32 * (i >> 1) + 8 * lq + 4 * (i & 1)) * 4);
+            } else {
+#pragma unroll
+                for (int i = 0; i < 8; ++i) {
+                    S[i] *= gC;
+                    Y[i / 4][i & 3] *= g[i];
+                }
+            }
+            if (DELTA) {
+#pragma unroll
+                for (int i = 0; i < 8; ++i) wt[i] = d[i / 4][i & 3];
+#pragma unroll
+                for (int i = 0; i < 12; ++i) {
+                    __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);
+                    __builtin_amdgcn_sched_group_barrier(0x002, 4, 0);
+                }
+            }
+            __builtin_amdgcn_sched_barrier(0);
+            // S <- gamma_C S + (sigma K)^T w
+            {
+                float f[8];
+#pragma unroll
+                for (int i = 0; i < 8; ++i) f[i] = KDA ? wt[i] : sg[i] * wt[i];
+                rb = split8(f);
+            }
+            __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+            for (int s = 0; s < 4; ++s) {
+                if (s < 3) read_kt(s + 1);
+                if (s == 2) read_tri(pf);
+                if (!KDA) {
+                    uint32_t u[3][1];
+                    split3<1>(wt + 2 * s, u);
+#pragma unroll
+                    for (int e = 0; e < 3; ++e) wb.t[e][s] = u[e][0];
+                }
+                if constexpr (TERMS == 1) {
+#pragma unroll
+                    for (int e = 2; e >= 0; --e)
+#pragma unroll
+                        for (int o = 0; o < 2; ++o) S[2 * s + o] = mfma_bf16(kt[s & 1][o][0], rb.t[e], S[2 * s + o]);
+                } else {
+#pragma unroll
+                    for (int e = 0; e < 6; ++e)
+#pragma unroll
+                        for (int o = 0; o < 2; ++o)
+                            S[2 * s + o] = mfma_bf16(kt[s & 1][o][kTermA[e]], rb.t[kTermB[e]], S[2 * s + o]);
+                }
+                __builtin_amdgcn_sched_group_barrier(0x100, 18, 0);
+#pragma unroll
+                for (int i = 0; i < (TERMS == 1 ? 6 : 12); ++i) {
+                    __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);
+                    __builtin_amdgcn_sched_group_barrier(0x002, 8, 0);
+                }
+                __builtin_amdgcn_sched_barrier(0);
+            }
+            if (KDA) wb = rb;
+            // y = gamma Y + P w, beside the next chunk's first split
+            sb = split_state(0);
+#pragma unroll
+            for (int e = 0; e < 6; ++e)
+#pragma unroll
+                for (int m = 0; m < 2; ++m) Y[m] = mfma_bf16(a[m][kTermA[e]], wb.t[kTermB[e]], Y[m]);
+#pragma unroll
+            for (int i = 0; i < 12; ++i) {
+                __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);
+                __builtin_amdgcn_sched_group_barrier(0x002, 4, 0);
+            }
+            __builtin_amdgcn_sched_barrier(0);
+            {
+                const __amdgpu_buffer_rsrc_t rs = cy.rsrc(left);
+                const int at = 8 * lq * int(cy.stride) + col * 4;
+#pragma unroll
+                for (int i = 0; i < 8; ++i) buffer_store_f32(Y[i / 4][i & 3], rs, at + i * int(cy.stride), 0);
+                cy.next();
+            }
+            if (TERMS == 3) {
+                if (KDA) put_groups();
+                __syncthreads();  // every wave is done with the planes; the groups' products are there
+                put_planes();
+                load_inputs(left - 2 * kC);
+            }
+            left -= kC;
+        }
+    }
+    const __amdgpu_buffer_rsrc_t so = buffer_rsrc(A.S + (size_t(sp.row) * A.H + h) * (kK * V), kK * V * 4);
+#pragma unroll
+    for (int t = 0; t < 8; ++t)
+#pragma unroll
+        for (int r = 0; r < 4; ++r) buffer_store_f32(S[t][r], so, svo, (32 * (t >> 1) + 4 * (t & 1) + r) * V * 4);
+}
+
+namespace {
+
+template <int KIND, typename QT, int NW>
+hipError_t launch_walk_t(const RaggedArgs& a, const char* ws, int V, hipStream_t s) {
+    constexpr int lds = WalkLds<KIND, QT, NW>::bytes;
+    static_assert(lds <= 160 * 1024, "LDS of a CU");
+    if (lds > 64 * 1024) {
+        const hipError_t e = hipFuncSetAttribute(reinterpret_cast<const void*>(walk_kernel<KIND, QT, NW>),
+                                                 hipFuncAttributeMaxDynamicSharedMemorySize, lds);
+        if (e != hipSuccess) return e;
+    }
+    const long blocks = long(a.n_seqs) * ((a.H + 7) / 8) * 8 * (V / (16 * NW));
+    if (blocks >= (1l << 31)) return hipErrorInvalidConfiguration;
+    hipLaunchKernelGGL((walk_kernel<KIND, QT, NW>), dim3(uint32_t(blocks)), dim3(NW * 64), lds, s, a, ws, V);
+    return hipGetLastError();
+}
+
+template <int KIND, typename QT>
+hipError_t launch_walk_v(const RaggedArgs& a, const char* ws, int V, hipStream_t s) {
+    switch (V) {
+        case 64: return launch_walk_t<KIND, QT, 4>(a, ws, V, s);
+        case 80: return launch_walk_t<KIND, QT, 5>(a, ws, V, s);
+        case 96: return launch_walk_t<KIND, QT, 6>(a, ws, V, s);
+        case 112: return launch_walk_t<KIND, QT, 7>(a, ws, V, s);
+        case 128: return launch_walk_t<KIND, QT, 4>(a, ws, V, s);
+    }
+    return hipErrorInvalidValue;
+}
+
+template <typename QT>
+hipError_t launch_prep(int kind, const RaggedArgs& a, char* ws, hipStream_t s) {
+    const long tasks = prefill_slots<kC>(a.total, a.n_seqs) * a.H;
+    if (tasks >= (1l << 31)) return hipErrorInvalidConfiguration;
+    const dim3 by4(uint32_t((tasks + 3) / 4)), by2(uint32_t((tasks + 1) / 2));
+    if (kind == SKSSM_KDA) hipLaunchKernelGGL((prep_kda_kernel<QT>), by2, dim3(128), 0, s, a, ws);
+    else if (kind == SKSSM_GDN) hipLaunchKernelGGL((prep_scalar_kernel<true, QT>), by4, dim3(256), 0, s, a, ws);
+    else hipLaunchKernelGGL((prep_scalar_kernel<false, QT>), by4, dim3(256), 0, s, a, ws);
+    return hipGetLastError();
+}
+
+}  // namespace
+
+size_t walk_workspace(const sketchssm_shape& sh, long n_seqs, long total) {
+    return size_t(prefill_slots<kC>(total, n_seqs)) * sh.H * Record::bytes;
+}
+
+hipError_t launch_walk(const sketchssm_shape& sh, const RaggedArgs& a, char* ws, hipStream_t s) {
+    const bool bf = sh.qkv == SKSSM_BF16;
+    const hipError_t e = bf ? launch_prep<Bf16Tag>(sh.kind, a, ws, s) : launch_prep<F32Tag>(sh.kind, a, ws, s);
+    if (e != hipSuccess) return e;
+    switch (sh.kind) {
+        case SKSSM_MAMBA2: return launch_walk_v<SKSSM_MAMBA2, F32Tag>(a, ws, sh.V, s);
+        case SKSSM_GDN:
+            return bf ? launch_walk_v<SKSSM_GDN, Bf16Tag>(a, ws, sh.V, s) : launch_walk_v<SKSSM_GDN, F32Tag>(a, ws, sh.V, s);
+        case SKSSM_KDA:
+            return bf ? launch_walk_v<SKSSM_KDA, Bf16Tag>(a, ws, sh.V, s) : launch_walk_v<SKSSM_KDA, F32Tag>(a, ws, sh.V, s);
+    }
+    return hipErrorInvalidValue;
+}
+
+}  // namespace skssm
