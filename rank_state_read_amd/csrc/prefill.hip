@@ -10,9 +10,6 @@ namespace {
 // Whether a call takes the chunked kernels, else the recurrent one.
 bool chunked(int max_len) { return max_len > 16; }
 
-// Mamba-2 with bf16 keys and queries needs no record of a chunk.
-bool needs_records(const sketchssm_shape& sh) { return sh.kind != SKSSM_MAMBA2 || sh.qkv != SKSSM_BF16; }
-
 }  // namespace
 
 }  // namespace skssm
@@ -22,7 +19,7 @@ using namespace skssm;
 extern "C" size_t sketchssm_prefill_workspace(const sketchssm_shape* shape, int32_t n_seqs, int32_t total_tokens,
                                               int32_t max_len) {
     if (check_shape(shape) != SKSSM_OK || n_seqs <= 0 || total_tokens < 0 || max_len < 0) return 0;
-    if (!chunked(max_len) || !needs_records(*shape)) return 0;
+    if (!chunked(max_len)) return 0;
     return walk_workspace(*shape, n_seqs, total_tokens);
 }
 
@@ -44,7 +41,6 @@ extern "C" sketchssm_status sketchssm_prefill(const sketchssm_shape* shape, cons
     hipStream_t s = static_cast<hipStream_t>(stream);
     hipError_t e;
     if (!chunked(max_len)) e = launch_recur(*shape, A, s);
-    else if (!needs_records(*shape)) e = launch_mamba2(A, shape->V, s);
     else e = launch_walk(*shape, A, static_cast<char*>(workspace), s);
     if (e == hipErrorInvalidConfiguration) return SKSSM_ESHAPE;  // more blocks than a launch takes
     return e == hipSuccess ? SKSSM_OK : SKSSM_ELAUNCH;

@@ -160,9 +160,8 @@ __device__ __forceinline__ int head_of(const RaggedArgs& A, int x, int u) {
     return A.Hk % 8 == 0 ? (x + 8 * (u / A.share)) * A.share + u % A.share : x + 8 * u;
 }
 
-// Launches of the chunked form (prefill_walk.hip, prefill_mamba2.hip).
+// The chunked form's launches (prefill_walk.hip).
 size_t walk_workspace(const sketchssm_shape& sh, long n_seqs, long total);
 hipError_t launch_walk(const sketchssm_shape& sh, const RaggedArgs& a, char* ws, hipStream_t s);
-hipError_t launch_mamba2(const RaggedArgs& a, int V, hipStream_t s);
 
 }  // namespace skssm

@@ -1,10 +1,12 @@
-// The chunked form for gfx950 (prefill_common.h) of the delta-rule layers, and of
-// Mamba-2 with float32 keys: chunks of C = 32 tokens.
+// The chunked form for gfx950 (prefill_common.h): chunks of C = 32 tokens.
 //
 // Two launches.  T and P depend on a chunk's own tokens alone, so the first
 // forms them for all chunks of all heads at once and leaves them in the
 // workspace; the second walks a sequence's chunks in order with the state in
-// registers.
+// registers.  A Mamba-2 layer with bf16 keys has many heads to a key head and
+// little work per value, so its P, one per head, would cost more to move than to
+// form: the first launch leaves q_i . k_j per key head and the decays' products,
+// and the walk forms P from them.
 #include <hip/hip_runtime.h>
 
 #include <type_traits>
@@ -26,6 +28,21 @@ struct Record {
     static constexpr int g = 2 * kTri;
     static constexpr int bytes = g + kFrag;  // whole pieces of 1 KB
 };
+
+// Mamba-2 with bf16 keys: gamma and sigma, the decays a [C], and with token groups
+// of four F[b][i] = a_{4b+4} .. a_i (1 for i = 4b + 3, 0 before); q_i . k_j per key
+// head in four tasks (row tile m, half o of the columns).
+struct DecayRecord {
+    static constexpr int g = 0;
+    static constexpr int a = 2 * kC * 4;
+    static constexpr int f = a + kC * 4;
+    static constexpr int bytes = f + 8 * kC * 4;
+    static constexpr int qk = 4 * kFrag;
+};
+
+// Mamba-2 with bf16 keys and queries: P is formed in the walk.
+template <int KIND, typename QT>
+constexpr bool kFormP = KIND == SKSSM_MAMBA2 && std::is_same<QT, Bf16Tag>::value;
 
 constexpr int kGS = kC + 4;  // row stride of a C x C matrix in LDS, floats
 
@@ -212,6 +229,75 @@ __global__ __launch_bounds__(256) void prep_scalar_kernel(RaggedArgs A, char* ws
     put_record<DELTA>(rec, g, gq, bj, lane);
 }
 
+// Mamba-2 with bf16 keys: one wave per (slot, key head) for q_i . k_j, formed
+// transposed so that a lane holds four columns of a row, and one per slot and two
+// heads, lane i = token i, for the decays' products.
+__global__ __launch_bounds__(256) void prep_mamba2_kernel(RaggedArgs A, char* ws, long slots) {
+    typedef DecayRecord R;
+    const int w = threadIdx.x >> 6, lane = threadIdx.x & 63, lr = lane & 15, lq = lane >> 4;
+    const int units = A.Hk + (A.H + 1) / 2;
+    const long task = long(blockIdx.x) * 4 + w;
+    const long slot = task / units;
+    const int u = int(task - slot * units);
+    int t0 = 0;
+    const int clen = slot_chunk<kC>(A, slot, lane, t0);
+    if (clen == 0) return;  // no wave waits for another one below
+    if (u < A.Hk) {
+        const Cursor<kC> ck(A.k, t0, A.Hk, u, kK * 2), cq(A.q, t0, A.Hk, u, kK * 2);
+        const __amdgpu_buffer_rsrc_t rk = ck.rsrc(clen), rq = cq.rsrc(clen);
+        u32x4 kf[2][4], qf[2][4];
+#pragma unroll
+        for (int m = 0; m < 2; ++m)
+#pragma unroll
+            for (int s = 0; s < 4; ++s) {
+                const int at = tile_row(m, lr) * int(ck.stride) + 64 * s + 16 * lq;
+                kf[m][s] = load16(rk, at);
+                qf[m][s] = load16(rq, at);
+            }
+        char* out = ws + slots * A.H * R::bytes + (slot * A.Hk + u) * R::qk + lane * 16;
+#pragma unroll
+        for (int m = 0; m < 2; ++m)
+#pragma unroll
+            for (int o = 0; o < 2; ++o) {
+                f32x4 d = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+                for (int s = 0; s < 4; ++s) d = mfma_bf16(kf[o][s], qf[m][s], d);
+                *reinterpret_cast<f32x4*>(out + (2 * m + o) * kFrag) = d;
+            }
+        return;
+    }
+    const int i = lane & 31, q = i & 3, b = i >> 2, h = 2 * (u - A.Hk) + (lane >> 5);
+    const bool in = i < clen && h < A.H;
+    const float av = in ? A.a[(size_t(t0) + i) * A.H + h] : 1.f;
+    // within the group: products up to token i, and after it
+    const float p1 = dpp_mov<0x90>(av);  // quad_perm [0,0,1,2]
+    float up = q >= 1 ? av * p1 : av;
+    const float p2 = dpp_mov<0x40>(up);  // quad_perm [0,0,0,1]
+    up = q >= 2 ? up * p2 : up;
+    const float n1 = dpp_mov<0xF9>(av);  // quad_perm [1,2,3,3]
+    const float s1 = q <= 2 ? n1 : 1.f;
+    const float n2 = dpp_mov<0xF9>(s1);
+    float down = q <= 1 ? s1 * n2 : s1;
+    const float n3 = dpp_mov<0xFF>(av);  // quad_perm [3,3,3,3]
+    down = q == 0 ? down * n3 : down;
+    char* rec = ws + (slot * A.H + h) * R::bytes;
+    float* f = reinterpret_cast<float*>(rec + R::f) + i;
+    float r = up, sg = down;
+#pragma unroll
+    for (int g = 7; g >= 0; --g) {
+        const float bg = __shfl(up, (lane & 32) + 4 * g + 3, 64);
+        const float x = g > b ? 0.f : g == b ? (q == 3 ? 1.f : 0.f) : r;
+        if (h < A.H) f[g * kC] = x;
+        r = g < b ? r * bg : r;
+        sg = g > b ? sg * bg : sg;
+    }
+    if (h < A.H) {
+        reinterpret_cast<float*>(rec + R::a)[i] = av;
+        reinterpret_cast<float*>(rec + R::g)[i] = r;
+        reinterpret_cast<float*>(rec + R::g)[kC + i] = in ? sg : 0.f;
+    }
+}
+
 // KDA: a decay per key channel, which does not leave the sums over channels and
 // must not be divided by.  For tokens j < i let b be the highest bit in which they
 // differ: all tokens with bit b set (U) against all with it clear (L), 16 each,
@@ -371,10 +457,11 @@ struct WalkLds {  // bytes
 template <int KIND, typename QT, int NW>
 __global__ __launch_bounds__(NW * 64)
 __attribute__((amdgpu_waves_per_eu(WalkLds<KIND, QT, NW>::terms == 3 && NW <= 4 ? 1 : 2)))
-void walk_kernel(RaggedArgs A, const char* ws, int V) {
+void walk_kernel(RaggedArgs A, const char* ws, long slots, int V) {
     constexpr bool DELTA = KIND != SKSSM_MAMBA2, KDA = KIND == SKSSM_KDA;
     constexpr bool BF = std::is_same<QT, Bf16Tag>::value;
     typedef WalkLds<KIND, QT, NW> L;
+    constexpr bool FORMP = kFormP<KIND, QT>;
     typedef Record R;
     constexpr int TERMS = L::terms;
     extern __shared__ __align__(16) char lds[];
@@ -414,13 +501,14 @@ void walk_kernel(RaggedArgs A, const char* ws, int V) {
     Cursor<kC> ck(A.k, sp.t0, A.Hk, hk, krow), cq(A.q, sp.t0, A.Hk, hk, krow);
     Cursor<kC> cv(A.v, sp.t0, A.H, h, vrow), cy(A.y, sp.t0, A.H, h, uint32_t(V) * 4);
     Cursor<kC> ca(A.a, sp.t0, A.H, h, kK * 4);  // KDA
-    uint64_t crec = reinterpret_cast<uint64_t>(ws) + (first_slot<kC>(sp.t0, seq) * A.H + h) * R::bytes;
+    constexpr int RB = FORMP ? DecayRecord::bytes : R::bytes;
+    uint64_t crec = reinterpret_cast<uint64_t>(ws) + (first_slot<kC>(sp.t0, seq) * A.H + h) * RB;
 
     // Pieces of 1 KB, on their way from memory to LDS through a wave's registers:
     // those of the record, piece w + j NW by wave w; of the block's value columns; and
     // (one term) 16 of keys and queries, four rows each, granules swizzled.
     constexpr int NKQ = TERMS == 1 ? (16 + NW - 1) / NW : 0, NVP = BF ? 1 : 2;
-    constexpr int NR = R::bytes / kFrag, NRW = (NR + NW - 1) / NW;
+    constexpr int NR = R::bytes / kFrag, NRW = FORMP ? 1 : (NR + NW - 1) / NW;
     constexpr int NP = NKQ + NVP + NRW;
     u32x4 st[NP];
     int kqoff[NKQ ? NKQ : 1], voff[NVP];
@@ -444,12 +532,13 @@ void walk_kernel(RaggedArgs A, const char* ws, int V) {
         }
         rsv = cv.rsrc(rows);
         cv.next();
-        rsr = buffer_rsrc(reinterpret_cast<const void*>(crec), rows > 0 ? R::bytes : 0);
-        crec += uint64_t(A.H) * R::bytes;
+        rsr = buffer_rsrc(reinterpret_cast<const void*>(crec), rows > 0 ? RB : 0);
+        crec += uint64_t(A.H) * RB;
     };
     auto fetch = [&](int j) {
         if (j < NKQ) st[j] = load16(w + j * NW < 8 ? rsk : rsq, kqoff[j]);
         else if (j < NKQ + NVP) st[j] = load16(rsv, voff[j - NKQ]);
+        else if (FORMP) st[j] = load16(rsr, DecayRecord::g + (lane & 15) * 16);
         else st[j] = load16(rsr, (w + (j - NKQ - NVP) * NW) * kFrag + lane * 16);
     };
     auto put = [&](int j, char* kq, char* v, char* rec) {
@@ -458,10 +547,42 @@ void walk_kernel(RaggedArgs A, const char* ws, int V) {
             if ((j + 1) * NW <= 16 || w + j * NW < 16) *reinterpret_cast<u32x4*>(kq + (w + j * NW) * kFrag + o) = st[j];
         } else if (j < NKQ + NVP) {
             *reinterpret_cast<u32x4*>(v + (w + (j - NKQ) * NW) * kFrag + o) = st[j];
+        } else if (FORMP) {
+            if (w == 0 && lane < 16) *reinterpret_cast<u32x4*>(rec + R::g + o) = st[j];
         } else {
             const int i = w + (j - NKQ - NVP) * NW;
             if ((j - NKQ - NVP + 1) * NW <= NR || i < NR) *reinterpret_cast<u32x4*>(rec + i * kFrag + o) = st[j];
         }
+    };
+
+    // ---- Mamba-2 with bf16 keys: P of a chunk ----
+    // Waves 0 .. 3 take a task each: 16 x 16 values, lane = row tile_row(m, lr) and
+    // columns 4 b .. 4 b + 3 with b = 2 lq + o; the decays between follow from F.
+    uint64_t cqk = reinterpret_cast<uint64_t>(ws) + uint64_t(slots) * A.H * DecayRecord::bytes +
+                   (first_slot<kC>(sp.t0, seq) * A.Hk + hk) * DecayRecord::qk;
+    f32x4 qk = {0.f, 0.f, 0.f, 0.f}, a4 = qk;
+    float f0 = 0.f;
+    const int pm = (w >> 1) & 1, po = w & 1, prow = tile_row(pm, lr), pb = 2 * lq + po;
+    auto load_p = [&](int rows) {  // from rsr's record: call it after aim()
+        const __amdgpu_buffer_rsrc_t rq = buffer_rsrc(reinterpret_cast<const void*>(cqk), rows > 0 ? DecayRecord::qk : 0);
+        qk = __builtin_bit_cast(f32x4, load16(rq, (w & 3) * kFrag + lane * 16));
+        a4 = __builtin_bit_cast(f32x4, load16(rsr, DecayRecord::a + 16 * pb));
+        f0 = buffer_load_f32(rsr, DecayRecord::f + (pb * kC + prow) * 4, 0);
+        cqk += uint64_t(A.Hk) * DecayRecord::qk;
+    };
+    auto put_p = [&](char* dst) {
+        float z[4], x = f0;
+        z[3] = qk[3] * x;
+#pragma unroll
+        for (int r = 2; r >= 0; --r) {
+            x = prow - 4 * pb == r ? 1.f : x * a4[r + 1];
+            z[r] = qk[r] * x;
+        }
+        uint32_t u[3][2];
+        split3<2>(z, u);
+#pragma unroll
+        for (int e = 0; e < 3; ++e)
+            *reinterpret_cast<u32x2*>(dst + (2 * e + pm) * kFrag + lane * 16 + 8 * po) = u32x2{u[e][0], u[e][1]};
     };
 
     // ---- three terms: planes from the inputs ----
@@ -580,6 +701,10 @@ void walk_kernel(RaggedArgs A, const char* ws, int V) {
         aim(left);
 #pragma unroll
         for (int j = 0; j < NP; ++j) fetch(j);
+        if (FORMP) {
+            load_p(left);
+            if (w < 4) put_p(lds + L::rec + R::p);
+        }
         if (TERMS == 3) {
             load_inputs(left);
             if (KDA) {
@@ -594,6 +719,7 @@ void walk_kernel(RaggedArgs A, const char* ws, int V) {
         aim(left - kC);
 #pragma unroll
         for (int j = 0; j < NP; ++j) fetch(j);
+        if (FORMP) load_p(left - kC);
         Split sb = split_state(0);
         for (int c = 0; left > 0; ++c) {
             __syncthreads();  // everything of chunk c is there, and nobody reads chunk c - 1 any more
@@ -691,9 +817,9 @@ void walk_kernel(RaggedArgs A, const char* ws, int V) {
                 if (TERMS == 1) {
                     __builtin_amdgcn_sched_group_barrier(0x100, 11, 0);
 #pragma unroll
-                    for (int i = 0; i < 12; ++i) {
+                    for (int i = 0; i < (DELTA ? 12 : 6); ++i) {
                         __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);
-                        __builtin_amdgcn_sched_group_barrier(0x002, 4, 0);
+                        __builtin_amdgcn_sched_group_barrier(0x002, DELTA ? 4 : 8, 0);
                     }
                 } else {
 #pragma unroll
@@ -765,7 +891,7 @@ void walk_kernel(RaggedArgs A, const char* ws, int V) {
             for (int s = 0; s < 4; ++s) {
                 if (s < 3) read_kt(s + 1);
                 if (s == 2) read_tri(pf);
-                if (!KDA) {
+                if (!KDA && !FORMP) {
                     uint32_t u[3][1];
                     split3<1>(wt + 2 * s, u);
 #pragma unroll
@@ -794,14 +920,21 @@ void walk_kernel(RaggedArgs A, const char* ws, int V) {
             if (KDA) wb = rb;
             // y = gamma Y + P w, beside the next chunk's first split
             sb = split_state(0);
+            if constexpr (FORMP) {  // w is v itself, an exact operand
 #pragma unroll
-            for (int e = 0; e < 6; ++e)
+                for (int e = 2; e >= 0; --e)
 #pragma unroll
-                for (int m = 0; m < 2; ++m) Y[m] = mfma_bf16(a[m][kTermA[e]], wb.t[kTermB[e]], Y[m]);
+                    for (int m = 0; m < 2; ++m) Y[m] = mfma_bf16(a[m][e], vb, Y[m]);
+            } else {
 #pragma unroll
-            for (int i = 0; i < 12; ++i) {
+                for (int e = 0; e < 6; ++e)
+#pragma unroll
+                    for (int m = 0; m < 2; ++m) Y[m] = mfma_bf16(a[m][kTermA[e]], wb.t[kTermB[e]], Y[m]);
+            }
+#pragma unroll
+            for (int i = 0; i < (FORMP ? 6 : 12); ++i) {
                 __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);
-                __builtin_amdgcn_sched_group_barrier(0x002, 4, 0);
+                __builtin_amdgcn_sched_group_barrier(0x002, FORMP ? 8 : 4, 0);
             }
             __builtin_amdgcn_sched_barrier(0);
             {
@@ -810,6 +943,10 @@ void walk_kernel(RaggedArgs A, const char* ws, int V) {
 #pragma unroll
                 for (int i = 0; i < 8; ++i) buffer_store_f32(Y[i / 4][i & 3], rs, at + i * int(cy.stride), 0);
                 cy.next();
+            }
+            if (FORMP) {  // P of the next chunk
+                if (w < 4) put_p(lds + L::rec + (cur ^ 1) * R::bytes + R::p);
+                load_p(left - 2 * kC);
             }
             if (TERMS == 3) {
                 if (KDA) put_groups();
@@ -831,6 +968,7 @@ namespace {
 
 template <int KIND, typename QT, int NW>
 hipError_t launch_walk_t(const RaggedArgs& a, const char* ws, int V, hipStream_t s) {
+    const long slots = prefill_slots<kC>(a.total, a.n_seqs);
     constexpr int lds = WalkLds<KIND, QT, NW>::bytes;
     static_assert(lds <= 160 * 1024, "LDS of a CU");
     if (lds > 64 * 1024) {
@@ -840,7 +978,7 @@ hipError_t launch_walk_t(const RaggedArgs& a, const char* ws, int V, hipStream_t
     }
     const long blocks = long(a.n_seqs) * ((a.H + 7) / 8) * 8 * (V / (16 * NW));
     if (blocks >= (1l << 31)) return hipErrorInvalidConfiguration;
-    hipLaunchKernelGGL((walk_kernel<KIND, QT, NW>), dim3(uint32_t(blocks)), dim3(NW * 64), lds, s, a, ws, V);
+    hipLaunchKernelGGL((walk_kernel<KIND, QT, NW>), dim3(uint32_t(blocks)), dim3(NW * 64), lds, s, a, ws, slots, V);
     return hipGetLastError();
 }
 
@@ -861,7 +999,11 @@ hipError_t launch_prep(int kind, const RaggedArgs& a, char* ws, hipStream_t s) {
     const long tasks = prefill_slots<kC>(a.total, a.n_seqs) * a.H;
     if (tasks >= (1l << 31)) return hipErrorInvalidConfiguration;
     const dim3 by4(uint32_t((tasks + 3) / 4)), by2(uint32_t((tasks + 1) / 2));
-    if (kind == SKSSM_KDA) hipLaunchKernelGGL((prep_kda_kernel<QT>), by2, dim3(128), 0, s, a, ws);
+    const long units = prefill_slots<kC>(a.total, a.n_seqs) * (a.Hk + (a.H + 1) / 2);
+    if (kFormP<SKSSM_MAMBA2, QT> && kind == SKSSM_MAMBA2)
+        hipLaunchKernelGGL(prep_mamba2_kernel, dim3(uint32_t((units + 3) / 4)), dim3(256), 0, s, a, ws,
+                           prefill_slots<kC>(a.total, a.n_seqs));
+    else if (kind == SKSSM_KDA) hipLaunchKernelGGL((prep_kda_kernel<QT>), by2, dim3(128), 0, s, a, ws);
     else if (kind == SKSSM_GDN) hipLaunchKernelGGL((prep_scalar_kernel<true, QT>), by4, dim3(256), 0, s, a, ws);
     else hipLaunchKernelGGL((prep_scalar_kernel<false, QT>), by4, dim3(256), 0, s, a, ws);
     return hipGetLastError();
@@ -870,7 +1012,10 @@ hipError_t launch_prep(int kind, const RaggedArgs& a, char* ws, hipStream_t s) {
 }  // namespace
 
 size_t walk_workspace(const sketchssm_shape& sh, long n_seqs, long total) {
-    return size_t(prefill_slots<kC>(total, n_seqs)) * sh.H * Record::bytes;
+    const size_t slots = prefill_slots<kC>(total, n_seqs);
+    if (sh.kind == SKSSM_MAMBA2 && sh.qkv == SKSSM_BF16)
+        return slots * (size_t(sh.H) * DecayRecord::bytes + size_t(kq_heads_of(sh)) * DecayRecord::qk);
+    return slots * sh.H * Record::bytes;
 }
 
 hipError_t launch_walk(const sketchssm_shape& sh, const RaggedArgs& a, char* ws, hipStream_t s) {
@@ -878,7 +1023,8 @@ hipError_t launch_walk(const sketchssm_shape& sh, const RaggedArgs& a, char* ws,
     const hipError_t e = bf ? launch_prep<Bf16Tag>(sh.kind, a, ws, s) : launch_prep<F32Tag>(sh.kind, a, ws, s);
     if (e != hipSuccess) return e;
     switch (sh.kind) {
-        case SKSSM_MAMBA2: return launch_walk_v<SKSSM_MAMBA2, F32Tag>(a, ws, sh.V, s);
+        case SKSSM_MAMBA2:
+            return bf ? launch_walk_v<SKSSM_MAMBA2, Bf16Tag>(a, ws, sh.V, s) : launch_walk_v<SKSSM_MAMBA2, F32Tag>(a, ws, sh.V, s);
         case SKSSM_GDN:
             return bf ? launch_walk_v<SKSSM_GDN, Bf16Tag>(a, ws, sh.V, s) : launch_walk_v<SKSSM_GDN, F32Tag>(a, ws, sh.V, s);
         case SKSSM_KDA:
