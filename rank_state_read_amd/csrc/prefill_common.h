@@ -122,8 +122,8 @@ __device__ __forceinline__ int slot_chunk(const RaggedArgs& A, long slot, int la
         const unsigned long long m = __ballot(hit);
         if (m) {
             const int f = __ffsll(m) - 1;
-            t0 = __shfl(tc, f, 64);
-            return __shfl(cl, f, 64);
+            t0 = __builtin_amdgcn_readlane(tc, f);
+            return __builtin_amdgcn_readlane(cl, f);
         }
     }
     return 0;
@@ -140,10 +140,17 @@ struct Cursor {
         : at(reinterpret_cast<uint64_t>(base) + (uint64_t(t0) * heads + head) * row_bytes),
           stride(heads * row_bytes),
           row(row_bytes) {}
-    // `rows` tokens from here to the end of the sequence
-    __device__ __forceinline__ __amdgpu_buffer_rsrc_t rsrc(int rows) const {
-        return buffer_rsrc(reinterpret_cast<const void*>(at), rows > 0 ? uint32_t(min(rows, C) - 1) * stride + row : 0u);
+    // bytes of a chunk with `rows` tokens from its first to the end of the sequence
+    __device__ __forceinline__ uint32_t bytes(int rows) const {
+        // (the compiler takes vector registers for this, which a resource must not have)
+        return __builtin_amdgcn_readfirstlane(rows >= C ? (C - 1) * stride + row
+                                              : rows > 0 ? (rows - 1) * stride + row
+                                                         : 0u);
     }
+    __device__ __forceinline__ __amdgpu_buffer_rsrc_t rsrc_of(uint32_t n) const {
+        return buffer_rsrc(reinterpret_cast<const void*>(at), n);
+    }
+    __device__ __forceinline__ __amdgpu_buffer_rsrc_t rsrc(int rows) const { return rsrc_of(bytes(rows)); }
     __device__ __forceinline__ void next() { at += uint64_t(C) * stride; }
 };
 

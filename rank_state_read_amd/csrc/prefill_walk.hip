@@ -148,7 +148,8 @@ __global__ __launch_bounds__(256) void prep_scalar_kernel(RaggedArgs A, char* ws
     constexpr bool BF = std::is_same<QT, Bf16Tag>::value;
     typedef Record R;
     __shared__ __align__(16) float tiles[4][2][kC * kGS];
-    const int w = threadIdx.x >> 6, lane = threadIdx.x & 63, lr = lane & 15, lq = lane >> 4;
+    const int w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int lane = threadIdx.x & 63, lr = lane & 15, lq = lane >> 4;
     const long task = long(blockIdx.x) * 4 + w;
     const long slot = task / A.H;
     const int h = int(task - slot * A.H), hk = h / A.share;
@@ -234,7 +235,8 @@ __global__ __launch_bounds__(256) void prep_scalar_kernel(RaggedArgs A, char* ws
 // heads, lane i = token i, for the decays' products.
 __global__ __launch_bounds__(256) void prep_mamba2_kernel(RaggedArgs A, char* ws, long slots) {
     typedef DecayRecord R;
-    const int w = threadIdx.x >> 6, lane = threadIdx.x & 63, lr = lane & 15, lq = lane >> 4;
+    const int w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int lane = threadIdx.x & 63, lr = lane & 15, lq = lane >> 4;
     const int units = A.Hk + (A.H + 1) / 2;
     const long task = long(blockIdx.x) * 4 + w;
     const long slot = task / units;
@@ -314,7 +316,8 @@ __global__ __launch_bounds__(128) void prep_kda_kernel(RaggedArgs A, char* ws) {
     typedef Record R;
     __shared__ __align__(16) float tiles[2][2][kC * kGS];
     __shared__ __align__(16) float rows[2][48 * kPS];
-    const int w = threadIdx.x >> 6, lane = threadIdx.x & 63, lr = lane & 15, lq = lane >> 4;
+    const int w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int lane = threadIdx.x & 63, lr = lane & 15, lq = lane >> 4;
     const long task = long(blockIdx.x) * 2 + w;
     const long slot = task / A.H;
     const int h = int(task - slot * A.H), hk = h / A.share;
@@ -447,16 +450,19 @@ struct WalkLds {  // bytes
     static constexpr int kd = 2 * terms * kPlane;              // KDA: sigma K
     static constexpr int kqbuf = (kda ? 3 : 2) * terms * kPlane;
     static constexpr int kq = 0;
-    static constexpr int vals = kq + (terms == 1 ? 2 : 1) * kqbuf;  // two chunks
-    static constexpr int rec = vals + 2 * v;                   // two chunks
-    static constexpr int gp = rec + 2 * Record::bytes;         // KDA: decays' products of token groups [8][K],
+    static constexpr int vals = kq + (terms == 1 ? 2 : 1) * kqbuf;
+    static constexpr int rec = vals + 2 * v;                   // P, (T,) gamma and sigma of two chunks
+    static constexpr int p = 0, t = kTri;
+    static constexpr int g = (kFormP<KIND, QT> ? 1 : 2) * kTri;
+    static constexpr int recbuf = kFormP<KIND, QT> ? g + 2 * kC * 4 : Record::bytes;
+    static constexpr int gp = rec + 2 * recbuf;                // KDA: decays' products of token groups [8][K],
     static constexpr int gc = gp + (kda ? 8 * kK * 4 : 0);     // of the chunk [K]
     static constexpr int bytes = gc + (kda ? kK * 4 : 0);
 };
 
 template <int KIND, typename QT, int NW>
 __global__ __launch_bounds__(NW * 64)
-__attribute__((amdgpu_waves_per_eu(WalkLds<KIND, QT, NW>::terms == 3 && NW <= 4 ? 1 : 2)))
+__attribute__((amdgpu_waves_per_eu(kFormP<KIND, QT> ? 3 : 2)))
 void walk_kernel(RaggedArgs A, const char* ws, long slots, int V) {
     constexpr bool DELTA = KIND != SKSSM_MAMBA2, KDA = KIND == SKSSM_KDA;
     constexpr bool BF = std::is_same<QT, Bf16Tag>::value;
@@ -476,7 +482,7 @@ void walk_kernel(RaggedArgs A, const char* ws, long slots, int V) {
     const int seq = rest / per, h = head_of(A, xcd, rest % per);
     if (h >= A.H) return;
     const int hk = h / A.share;
-    const SeqSpan sp = seq_span(A, seq);
+    const SeqSpan sp = seq_span_uniform(A, seq);
     if (!sp.live) return;
     const int col = 16 * (slice * NW + w) + lr;
 
@@ -509,7 +515,7 @@ void walk_kernel(RaggedArgs A, const char* ws, long slots, int V) {
     // (one term) 16 of keys and queries, four rows each, granules swizzled.
     constexpr int NKQ = TERMS == 1 ? (16 + NW - 1) / NW : 0, NVP = BF ? 1 : 2;
     constexpr int NR = R::bytes / kFrag, NRW = FORMP ? 1 : (NR + NW - 1) / NW;
-    constexpr int NP = NKQ + NVP + NRW;
+    constexpr int NP = NKQ + NRW + NVP;
     u32x4 st[NP];
     int kqoff[NKQ ? NKQ : 1], voff[NVP];
 #pragma unroll
@@ -525,8 +531,9 @@ void walk_kernel(RaggedArgs A, const char* ws, long slots, int V) {
     __amdgpu_buffer_rsrc_t rsk, rsq, rsv, rsr;
     auto aim = [&](int rows) {  // the next chunk, `rows` tokens from its first on
         if (TERMS == 1) {
-            rsk = ck.rsrc(rows);
-            rsq = cq.rsrc(rows);
+            const uint32_t n = ck.bytes(rows);
+            rsk = ck.rsrc_of(n);
+            rsq = cq.rsrc_of(n);
             ck.next();
             cq.next();
         }
@@ -537,21 +544,21 @@ void walk_kernel(RaggedArgs A, const char* ws, long slots, int V) {
     };
     auto fetch = [&](int j) {
         if (j < NKQ) st[j] = load16(w + j * NW < 8 ? rsk : rsq, kqoff[j]);
-        else if (j < NKQ + NVP) st[j] = load16(rsv, voff[j - NKQ]);
+        else if (j >= NKQ + NRW) st[j] = load16(rsv, voff[j - NKQ - NRW]);
         else if (FORMP) st[j] = load16(rsr, DecayRecord::g + (lane & 15) * 16);
-        else st[j] = load16(rsr, (w + (j - NKQ - NVP) * NW) * kFrag + lane * 16);
+        else st[j] = load16(rsr, (w + (j - NKQ) * NW) * kFrag + lane * 16);
     };
     auto put = [&](int j, char* kq, char* v, char* rec) {
         const int o = lane * 16;
         if (j < NKQ) {
             if ((j + 1) * NW <= 16 || w + j * NW < 16) *reinterpret_cast<u32x4*>(kq + (w + j * NW) * kFrag + o) = st[j];
-        } else if (j < NKQ + NVP) {
-            *reinterpret_cast<u32x4*>(v + (w + (j - NKQ) * NW) * kFrag + o) = st[j];
+        } else if (j >= NKQ + NRW) {
+            *reinterpret_cast<u32x4*>(v + (w + (j - NKQ - NRW) * NW) * kFrag + o) = st[j];
         } else if (FORMP) {
-            if (w == 0 && lane < 16) *reinterpret_cast<u32x4*>(rec + R::g + o) = st[j];
+            if (w == 0 && lane < 16) *reinterpret_cast<u32x4*>(rec + L::g + o) = st[j];
         } else {
-            const int i = w + (j - NKQ - NVP) * NW;
-            if ((j - NKQ - NVP + 1) * NW <= NR || i < NR) *reinterpret_cast<u32x4*>(rec + i * kFrag + o) = st[j];
+            const int i = w + (j - NKQ) * NW;
+            if ((j - NKQ + 1) * NW <= NR || i < NR) *reinterpret_cast<u32x4*>(rec + i * kFrag + o) = st[j];
         }
     };
 
@@ -608,22 +615,24 @@ void walk_kernel(RaggedArgs A, const char* ws, long slots, int V) {
                 const int t = 4 * (w + n * NW) + i;  // beyond the chunk where NW does not divide 8: not used
                 kin[n][i] = load_pair(rk, t * int(ck.stride) + lane * 2 * E);
                 qin[n][i] = load_pair(rq, t * int(cq.stride) + lane * 2 * E);
-                if (KDA) {
-                    const f32x2 x = __builtin_bit_cast(
+                if (KDA)
+                    ain[n][i] = __builtin_bit_cast(
                         f32x2, __builtin_amdgcn_raw_buffer_load_b64(ra, t * int(ca.stride) + lane * 8, 0, 0));
-                    ain[n][i] = t < rows ? x : f32x2{1.f, 1.f};
-                }
             }
         ck.next();
         cq.next();
         ca.next();
     };
-    auto put_groups = [&]() {  // KDA: each token group's decays' product
+    auto put_groups = [&](int rows) {  // KDA: each token group's decays' product
 #pragma unroll
-        for (int n = 0; n < NG; ++n)
+        for (int n = 0; n < NG; ++n) {
+#pragma unroll
+            for (int i = 0; i < 4; ++i)  // behind the sequence nothing decays
+                if (4 * (w + n * NW) + i >= rows) ain[n][i] = f32x2{1.f, 1.f};
             if ((n + 1) * NW <= 8 || w + n * NW < 8)
                 *reinterpret_cast<f32x2*>(lds + L::gp + ((w + n * NW) * kK + 2 * lane) * 4) =
                     (ain[n][0] * ain[n][1]) * (ain[n][2] * ain[n][3]);
+        }
     };
     auto put_planes = [&]() {
         f32x2 gprod[KDA ? 8 : 1];
@@ -703,12 +712,12 @@ void walk_kernel(RaggedArgs A, const char* ws, long slots, int V) {
         for (int j = 0; j < NP; ++j) fetch(j);
         if (FORMP) {
             load_p(left);
-            if (w < 4) put_p(lds + L::rec + R::p);
+            if (w < 4) put_p(lds + L::rec + L::p);
         }
         if (TERMS == 3) {
             load_inputs(left);
             if (KDA) {
-                put_groups();
+                put_groups(left);
                 __syncthreads();
             }
             put_planes();
@@ -725,10 +734,10 @@ void walk_kernel(RaggedArgs A, const char* ws, long slots, int V) {
             __syncthreads();  // everything of chunk c is there, and nobody reads chunk c - 1 any more
             const int cur = c & 1;
             const char* keys = lds + L::kq + (TERMS == 1 ? cur : 0) * L::kqbuf;
-            const char* rec = lds + L::rec + cur * R::bytes;
-            const float* gam = reinterpret_cast<const float*>(rec + R::g);
-            const char* pf = rec + R::p + lane * 16;
-            const char* tf = rec + R::t + lane * 16;
+            const char* rec = lds + L::rec + cur * L::recbuf;
+            const float* gam = reinterpret_cast<const float*>(rec + L::g);
+            const char* pf = rec + L::p + lane * 16;
+            const char* tf = rec + L::t + lane * 16;
             const char* vals = lds + L::vals + cur * L::v;
             aim(left - 2 * kC);
 
@@ -758,6 +767,13 @@ void walk_kernel(RaggedArgs A, const char* ws, long slots, int V) {
             __builtin_amdgcn_sched_barrier(0);
             float g[8], sg[8], wt[8], gC = 0.f;
             u32x4 vb = {0, 0, 0, 0};  // values, tokens 8 lq .. 8 lq + 7
+            auto unpack_values = [&]() {
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    wt[2 * i] = __uint_as_float(vb[i] << 16);
+                    wt[2 * i + 1] = __uint_as_float(vb[i] & 0xffff0000u);
+                }
+            };
 #pragma unroll
             for (int s = 0; s < 4; ++s) {
                 if (TERMS == 1 && s < 3) read_rows(s + 1);
@@ -765,7 +781,7 @@ void walk_kernel(RaggedArgs A, const char* ws, long slots, int V) {
                     if (DELTA) read_tri(tf);
                     if (!KDA) {
                         load8f(gam + 8 * lq, g);
-                        load8f(gam + kC + 8 * lq, sg);
+                        if (!FORMP) load8f(gam + kC + 8 * lq, sg);
                         gC = gam[kC - 1];
                     }
                 }
@@ -782,7 +798,7 @@ void walk_kernel(RaggedArgs A, const char* ws, long slots, int V) {
 #pragma unroll
                 for (int j = NP * s / 4; j < NP * (s + 1) / 4; ++j) {
                     put(j, lds + L::kq + (cur ^ 1) * L::kqbuf, lds + L::vals + (cur ^ 1) * L::v,
-                        lds + L::rec + (cur ^ 1) * R::bytes);
+                        lds + L::rec + (cur ^ 1) * L::recbuf);
                     fetch(j);
                 }
                 Split nb;
@@ -807,12 +823,8 @@ void walk_kernel(RaggedArgs A, const char* ws, long slots, int V) {
                 }
                 if (s < 3) {
                     sb = nb;
-                } else if constexpr (BF) {
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) {
-                        wt[2 * i] = __uint_as_float(vb[i] << 16);
-                        wt[2 * i + 1] = __uint_as_float(vb[i] & 0xffff0000u);
-                    }
+                } else if constexpr (BF && !FORMP) {
+                    unpack_values();
                 }
                 if (TERMS == 1) {
                     __builtin_amdgcn_sched_group_barrier(0x100, 11, 0);
@@ -880,6 +892,10 @@ void walk_kernel(RaggedArgs A, const char* ws, long slots, int V) {
             }
             __builtin_amdgcn_sched_barrier(0);
             // S <- gamma_C S + (sigma K)^T w
+            if constexpr (FORMP) {
+                load8f(gam + kC + 8 * lq, sg);
+                unpack_values();
+            }
             {
                 float f[8];
 #pragma unroll
@@ -890,7 +906,7 @@ void walk_kernel(RaggedArgs A, const char* ws, long slots, int V) {
 #pragma unroll
             for (int s = 0; s < 4; ++s) {
                 if (s < 3) read_kt(s + 1);
-                if (s == 2) read_tri(pf);
+                if (s == (FORMP ? 3 : 2)) read_tri(pf);
                 if (!KDA && !FORMP) {
                     uint32_t u[3][1];
                     split3<1>(wt + 2 * s, u);
@@ -945,11 +961,11 @@ void walk_kernel(RaggedArgs A, const char* ws, long slots, int V) {
                 cy.next();
             }
             if (FORMP) {  // P of the next chunk
-                if (w < 4) put_p(lds + L::rec + (cur ^ 1) * R::bytes + R::p);
+                if (w < 4) put_p(lds + L::rec + (cur ^ 1) * L::recbuf + L::p);
                 load_p(left - 2 * kC);
             }
             if (TERMS == 3) {
-                if (KDA) put_groups();
+                if (KDA) put_groups(left - kC);
                 __syncthreads();  // every wave is done with the planes; the groups' products are there
                 put_planes();
                 load_inputs(left - 2 * kC);

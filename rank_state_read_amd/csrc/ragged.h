@@ -46,6 +46,19 @@ __device__ __forceinline__ SeqSpan seq_span(const RaggedArgs& A, int i) {
     return s;
 }
 
+// The same where every lane asks for one sequence.  What lanes share is moved to
+// scalar registers: a buffer resource built from vector registers costs a loop
+// over their values at each access.
+__device__ __forceinline__ SeqSpan seq_span_uniform(const RaggedArgs& A, int i) {
+    SeqSpan s = seq_span(A, __builtin_amdgcn_readfirstlane(i));
+    s.row = __builtin_amdgcn_readfirstlane(s.row);
+    s.row0 = __builtin_amdgcn_readfirstlane(s.row0);
+    s.t0 = __builtin_amdgcn_readfirstlane(s.t0);
+    s.len = __builtin_amdgcn_readfirstlane(s.len);
+    s.live = __builtin_amdgcn_readfirstlane(int(s.live)) != 0;
+    return s;
+}
+
 // Checks the arguments of a ragged entry point (host) and fills `out`.
 sketchssm_status ragged_args(const sketchssm_shape* shape, const float* S0, int32_t n_rows0, const int32_t* rows0,
                              float* S, const int32_t* rows, const int32_t* offsets, int32_t n_seqs,

@@ -71,7 +71,7 @@ void recur_kernel(RaggedArgs A) {
     const int seq = blockIdx.x / A.H;
     const int h = blockIdx.x - seq * A.H;
     const int hk = h / A.share;
-    const SeqSpan sp = seq_span(A, seq);
+    const SeqSpan sp = seq_span_uniform(A, seq);
     if (!sp.live) return;
 
     f32x4 s[8];
