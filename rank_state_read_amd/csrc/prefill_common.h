@@ -129,6 +129,20 @@ __device__ __forceinline__ int slot_chunk(const RaggedArgs& A, long slot, int la
     return 0;
 }
 
+// The sequence that the r-th group of blocks takes: the longest first, so that the
+// last blocks to start are short ones.  Up to 64 sequences, one per lane; with more,
+// the order they come in (the blocks of any one are then few among many).
+__device__ __forceinline__ int seq_of_rank(const RaggedArgs& A, int r, int lane) {
+    if (A.n_seqs > 64) return r;
+    const int len = lane < A.n_seqs ? max(A.offsets[lane + 1] - A.offsets[lane], 0) : -1;
+    int rank = 0;
+    for (int j = 0; j < A.n_seqs; ++j) {
+        const int other = __builtin_amdgcn_readlane(len, j);
+        rank += other > len || (other == len && j < lane) ? 1 : 0;
+    }
+    return __ffsll(__ballot(lane < A.n_seqs && rank == r)) - 1;
+}
+
 // The rows of one head over a sequence's chunks: a buffer resource whose first
 // address moves on by C tokens a time and which ends with the sequence, so that
 // what lies behind it reads as 0 and is not written.

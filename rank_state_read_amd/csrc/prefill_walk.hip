@@ -479,9 +479,9 @@ void walk_kernel(RaggedArgs A, const char* ws, long slots, int V) {
     int rest = blockIdx.x >> 3;
     const int slice = rest % slices;
     rest /= slices;
-    const int seq = rest / per, h = head_of(A, xcd, rest % per);
+    const int h = head_of(A, xcd, rest % per);
     if (h >= A.H) return;
-    const int hk = h / A.share;
+    const int hk = h / A.share, seq = seq_of_rank(A, rest / per, lane);
     const SeqSpan sp = seq_span_uniform(A, seq);
     if (!sp.live) return;
     const int col = 16 * (slice * NW + w) + lr;
