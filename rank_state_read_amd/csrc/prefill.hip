@@ -20,7 +20,7 @@ extern "C" size_t sketchssm_prefill_workspace(const sketchssm_shape* shape, int3
                                               int32_t max_len) {
     if (check_shape(shape) != SKSSM_OK || n_seqs <= 0 || total_tokens < 0 || max_len < 0) return 0;
     if (!chunked(max_len)) return 0;
-    return walk_workspace(*shape, n_seqs, total_tokens);
+    return walk_workspace(*shape, n_seqs, total_tokens, max_len);
 }
 
 extern "C" sketchssm_status sketchssm_prefill(const sketchssm_shape* shape, const float* S0, int32_t n_rows0,

@@ -182,7 +182,7 @@ __device__ __forceinline__ int head_of(const RaggedArgs& A, int x, int u) {
 }
 
 // The chunked form's launches (prefill_walk.hip).
-size_t walk_workspace(const sketchssm_shape& sh, long n_seqs, long total);
+size_t walk_workspace(const sketchssm_shape& sh, long n_seqs, long total, long max_len);
 hipError_t launch_walk(const sketchssm_shape& sh, const RaggedArgs& a, char* ws, hipStream_t s);
 
 }  // namespace skssm

@@ -9,6 +9,7 @@
 // and the walk forms P from them.
 #include <hip/hip_runtime.h>
 
+#include <algorithm>
 #include <type_traits>
 
 #include "prefill_common.h"
@@ -429,6 +430,24 @@ __global__ __launch_bounds__(128) void prep_kda_kernel(RaggedArgs A, char* ws) {
 }  // namespace
 
 // ---------------------------------------------------------------------------
+// Segments.  With few sequences and heads a walk leaves most of the chip idle: its
+// chunks follow each other.  A state passes through a segment of tokens as
+// S -> M S + N, so a long sequence is cut into segments of `len` tokens and three
+// launches take the walk's place: one forms M and N of every segment but the last
+// (the walk without outputs, on the identity without values and on the zero
+// state), one the state at each segment's end in turn, and one walks all segments
+// at once from there.  Mamba-2's M is one number.
+// ---------------------------------------------------------------------------
+struct Segments {
+    int len;     // tokens, a multiple of C; 0: none
+    int most;    // segments of the longest sequence
+    char* ends;  // per segment and head N [K, V], which becomes the state at its end, and M [K, K]
+    __device__ __forceinline__ float* n_of(long t0, int seq, int seg, int H, int h, int V) const {
+        return reinterpret_cast<float*>(ends) + ((t0 / len + seq + seg) * H + h) * long(kK * V + kK * kK);
+    }
+};
+
+// ---------------------------------------------------------------------------
 // The walk over a sequence's chunks: NW waves of 16 value columns each,
 // V / (16 NW) blocks per sequence and head.
 //
@@ -460,37 +479,58 @@ struct WalkLds {  // bytes
     static constexpr int bytes = gc + (kda ? kK * 4 : 0);
 };
 
-template <int KIND, typename QT, int NW>
+// ENDS: M and N of segments, no outputs.  The columns of M follow those of N.
+template <int KIND, typename QT, int NW, bool ENDS>
 __global__ __launch_bounds__(NW * 64)
 __attribute__((amdgpu_waves_per_eu(kFormP<KIND, QT> ? 3 : 2)))
-void walk_kernel(RaggedArgs A, const char* ws, long slots, int V) {
+void walk_kernel(RaggedArgs A, const char* ws, long slots, int V, Segments SG) {
     constexpr bool DELTA = KIND != SKSSM_MAMBA2, KDA = KIND == SKSSM_KDA;
     constexpr bool BF = std::is_same<QT, Bf16Tag>::value;
     typedef WalkLds<KIND, QT, NW> L;
-    constexpr bool FORMP = kFormP<KIND, QT>;
+    constexpr bool FORMP = kFormP<KIND, QT>, OUT = !ENDS;
     typedef Record R;
     constexpr int TERMS = L::terms;
     extern __shared__ __align__(16) char lds[];
     const int w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);  // the same in every lane
     const int lane = threadIdx.x & 63, lr = lane & 15, lq = lane >> 4;
     const int per = (A.H + 7) / 8;
-    const int slices = V / (16 * NW);
+    const int vslices = V / (16 * NW), slices = vslices + (ENDS && DELTA ? (kK / 16 + NW - 1) / NW : 0);
     const int xcd = blockIdx.x & 7;
     int rest = blockIdx.x >> 3;
     const int slice = rest % slices;
     rest /= slices;
     const int h = head_of(A, xcd, rest % per);
     if (h >= A.H) return;
-    const int hk = h / A.share, seq = seq_of_rank(A, rest / per, lane);
-    const SeqSpan sp = seq_span_uniform(A, seq);
+    rest /= per;
+    const int seg = SG.len ? rest % SG.most : 0;
+    if (SG.len) rest /= SG.most;
+    const int hk = h / A.share, seq = seq_of_rank(A, rest, lane);
+    SeqSpan sp = seq_span_uniform(A, seq);
     if (!sp.live) return;
+    // the segment's part of the sequence
+    const int seq_t0 = sp.t0;
+    bool at_end = true;
+    int n = 1;
+    if (SG.len) {
+        n = max(1, (sp.len + SG.len - 1) / SG.len);
+        at_end = seg == n - 1;
+        if (ENDS ? seg >= n - 1 : seg >= n) return;
+        sp.t0 += seg * SG.len;
+        sp.len = min(SG.len, sp.len - seg * SG.len);
+    }
+    const bool is_m = ENDS && slice >= vslices;  // columns of M
+    if (is_m && seg == 0) return;                // the first segment starts from the sequence's own state
+    const int mcol = 16 * ((slice - vslices) * NW + w) + lr;
     const int col = 16 * (slice * NW + w) + lr;
 
     // the state: tile 2 s + o, register r <-> channel 32 s + 8 lq + 4 o + r
     f32x4 S[8];
     const int svo = (8 * lq * V + col) * 4;
-    if (sp.row0 >= 0) {
-        const __amdgpu_buffer_rsrc_t s0 = buffer_rsrc(A.S0 + (size_t(sp.row0) * A.H + h) * (kK * V), kK * V * 4);
+    // (the last segment's state may take S0's place while the first one starts: it starts from a copy)
+    if (seg > 0 ? !ENDS : sp.row0 >= 0) {
+        const float* from = !ENDS && n > 1 ? SG.n_of(seq_t0, seq, seg > 0 ? seg - 1 : n - 1, A.H, h, V)
+                                           : A.S0 + (size_t(sp.row0) * A.H + h) * (kK * V);
+        const __amdgpu_buffer_rsrc_t s0 = buffer_rsrc(from, kK * V * 4);
 #pragma unroll
         for (int t = 0; t < 8; ++t)
 #pragma unroll
@@ -498,7 +538,18 @@ void walk_kernel(RaggedArgs A, const char* ws, long slots, int V) {
                 S[t][r] = buffer_load_f32(s0, svo, (32 * (t >> 1) + 4 * (t & 1) + r) * V * 4);
     } else {
 #pragma unroll
-        for (int t = 0; t < 8; ++t) S[t] = f32x4{0.f, 0.f, 0.f, 0.f};
+        for (int t = 0; t < 8; ++t)
+#pragma unroll
+            for (int r = 0; r < 4; ++r)
+                S[t][r] = is_m && 32 * (t >> 1) + 8 * lq + 4 * (t & 1) + r == mcol ? 1.f : 0.f;
+    }
+    if (ENDS && seg == 0) {
+        const __amdgpu_buffer_rsrc_t s0 = buffer_rsrc(SG.n_of(seq_t0, seq, n - 1, A.H, h, V), kK * V * 4);
+#pragma unroll
+        for (int t = 0; t < 8; ++t)
+#pragma unroll
+            for (int r = 0; r < 4; ++r)
+                buffer_store_f32(S[t][r], s0, svo, (32 * (t >> 1) + 4 * (t & 1) + r) * V * 4);
     }
 
     // ---- where a chunk's data come from ----
@@ -508,13 +559,16 @@ void walk_kernel(RaggedArgs A, const char* ws, long slots, int V) {
     Cursor<kC> cv(A.v, sp.t0, A.H, h, vrow), cy(A.y, sp.t0, A.H, h, uint32_t(V) * 4);
     Cursor<kC> ca(A.a, sp.t0, A.H, h, kK * 4);  // KDA
     constexpr int RB = FORMP ? DecayRecord::bytes : R::bytes;
-    uint64_t crec = reinterpret_cast<uint64_t>(ws) + (first_slot<kC>(sp.t0, seq) * A.H + h) * RB;
+    const long slot0 = first_slot<kC>(seq_t0, seq) + (sp.t0 - seq_t0) / kC;
+    uint64_t crec = reinterpret_cast<uint64_t>(ws) + (slot0 * A.H + h) * RB;
 
     // Pieces of 1 KB, on their way from memory to LDS through a wave's registers:
     // those of the record, piece w + j NW by wave w; of the block's value columns; and
     // (one term) 16 of keys and queries, four rows each, granules swizzled.
-    constexpr int NKQ = TERMS == 1 ? (16 + NW - 1) / NW : 0, NVP = BF ? 1 : 2;
-    constexpr int NR = R::bytes / kFrag, NRW = FORMP ? 1 : (NR + NW - 1) / NW;
+    constexpr int KQP = OUT ? 16 : 8;                 // without outputs no queries
+    constexpr int RAT = OUT ? 0 : R::t;               // and no P
+    constexpr int NKQ = TERMS == 1 ? (KQP + NW - 1) / NW : 0, NVP = BF ? 1 : 2;
+    constexpr int NR = (R::bytes - RAT) / kFrag, NRW = FORMP ? 1 : (NR + NW - 1) / NW;
     constexpr int NP = NKQ + NRW + NVP;
     u32x4 st[NP];
     int kqoff[NKQ ? NKQ : 1], voff[NVP];
@@ -537,7 +591,7 @@ void walk_kernel(RaggedArgs A, const char* ws, long slots, int V) {
             ck.next();
             cq.next();
         }
-        rsv = cv.rsrc(rows);
+        rsv = cv.rsrc(is_m ? 0 : rows);  // M takes no values
         cv.next();
         rsr = buffer_rsrc(reinterpret_cast<const void*>(crec), rows > 0 ? RB : 0);
         crec += uint64_t(A.H) * RB;
@@ -546,19 +600,19 @@ void walk_kernel(RaggedArgs A, const char* ws, long slots, int V) {
         if (j < NKQ) st[j] = load16(w + j * NW < 8 ? rsk : rsq, kqoff[j]);
         else if (j >= NKQ + NRW) st[j] = load16(rsv, voff[j - NKQ - NRW]);
         else if (FORMP) st[j] = load16(rsr, DecayRecord::g + (lane & 15) * 16);
-        else st[j] = load16(rsr, (w + (j - NKQ) * NW) * kFrag + lane * 16);
+        else st[j] = load16(rsr, RAT + (w + (j - NKQ) * NW) * kFrag + lane * 16);
     };
     auto put = [&](int j, char* kq, char* v, char* rec) {
         const int o = lane * 16;
         if (j < NKQ) {
-            if ((j + 1) * NW <= 16 || w + j * NW < 16) *reinterpret_cast<u32x4*>(kq + (w + j * NW) * kFrag + o) = st[j];
+            if ((j + 1) * NW <= KQP || w + j * NW < KQP) *reinterpret_cast<u32x4*>(kq + (w + j * NW) * kFrag + o) = st[j];
         } else if (j >= NKQ + NRW) {
             *reinterpret_cast<u32x4*>(v + (w + (j - NKQ - NRW) * NW) * kFrag + o) = st[j];
         } else if (FORMP) {
             if (w == 0 && lane < 16) *reinterpret_cast<u32x4*>(rec + L::g + o) = st[j];
         } else {
             const int i = w + (j - NKQ) * NW;
-            if ((j - NKQ + 1) * NW <= NR || i < NR) *reinterpret_cast<u32x4*>(rec + i * kFrag + o) = st[j];
+            if ((j - NKQ + 1) * NW <= NR || i < NR) *reinterpret_cast<u32x4*>(rec + RAT + i * kFrag + o) = st[j];
         }
     };
 
@@ -566,7 +620,7 @@ void walk_kernel(RaggedArgs A, const char* ws, long slots, int V) {
     // Waves 0 .. 3 take a task each: 16 x 16 values, lane = row tile_row(m, lr) and
     // columns 4 b .. 4 b + 3 with b = 2 lq + o; the decays between follow from F.
     uint64_t cqk = reinterpret_cast<uint64_t>(ws) + uint64_t(slots) * A.H * DecayRecord::bytes +
-                   (first_slot<kC>(sp.t0, seq) * A.Hk + hk) * DecayRecord::qk;
+                   (slot0 * A.Hk + hk) * DecayRecord::qk;
     f32x4 qk = {0.f, 0.f, 0.f, 0.f}, a4 = qk;
     float f0 = 0.f;
     const int pm = (w >> 1) & 1, po = w & 1, prow = tile_row(pm, lr), pb = 2 * lq + po;
@@ -614,7 +668,7 @@ void walk_kernel(RaggedArgs A, const char* ws, long slots, int V) {
             for (int i = 0; i < 4; ++i) {
                 const int t = 4 * (w + n * NW) + i;  // beyond the chunk where NW does not divide 8: not used
                 kin[n][i] = load_pair(rk, t * int(ck.stride) + lane * 2 * E);
-                qin[n][i] = load_pair(rq, t * int(cq.stride) + lane * 2 * E);
+                if (OUT) qin[n][i] = load_pair(rq, t * int(cq.stride) + lane * 2 * E);
                 if (KDA)
                     ain[n][i] = __builtin_bit_cast(
                         f32x2, __builtin_amdgcn_raw_buffer_load_b64(ra, t * int(ca.stride) + lane * 8, 0, 0));
@@ -677,9 +731,12 @@ void walk_kernel(RaggedArgs A, const char* ws, long slots, int V) {
 #pragma unroll
                     for (int e = 0; e < 3; ++e) *reinterpret_cast<uint32_t*>(dst + e * kPlane) = u[e][0];
                 };
-                const f32x2 kx = unpack(kin[n][i]), qx = unpack(qin[n][i]);
+                const f32x2 kx = unpack(kin[n][i]);
                 three(at, KDA ? kx * pre[i] : kx);
-                three(at + L::q, KDA ? qx * pre[i] : qx);
+                if (OUT) {
+                    const f32x2 qx = unpack(qin[n][i]);
+                    three(at + L::q, KDA ? qx * pre[i] : qx);
+                }
                 if (KDA) three(at + L::kd, kx * suf[i]);
             }
         }
@@ -705,12 +762,13 @@ void walk_kernel(RaggedArgs A, const char* ws, long slots, int V) {
         return split8(f);
     };
 
+    float through = 1.f;  // Mamba-2's M
     int left = sp.len;  // tokens from chunk c on
     if (left > 0) {
         aim(left);
 #pragma unroll
         for (int j = 0; j < NP; ++j) fetch(j);
-        if (FORMP) {
+        if (FORMP && OUT) {
             load_p(left);
             if (w < 4) put_p(lds + L::rec + L::p);
         }
@@ -728,7 +786,7 @@ void walk_kernel(RaggedArgs A, const char* ws, long slots, int V) {
         aim(left - kC);
 #pragma unroll
         for (int j = 0; j < NP; ++j) fetch(j);
-        if (FORMP) load_p(left - kC);
+        if (FORMP && OUT) load_p(left - kC);
         Split sb = split_state(0);
         for (int c = 0; left > 0; ++c) {
             __syncthreads();  // everything of chunk c is there, and nobody reads chunk c - 1 any more
@@ -754,7 +812,7 @@ void walk_kernel(RaggedArgs A, const char* ws, long slots, int V) {
                     for (int e = 0; e < TERMS; ++e) {
                         const char* p = keys + (ra[m] ^ (64 * s)) + e * kPlane;
                         if (DELTA) ka[s % AB][m][e] = *reinterpret_cast<const u32x4*>(p);
-                        qa[s % AB][m][e] = *reinterpret_cast<const u32x4*>(p + L::q);
+                        if (OUT) qa[s % AB][m][e] = *reinterpret_cast<const u32x4*>(p + L::q);
                     }
             };
             auto read_tri = [&](const char* f) {
@@ -802,14 +860,14 @@ void walk_kernel(RaggedArgs A, const char* ws, long slots, int V) {
                     fetch(j);
                 }
                 Split nb;
-                if (s < 3) nb = split_state(s + 1);
+                if (s < 3 && (DELTA || OUT)) nb = split_state(s + 1);
                 if constexpr (TERMS == 1) {
 #pragma unroll
                     for (int e = 2; e >= 0; --e)
 #pragma unroll
                         for (int m = 0; m < 2; ++m) {
                             if (DELTA) X[m] = mfma_bf16(ka[s % AB][m][0], sb.t[e], X[m]);
-                            Y[m] = mfma_bf16(qa[s % AB][m][0], sb.t[e], Y[m]);
+                            if (OUT) Y[m] = mfma_bf16(qa[s % AB][m][0], sb.t[e], Y[m]);
                         }
                 } else {
 #pragma unroll
@@ -817,27 +875,27 @@ void walk_kernel(RaggedArgs A, const char* ws, long slots, int V) {
 #pragma unroll
                         for (int m = 0; m < 2; ++m) {
                             if (DELTA) X[m] = mfma_bf16(ka[s % AB][m][kTermA[e]], sb.t[kTermB[e]], X[m]);
-                            Y[m] = mfma_bf16(qa[s % AB][m][kTermA[e]], sb.t[kTermB[e]], Y[m]);
+                            if (OUT) Y[m] = mfma_bf16(qa[s % AB][m][kTermA[e]], sb.t[kTermB[e]], Y[m]);
                         }
                     if (s < 3) read_rows(s + 1);
                 }
                 if (s < 3) {
-                    sb = nb;
+                    if (DELTA || OUT) sb = nb;
                 } else if constexpr (BF && !FORMP) {
                     unpack_values();
                 }
                 if (TERMS == 1) {
                     __builtin_amdgcn_sched_group_barrier(0x100, 11, 0);
 #pragma unroll
-                    for (int i = 0; i < (DELTA ? 12 : 6); ++i) {
+                    for (int i = 0; i < (DELTA && OUT ? 12 : 6); ++i) {
                         __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);
-                        __builtin_amdgcn_sched_group_barrier(0x002, DELTA ? 4 : 8, 0);
+                        __builtin_amdgcn_sched_group_barrier(0x002, DELTA && OUT ? 4 : 8, 0);
                     }
                 } else {
 #pragma unroll
-                    for (int i = 0; i < (DELTA ? 24 : 12); ++i) {
+                    for (int i = 0; i < (DELTA && OUT ? 24 : 12); ++i) {
                         __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);
-                        __builtin_amdgcn_sched_group_barrier(0x002, DELTA ? 2 : 4, 0);
+                        __builtin_amdgcn_sched_group_barrier(0x002, DELTA && OUT ? 2 : 4, 0);
                     }
                 }
                 __builtin_amdgcn_sched_barrier(0);
@@ -878,8 +936,9 @@ void walk_kernel(RaggedArgs A, const char* ws, long slots, int V) {
 #pragma unroll
                 for (int i = 0; i < 8; ++i) {
                     S[i] *= gC;
-                    Y[i / 4][i & 3] *= g[i];
+                    if (OUT) Y[i / 4][i & 3] *= g[i];
                 }
+                if (ENDS && !DELTA) through *= gC;
             }
             if (DELTA) {
 #pragma unroll
@@ -906,8 +965,8 @@ void walk_kernel(RaggedArgs A, const char* ws, long slots, int V) {
 #pragma unroll
             for (int s = 0; s < 4; ++s) {
                 if (s < 3) read_kt(s + 1);
-                if (s == (FORMP ? 3 : 2)) read_tri(pf);
-                if (!KDA && !FORMP) {
+                if (OUT && s == (FORMP ? 3 : 2)) read_tri(pf);
+                if (OUT && !KDA && !FORMP) {
                     uint32_t u[3][1];
                     split3<1>(wt + 2 * s, u);
 #pragma unroll
@@ -935,8 +994,9 @@ void walk_kernel(RaggedArgs A, const char* ws, long slots, int V) {
             }
             if (KDA) wb = rb;
             // y = gamma Y + P w, beside the next chunk's first split
-            sb = split_state(0);
-            if constexpr (FORMP) {  // w is v itself, an exact operand
+            if (DELTA || OUT) sb = split_state(0);
+            if constexpr (ENDS) {
+            } else if constexpr (FORMP) {  // w is v itself, an exact operand
 #pragma unroll
                 for (int e = 2; e >= 0; --e)
 #pragma unroll
@@ -953,14 +1013,14 @@ void walk_kernel(RaggedArgs A, const char* ws, long slots, int V) {
                 __builtin_amdgcn_sched_group_barrier(0x002, FORMP ? 8 : 4, 0);
             }
             __builtin_amdgcn_sched_barrier(0);
-            {
+            if (OUT) {
                 const __amdgpu_buffer_rsrc_t rs = cy.rsrc(left);
                 const int at = 8 * lq * int(cy.stride) + col * 4;
 #pragma unroll
                 for (int i = 0; i < 8; ++i) buffer_store_f32(Y[i / 4][i & 3], rs, at + i * int(cy.stride), 0);
                 cy.next();
             }
-            if (FORMP) {  // P of the next chunk
+            if (FORMP && OUT) {  // P of the next chunk
                 if (w < 4) put_p(lds + L::rec + (cur ^ 1) * L::recbuf + L::p);
                 load_p(left - 2 * kC);
             }
@@ -973,39 +1033,117 @@ void walk_kernel(RaggedArgs A, const char* ws, long slots, int V) {
             left -= kC;
         }
     }
-    const __amdgpu_buffer_rsrc_t so = buffer_rsrc(A.S + (size_t(sp.row) * A.H + h) * (kK * V), kK * V * 4);
+    // the last state
+    if (ENDS ? is_m && mcol >= kK : !at_end) return;
+    const int cols = is_m ? kK : V;
+    float* to = !ENDS ? A.S + (size_t(sp.row) * A.H + h) * (kK * V)
+                      : SG.n_of(seq_t0, seq, seg, A.H, h, V) + (is_m ? kK * V : 0);
+    if (ENDS && !DELTA && slice == 0 && threadIdx.x == 0) to[kK * V] = through;
+    const __amdgpu_buffer_rsrc_t so = buffer_rsrc(to, kK * cols * 4);
+    const int wo = (8 * lq * cols + (is_m ? mcol : col)) * 4;
 #pragma unroll
     for (int t = 0; t < 8; ++t)
 #pragma unroll
-        for (int r = 0; r < 4; ++r) buffer_store_f32(S[t][r], so, svo, (32 * (t >> 1) + 4 * (t & 1) + r) * V * 4);
+        for (int r = 0; r < 4; ++r) buffer_store_f32(S[t][r], so, wo, (32 * (t >> 1) + 4 * (t & 1) + r) * cols * 4);
+}
+
+// The state at the end of each segment in turn: S_g = N_g + M_g S_{g-1}.  A block has
+// 16 value columns of one head, the state in LDS; wave w forms rows 32 w ..
+// 32 w + 31 with the fp32 matrix instruction.
+template <bool DELTA>
+__global__ __launch_bounds__(256) void join_kernel(RaggedArgs A, int V, Segments SG) {
+    constexpr int SS = 16 + 1;
+    __shared__ float st[kK * SS];
+    const int w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int lane = threadIdx.x & 63, lr = lane & 15, lq = lane >> 4;
+    const int slices = V / 16;
+    int rest = blockIdx.x;
+    const int slice = rest % slices;
+    rest /= slices;
+    const int h = rest % A.H, seq = rest / A.H;
+    const SeqSpan sp = seq_span_uniform(A, seq);
+    if (!sp.live) return;
+    const int n = (sp.len + SG.len - 1) / SG.len;
+    const int col = 16 * slice + lr, row = 32 * w + 4 * lq;  // rows row + 16 o + r
+    f32x4 c[2];
+    for (int g = 0; g < n - 1; ++g) {
+        float* at = SG.n_of(sp.t0, seq, g, A.H, h, V);
+        if (!DELTA) {
+            const float m = at[kK * V];
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                float* p = at + (row + 16 * (i / 4) + (i & 3)) * V + col;
+                c[i / 4][i & 3] = g ? fmaf(m, c[i / 4][i & 3], *p) : *p;
+                if (g) *p = c[i / 4][i & 3];
+            }
+            continue;
+        }
+#pragma unroll
+        for (int i = 0; i < 8; ++i) c[i / 4][i & 3] = at[(row + 16 * (i / 4) + (i & 3)) * V + col];
+        if (g) {
+            const float* m = at + kK * V + (32 * w + lr) * kK + 32 * lq;  // lane's channels 32 lq + s
+            f32x4 ma[2][8];
+#pragma unroll
+            for (int o = 0; o < 2; ++o)
+#pragma unroll
+                for (int s = 0; s < 8; ++s) ma[o][s] = *reinterpret_cast<const f32x4*>(m + 16 * o * kK + 4 * s);
+#pragma unroll
+            for (int s = 0; s < 32; ++s) {
+                const float b = st[(32 * lq + s) * SS + lr];
+#pragma unroll
+                for (int o = 0; o < 2; ++o) c[o] = mfma_16x16x4(ma[o][s / 4][s & 3], b, c[o]);
+            }
+#pragma unroll
+            for (int i = 0; i < 8; ++i) at[(row + 16 * (i / 4) + (i & 3)) * V + col] = c[i / 4][i & 3];
+        }
+        __syncthreads();
+#pragma unroll
+        for (int i = 0; i < 8; ++i) st[(row + 16 * (i / 4) + (i & 3)) * SS + lr] = c[i / 4][i & 3];
+        __syncthreads();
+    }
 }
 
 namespace {
 
-template <int KIND, typename QT, int NW>
-hipError_t launch_walk_t(const RaggedArgs& a, const char* ws, int V, hipStream_t s) {
+template <int KIND, typename QT, int NW, bool ENDS>
+hipError_t launch_walk_t(const RaggedArgs& a, const char* ws, int V, const Segments& sg, hipStream_t s) {
     const long slots = prefill_slots<kC>(a.total, a.n_seqs);
     constexpr int lds = WalkLds<KIND, QT, NW>::bytes;
     static_assert(lds <= 160 * 1024, "LDS of a CU");
     if (lds > 64 * 1024) {
-        const hipError_t e = hipFuncSetAttribute(reinterpret_cast<const void*>(walk_kernel<KIND, QT, NW>),
+        const hipError_t e = hipFuncSetAttribute(reinterpret_cast<const void*>(walk_kernel<KIND, QT, NW, ENDS>),
                                                  hipFuncAttributeMaxDynamicSharedMemorySize, lds);
         if (e != hipSuccess) return e;
     }
-    const long blocks = long(a.n_seqs) * ((a.H + 7) / 8) * 8 * (V / (16 * NW));
+    const int slices = V / (16 * NW) + (ENDS && KIND != SKSSM_MAMBA2 ? (kK / 16 + NW - 1) / NW : 0);
+    const long blocks = long(a.n_seqs) * (sg.len ? sg.most : 1) * ((a.H + 7) / 8) * 8 * slices;
     if (blocks >= (1l << 31)) return hipErrorInvalidConfiguration;
-    hipLaunchKernelGGL((walk_kernel<KIND, QT, NW>), dim3(uint32_t(blocks)), dim3(NW * 64), lds, s, a, ws, slots, V);
+    hipLaunchKernelGGL((walk_kernel<KIND, QT, NW, ENDS>), dim3(uint32_t(blocks)), dim3(NW * 64), lds, s, a, ws, slots, V,
+                       sg);
     return hipGetLastError();
 }
 
+template <int KIND, typename QT, int NW>
+hipError_t launch_walk_n(const RaggedArgs& a, const char* ws, int V, const Segments& sg, hipStream_t s) {
+    if (sg.len) {
+        hipError_t e = launch_walk_t<KIND, QT, NW, true>(a, ws, V, sg, s);
+        if (e != hipSuccess) return e;
+        const long blocks = long(a.n_seqs) * a.H * (V / 16);  // at most 8 x 4096
+        hipLaunchKernelGGL((join_kernel<KIND != SKSSM_MAMBA2>), dim3(uint32_t(blocks)), dim3(256), 0, s, a, V, sg);
+        e = hipGetLastError();
+        if (e != hipSuccess) return e;
+    }
+    return launch_walk_t<KIND, QT, NW, false>(a, ws, V, sg, s);
+}
+
 template <int KIND, typename QT>
-hipError_t launch_walk_v(const RaggedArgs& a, const char* ws, int V, hipStream_t s) {
+hipError_t launch_walk_v(const RaggedArgs& a, const char* ws, int V, const Segments& sg, hipStream_t s) {
     switch (V) {
-        case 64: return launch_walk_t<KIND, QT, 4>(a, ws, V, s);
-        case 80: return launch_walk_t<KIND, QT, 5>(a, ws, V, s);
-        case 96: return launch_walk_t<KIND, QT, 6>(a, ws, V, s);
-        case 112: return launch_walk_t<KIND, QT, 7>(a, ws, V, s);
-        case 128: return launch_walk_t<KIND, QT, 4>(a, ws, V, s);
+        case 64: return launch_walk_n<KIND, QT, 4>(a, ws, V, sg, s);
+        case 80: return launch_walk_n<KIND, QT, 5>(a, ws, V, sg, s);
+        case 96: return launch_walk_n<KIND, QT, 6>(a, ws, V, sg, s);
+        case 112: return launch_walk_n<KIND, QT, 7>(a, ws, V, sg, s);
+        case 128: return launch_walk_n<KIND, QT, 4>(a, ws, V, sg, s);
     }
     return hipErrorInvalidValue;
 }
@@ -1027,24 +1165,62 @@ hipError_t launch_prep(int kind, const RaggedArgs& a, char* ws, hipStream_t s) {
 
 }  // namespace
 
-size_t walk_workspace(const sketchssm_shape& sh, long n_seqs, long total) {
+namespace {
+
+size_t record_bytes(const sketchssm_shape& sh, long n_seqs, long total) {
     const size_t slots = prefill_slots<kC>(total, n_seqs);
+    size_t n = slots * sh.H * Record::bytes;
     if (sh.kind == SKSSM_MAMBA2 && sh.qkv == SKSSM_BF16)
-        return slots * (size_t(sh.H) * DecayRecord::bytes + size_t(kq_heads_of(sh)) * DecayRecord::qk);
-    return slots * sh.H * Record::bytes;
+        n = slots * (size_t(sh.H) * DecayRecord::bytes + size_t(kq_heads_of(sh)) * DecayRecord::qk);
+    return (n + 255) / 256 * 256;
+}
+
+// Whether and how long sequences are cut: so that the walk has a block for each of
+// the 256 CUs, in segments of 256 tokens or more, where that is worth the second
+// pass.  One sequence, us without and with: GDN, 32 heads of 128, 4 segments: 4096
+// tokens 251, 181 and 1024 tokens 75, 76; 64 heads, 2 segments: 4096 tokens 285, 270
+// and 1024 tokens 79, 83; more segments than CUs need (64 heads, 4): 285, 298.
+// Mamba-2, 16 heads of 64, 4096 tokens, 16 segments: 233, 76.
+Segments segments_of(const sketchssm_shape& sh, long n_seqs, long total, long max_len) {
+    Segments sg = {0, 1, nullptr};
+    const int nw = sh.V == 128 ? 4 : sh.V / 16;
+    const long len = std::min(max_len, total), per_seq = long(sh.H) * (sh.V / (16 * nw));
+    if (len <= 0) return sg;
+    const long blocks = (total + len - 1) / len * per_seq;  // as though the longest were all
+    const long count = std::min(256 / blocks, len / 256);
+    if (count < 2 || count * len < 4096) return sg;
+    if (n_seqs * per_seq * count > 4096) return sg;  // among many short ones most blocks would have no segment
+    sg.len = int((len + count - 1) / count + kC - 1) / kC * kC;
+    sg.most = int((len + sg.len - 1) / sg.len);
+    return sg;
+}
+
+size_t segment_bytes(const sketchssm_shape& sh, const Segments& sg, long n_seqs, long total) {
+    return sg.len ? size_t(total / sg.len + n_seqs) * sh.H * (kK * sh.V + kK * kK) * 4 : 0;
+}
+
+}  // namespace
+
+size_t walk_workspace(const sketchssm_shape& sh, long n_seqs, long total, long max_len) {
+    return record_bytes(sh, n_seqs, total) + segment_bytes(sh, segments_of(sh, n_seqs, total, max_len), n_seqs, total);
 }
 
 hipError_t launch_walk(const sketchssm_shape& sh, const RaggedArgs& a, char* ws, hipStream_t s) {
     const bool bf = sh.qkv == SKSSM_BF16;
     const hipError_t e = bf ? launch_prep<Bf16Tag>(sh.kind, a, ws, s) : launch_prep<F32Tag>(sh.kind, a, ws, s);
     if (e != hipSuccess) return e;
+    Segments sg = segments_of(sh, a.n_seqs, a.total, a.max_len);
+    sg.ends = ws + record_bytes(sh, a.n_seqs, a.total);
     switch (sh.kind) {
         case SKSSM_MAMBA2:
-            return bf ? launch_walk_v<SKSSM_MAMBA2, Bf16Tag>(a, ws, sh.V, s) : launch_walk_v<SKSSM_MAMBA2, F32Tag>(a, ws, sh.V, s);
+            return bf ? launch_walk_v<SKSSM_MAMBA2, Bf16Tag>(a, ws, sh.V, sg, s)
+                      : launch_walk_v<SKSSM_MAMBA2, F32Tag>(a, ws, sh.V, sg, s);
         case SKSSM_GDN:
-            return bf ? launch_walk_v<SKSSM_GDN, Bf16Tag>(a, ws, sh.V, s) : launch_walk_v<SKSSM_GDN, F32Tag>(a, ws, sh.V, s);
+            return bf ? launch_walk_v<SKSSM_GDN, Bf16Tag>(a, ws, sh.V, sg, s)
+                      : launch_walk_v<SKSSM_GDN, F32Tag>(a, ws, sh.V, sg, s);
         case SKSSM_KDA:
-            return bf ? launch_walk_v<SKSSM_KDA, Bf16Tag>(a, ws, sh.V, s) : launch_walk_v<SKSSM_KDA, F32Tag>(a, ws, sh.V, s);
+            return bf ? launch_walk_v<SKSSM_KDA, Bf16Tag>(a, ws, sh.V, sg, s)
+                      : launch_walk_v<SKSSM_KDA, F32Tag>(a, ws, sh.V, sg, s);
     }
     return hipErrorInvalidValue;
 }
