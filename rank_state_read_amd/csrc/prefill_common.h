@@ -176,9 +176,12 @@ __device__ __forceinline__ u32x2 tr_read(const char* p) {
 }
 
 // The heads' order over the blocks: those that share a key head sit on one XCD
-// (blocks go round the eight by index).  Head of unit u of XCD x, or >= H.
+// (blocks go round the eight by index).  First head of unit u of XCD x, a unit being
+// HB heads of one key head, or >= H.
+template <int HB>
 __device__ __forceinline__ int head_of(const RaggedArgs& A, int x, int u) {
-    return A.Hk % 8 == 0 ? (x + 8 * (u / A.share)) * A.share + u % A.share : x + 8 * u;
+    const int share = A.share / HB;
+    return HB * (A.Hk % 8 == 0 ? (x + 8 * (u / share)) * share + u % share : x + 8 * u);
 }
 
 // The chunked form's launches (prefill_walk.hip).

@@ -460,47 +460,49 @@ struct Segments {
 //   three terms: one buffer of planes and two barriers, between which the waves
 //                form the next chunk's planes from inputs already in registers.
 // ---------------------------------------------------------------------------
-template <int KIND, typename QT, int NW>
+template <int KIND, typename QT, int NW, int HB>
 struct WalkLds {  // bytes
     static constexpr bool bf = std::is_same<QT, Bf16Tag>::value, kda = KIND == SKSSM_KDA;
     static constexpr int terms = bf && !kda ? 1 : 3;
-    static constexpr int v = NW * kFrag * (bf ? 1 : 2);        // a chunk's values [C][16 NW]
+    static constexpr int v = NW * kFrag * (bf ? 1 : 2);        // a chunk's values of a head [C][16 NW]
     static constexpr int q = terms * kPlane;                   // queries' planes behind the keys'
     static constexpr int kd = 2 * terms * kPlane;              // KDA: sigma K
     static constexpr int kqbuf = (kda ? 3 : 2) * terms * kPlane;
     static constexpr int kq = 0;
     static constexpr int vals = kq + (terms == 1 ? 2 : 1) * kqbuf;
-    static constexpr int rec = vals + 2 * v;                   // P, (T,) gamma and sigma of two chunks
+    static constexpr int rec = vals + 2 * HB * v;                  // P, (T,) gamma and sigma of two chunks
     static constexpr int p = 0, t = kTri;
     static constexpr int g = (kFormP<KIND, QT> ? 1 : 2) * kTri;
     static constexpr int recbuf = kFormP<KIND, QT> ? g + 2 * kC * 4 : Record::bytes;
-    static constexpr int gp = rec + 2 * recbuf;                // KDA: decays' products of token groups [8][K],
+    static constexpr int gp = rec + 2 * HB * recbuf;               // KDA: decays' products of token groups [8][K],
     static constexpr int gc = gp + (kda ? 8 * kK * 4 : 0);     // of the chunk [K]
     static constexpr int bytes = gc + (kda ? kK * 4 : 0);
 };
 
-// ENDS: M and N of segments, no outputs.  The columns of M follow those of N.
-template <int KIND, typename QT, int NW, bool ENDS>
-__global__ __launch_bounds__(NW * 64)
+// HB heads of a key head to a block, NW waves each.  ENDS: M and N of segments, no outputs.  The columns of M follow those of N.
+template <int KIND, typename QT, int NW, int HB, bool ENDS>
+__global__ __launch_bounds__(HB * NW * 64)
 __attribute__((amdgpu_waves_per_eu(kFormP<KIND, QT> ? 3 : 2)))
 void walk_kernel(RaggedArgs A, const char* ws, long slots, int V, Segments SG) {
     constexpr bool DELTA = KIND != SKSSM_MAMBA2, KDA = KIND == SKSSM_KDA;
     constexpr bool BF = std::is_same<QT, Bf16Tag>::value;
-    typedef WalkLds<KIND, QT, NW> L;
+    typedef WalkLds<KIND, QT, NW, HB> L;
+    constexpr int NT = HB * NW;
     constexpr bool FORMP = kFormP<KIND, QT>, OUT = !ENDS;
     typedef Record R;
     constexpr int TERMS = L::terms;
     extern __shared__ __align__(16) char lds[];
-    const int w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);  // the same in every lane
+    const int bw = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);  // the same in every lane
+    const int w = bw % NW, hb = bw / NW;                              // column tile and head in the block
     const int lane = threadIdx.x & 63, lr = lane & 15, lq = lane >> 4;
-    const int per = (A.H + 7) / 8;
+    const int per = (A.H / HB + 7) / 8;
     const int vslices = V / (16 * NW), slices = vslices + (ENDS && DELTA ? (kK / 16 + NW - 1) / NW : 0);
     const int xcd = blockIdx.x & 7;
     int rest = blockIdx.x >> 3;
     const int slice = rest % slices;
     rest /= slices;
-    const int h = head_of(A, xcd, rest % per);
-    if (h >= A.H) return;
+    const int h = head_of<HB>(A, xcd, rest % per) + hb;
+    if (h >= A.H) return;  // of all the block's heads, or none
     rest /= per;
     const int seg = SG.len ? rest % SG.most : 0;
     if (SG.len) rest /= SG.most;
@@ -555,6 +557,8 @@ void walk_kernel(RaggedArgs A, const char* ws, long slots, int V, Segments SG) {
     // ---- where a chunk's data come from ----
     constexpr int E = Vec8<QT>::kElemBytes;
     const uint32_t krow = kK * E, vrow = uint32_t(V) * E;
+    char* const my_vals = lds + L::vals + hb * 2 * L::v;
+    char* const my_rec = lds + L::rec + hb * 2 * L::recbuf;
     Cursor<kC> ck(A.k, sp.t0, A.Hk, hk, krow), cq(A.q, sp.t0, A.Hk, hk, krow);
     Cursor<kC> cv(A.v, sp.t0, A.H, h, vrow), cy(A.y, sp.t0, A.H, h, uint32_t(V) * 4);
     Cursor<kC> ca(A.a, sp.t0, A.H, h, kK * 4);  // KDA
@@ -563,18 +567,18 @@ void walk_kernel(RaggedArgs A, const char* ws, long slots, int V, Segments SG) {
     uint64_t crec = reinterpret_cast<uint64_t>(ws) + (slot0 * A.H + h) * RB;
 
     // Pieces of 1 KB, on their way from memory to LDS through a wave's registers:
-    // those of the record, piece w + j NW by wave w; of the block's value columns; and
+    // those of a head's record, piece w + j NW by its wave w; of its value columns; and
     // (one term) 16 of keys and queries, four rows each, granules swizzled.
     constexpr int KQP = OUT ? 16 : 8;                 // without outputs no queries
     constexpr int RAT = OUT ? 0 : R::t;               // and no P
-    constexpr int NKQ = TERMS == 1 ? (KQP + NW - 1) / NW : 0, NVP = BF ? 1 : 2;
+    constexpr int NKQ = TERMS == 1 ? (KQP + NT - 1) / NT : 0, NVP = BF ? 1 : 2;
     constexpr int NR = (R::bytes - RAT) / kFrag, NRW = FORMP ? 1 : (NR + NW - 1) / NW;
     constexpr int NP = NKQ + NRW + NVP;
     u32x4 st[NP];
     int kqoff[NKQ ? NKQ : 1], voff[NVP];
 #pragma unroll
     for (int j = 0; j < NKQ; ++j) {
-        const int r = 4 * ((w + j * NW) & 7) + lq;
+        const int r = 4 * ((bw + j * NT) & 7) + lq;
         kqoff[j] = int(r * ck.stride) + (lr ^ row_swizzle(r)) * 16;
     }
 #pragma unroll
@@ -597,7 +601,7 @@ void walk_kernel(RaggedArgs A, const char* ws, long slots, int V, Segments SG) {
         crec += uint64_t(A.H) * RB;
     };
     auto fetch = [&](int j) {
-        if (j < NKQ) st[j] = load16(w + j * NW < 8 ? rsk : rsq, kqoff[j]);
+        if (j < NKQ) st[j] = load16(bw + j * NT < 8 ? rsk : rsq, kqoff[j]);
         else if (j >= NKQ + NRW) st[j] = load16(rsv, voff[j - NKQ - NRW]);
         else if (FORMP) st[j] = load16(rsr, DecayRecord::g + (lane & 15) * 16);
         else st[j] = load16(rsr, RAT + (w + (j - NKQ) * NW) * kFrag + lane * 16);
@@ -605,7 +609,8 @@ void walk_kernel(RaggedArgs A, const char* ws, long slots, int V, Segments SG) {
     auto put = [&](int j, char* kq, char* v, char* rec) {
         const int o = lane * 16;
         if (j < NKQ) {
-            if ((j + 1) * NW <= KQP || w + j * NW < KQP) *reinterpret_cast<u32x4*>(kq + (w + j * NW) * kFrag + o) = st[j];
+            if ((j + 1) * NT <= KQP || bw + j * NT < KQP)
+                *reinterpret_cast<u32x4*>(kq + (bw + j * NT) * kFrag + o) = st[j];
         } else if (j >= NKQ + NRW) {
             *reinterpret_cast<u32x4*>(v + (w + (j - NKQ - NRW) * NW) * kFrag + o) = st[j];
         } else if (FORMP) {
@@ -770,7 +775,7 @@ void walk_kernel(RaggedArgs A, const char* ws, long slots, int V, Segments SG) {
         for (int j = 0; j < NP; ++j) fetch(j);
         if (FORMP && OUT) {
             load_p(left);
-            if (w < 4) put_p(lds + L::rec + L::p);
+            if (w < 4) put_p(my_rec + L::p);
         }
         if (TERMS == 3) {
             load_inputs(left);
@@ -782,7 +787,7 @@ void walk_kernel(RaggedArgs A, const char* ws, long slots, int V, Segments SG) {
             load_inputs(left - kC);
         }
 #pragma unroll
-        for (int j = 0; j < NP; ++j) put(j, lds + L::kq, lds + L::vals, lds + L::rec);
+        for (int j = 0; j < NP; ++j) put(j, lds + L::kq, my_vals, my_rec);
         aim(left - kC);
 #pragma unroll
         for (int j = 0; j < NP; ++j) fetch(j);
@@ -792,11 +797,11 @@ void walk_kernel(RaggedArgs A, const char* ws, long slots, int V, Segments SG) {
             __syncthreads();  // everything of chunk c is there, and nobody reads chunk c - 1 any more
             const int cur = c & 1;
             const char* keys = lds + L::kq + (TERMS == 1 ? cur : 0) * L::kqbuf;
-            const char* rec = lds + L::rec + cur * L::recbuf;
+            const char* rec = my_rec + cur * L::recbuf;
             const float* gam = reinterpret_cast<const float*>(rec + L::g);
             const char* pf = rec + L::p + lane * 16;
             const char* tf = rec + L::t + lane * 16;
-            const char* vals = lds + L::vals + cur * L::v;
+            const char* vals = my_vals + cur * L::v;
             aim(left - 2 * kC);
 
             // X = K S, Y = Q S: while a step's products run, the next step's state is
@@ -855,8 +860,7 @@ void walk_kernel(RaggedArgs A, const char* ws, long slots, int V, Segments SG) {
                 }
 #pragma unroll
                 for (int j = NP * s / 4; j < NP * (s + 1) / 4; ++j) {
-                    put(j, lds + L::kq + (cur ^ 1) * L::kqbuf, lds + L::vals + (cur ^ 1) * L::v,
-                        lds + L::rec + (cur ^ 1) * L::recbuf);
+                    put(j, lds + L::kq + (cur ^ 1) * L::kqbuf, my_vals + (cur ^ 1) * L::v, my_rec + (cur ^ 1) * L::recbuf);
                     fetch(j);
                 }
                 Split nb;
@@ -1021,7 +1025,7 @@ void walk_kernel(RaggedArgs A, const char* ws, long slots, int V, Segments SG) {
                 cy.next();
             }
             if (FORMP && OUT) {  // P of the next chunk
-                if (w < 4) put_p(lds + L::rec + (cur ^ 1) * L::recbuf + L::p);
+                if (w < 4) put_p(my_rec + (cur ^ 1) * L::recbuf + L::p);
                 load_p(left - 2 * kC);
             }
             if (TERMS == 3) {
@@ -1038,7 +1042,7 @@ void walk_kernel(RaggedArgs A, const char* ws, long slots, int V, Segments SG) {
     const int cols = is_m ? kK : V;
     float* to = !ENDS ? A.S + (size_t(sp.row) * A.H + h) * (kK * V)
                       : SG.n_of(seq_t0, seq, seg, A.H, h, V) + (is_m ? kK * V : 0);
-    if (ENDS && !DELTA && slice == 0 && threadIdx.x == 0) to[kK * V] = through;
+    if (ENDS && !DELTA && slice == 0 && w == 0 && lane == 0) to[kK * V] = through;
     const __amdgpu_buffer_rsrc_t so = buffer_rsrc(to, kK * cols * 4);
     const int wo = (8 * lq * cols + (is_m ? mcol : col)) * 4;
 #pragma unroll
@@ -1105,45 +1109,52 @@ __global__ __launch_bounds__(256) void join_kernel(RaggedArgs A, int V, Segments
 
 namespace {
 
-template <int KIND, typename QT, int NW, bool ENDS>
+template <int KIND, typename QT, int NW, int HB, bool ENDS>
 hipError_t launch_walk_t(const RaggedArgs& a, const char* ws, int V, const Segments& sg, hipStream_t s) {
     const long slots = prefill_slots<kC>(a.total, a.n_seqs);
-    constexpr int lds = WalkLds<KIND, QT, NW>::bytes;
+    constexpr int lds = WalkLds<KIND, QT, NW, HB>::bytes;
     static_assert(lds <= 160 * 1024, "LDS of a CU");
     if (lds > 64 * 1024) {
-        const hipError_t e = hipFuncSetAttribute(reinterpret_cast<const void*>(walk_kernel<KIND, QT, NW, ENDS>),
+        const hipError_t e = hipFuncSetAttribute(reinterpret_cast<const void*>(walk_kernel<KIND, QT, NW, HB, ENDS>),
                                                  hipFuncAttributeMaxDynamicSharedMemorySize, lds);
         if (e != hipSuccess) return e;
     }
     const int slices = V / (16 * NW) + (ENDS && KIND != SKSSM_MAMBA2 ? (kK / 16 + NW - 1) / NW : 0);
-    const long blocks = long(a.n_seqs) * (sg.len ? sg.most : 1) * ((a.H + 7) / 8) * 8 * slices;
+    const long blocks = long(a.n_seqs) * (sg.len ? sg.most : 1) * ((a.H / HB + 7) / 8) * 8 * slices;
     if (blocks >= (1l << 31)) return hipErrorInvalidConfiguration;
-    hipLaunchKernelGGL((walk_kernel<KIND, QT, NW, ENDS>), dim3(uint32_t(blocks)), dim3(NW * 64), lds, s, a, ws, slots, V,
+    hipLaunchKernelGGL((walk_kernel<KIND, QT, NW, HB, ENDS>), dim3(uint32_t(blocks)), dim3(HB * NW * 64), lds, s, a, ws, slots, V,
                        sg);
     return hipGetLastError();
 }
 
-template <int KIND, typename QT, int NW>
-hipError_t launch_walk_n(const RaggedArgs& a, const char* ws, int V, const Segments& sg, hipStream_t s) {
+template <int KIND, typename QT, int NW, int HB>
+hipError_t launch_walk_b(const RaggedArgs& a, const char* ws, int V, const Segments& sg, hipStream_t s) {
     if (sg.len) {
-        hipError_t e = launch_walk_t<KIND, QT, NW, true>(a, ws, V, sg, s);
+        hipError_t e = launch_walk_t<KIND, QT, NW, HB, true>(a, ws, V, sg, s);
         if (e != hipSuccess) return e;
         const long blocks = long(a.n_seqs) * a.H * (V / 16);  // at most 8 x 4096
         hipLaunchKernelGGL((join_kernel<KIND != SKSSM_MAMBA2>), dim3(uint32_t(blocks)), dim3(256), 0, s, a, V, sg);
         e = hipGetLastError();
         if (e != hipSuccess) return e;
     }
-    return launch_walk_t<KIND, QT, NW, false>(a, ws, V, sg, s);
+    return launch_walk_t<KIND, QT, NW, HB, false>(a, ws, V, sg, s);
+}
+
+template <int KIND, typename QT, int NW>
+hipError_t launch_walk_n(const RaggedArgs& a, const char* ws, int V, int heads, const Segments& sg, hipStream_t s) {
+    if constexpr (kFormP<KIND, QT> && (NW == 5 || NW == 6))
+        if (heads == 2) return launch_walk_b<KIND, QT, NW, 2>(a, ws, V, sg, s);
+    return launch_walk_b<KIND, QT, NW, 1>(a, ws, V, sg, s);
 }
 
 template <int KIND, typename QT>
-hipError_t launch_walk_v(const RaggedArgs& a, const char* ws, int V, const Segments& sg, hipStream_t s) {
+hipError_t launch_walk_v(const RaggedArgs& a, const char* ws, int V, int heads, const Segments& sg, hipStream_t s) {
     switch (V) {
-        case 64: return launch_walk_n<KIND, QT, 4>(a, ws, V, sg, s);
-        case 80: return launch_walk_n<KIND, QT, 5>(a, ws, V, sg, s);
-        case 96: return launch_walk_n<KIND, QT, 6>(a, ws, V, sg, s);
-        case 112: return launch_walk_n<KIND, QT, 7>(a, ws, V, sg, s);
-        case 128: return launch_walk_n<KIND, QT, 4>(a, ws, V, sg, s);
+        case 64: return launch_walk_n<KIND, QT, 4>(a, ws, V, heads, sg, s);
+        case 80: return launch_walk_n<KIND, QT, 5>(a, ws, V, heads, sg, s);
+        case 96: return launch_walk_n<KIND, QT, 6>(a, ws, V, heads, sg, s);
+        case 112: return launch_walk_n<KIND, QT, 7>(a, ws, V, heads, sg, s);
+        case 128: return launch_walk_n<KIND, QT, 4>(a, ws, V, heads, sg, s);
     }
     return hipErrorInvalidValue;
 }
@@ -1175,24 +1186,47 @@ size_t record_bytes(const sketchssm_shape& sh, long n_seqs, long total) {
     return (n + 255) / 256 * 256;
 }
 
-// Whether and how long sequences are cut: so that the walk has a block for each of
-// the 256 CUs, in segments of 256 tokens or more, where that is worth the second
-// pass.  One sequence, us without and with: GDN, 32 heads of 128, 4 segments: 4096
-// tokens 251, 181 and 1024 tokens 75, 76; 64 heads, 2 segments: 4096 tokens 285, 270
-// and 1024 tokens 79, 83; more segments than CUs need (64 heads, 4): 285, 298.
-// Mamba-2, 16 heads of 64, 4096 tokens, 16 segments: 233, 76.
-Segments segments_of(const sketchssm_shape& sh, long n_seqs, long total, long max_len) {
-    Segments sg = {0, 1, nullptr};
+// How the walk is cut into blocks.  With few sequences the longest decides: blocks
+// are counted as though all were as long as it.
+//
+// Two heads of a key head share a block, its keys and its queries, in Mamba-2 layers
+// with bf16 keys whose head has 5 or 6 waves: a CU takes one such block of one head,
+// as a SIMD takes 3 of these waves and a block's fifth and sixth go where the next
+// block's would; of two heads it takes 10 or 12 waves.  us apart and together, 16384
+// tokens of 64 sequences: 128 heads of 80 862, 608; 64 heads of 96 460, 361; but 64
+// heads of 64, where a CU takes blocks of 4 waves anyway, 255, 281.  With less than
+// a pair for three CUs of four, blocks of one head: 512 tokens of one sequence, 128
+// heads of 80, 47, 59.
+//
+// Long sequences are cut into segments so that there is a block for each of the 256
+// CUs, in segments of 256 tokens or more, where that is worth the second pass.  One
+// sequence, us without and with: GDN, 32 heads of 128, 4 segments: 4096 tokens 251,
+// 181 and 1024 tokens 75, 76; 64 heads, 2 segments: 4096 tokens 285, 270 and 1024
+// tokens 79, 83; more segments than CUs need (64 heads, 4): 285, 298.  Mamba-2, 16
+// heads of 64, 4096 tokens, 16 segments: 233, 76.
+struct Cut {
+    int heads;  // of a block
+    Segments sg;
+};
+
+Cut cut_of(const sketchssm_shape& sh, long n_seqs, long total, long max_len) {
+    Cut cut = {1, {0, 1, nullptr}};
+    const long len = std::min(max_len, total);
+    if (len <= 0) return cut;
     const int nw = sh.V == 128 ? 4 : sh.V / 16;
-    const long len = std::min(max_len, total), per_seq = long(sh.H) * (sh.V / (16 * nw));
-    if (len <= 0) return sg;
-    const long blocks = (total + len - 1) / len * per_seq;  // as though the longest were all
-    const long count = std::min(256 / blocks, len / 256);
-    if (count < 2 || count * len < 4096) return sg;
-    if (n_seqs * per_seq * count > 4096) return sg;  // among many short ones most blocks would have no segment
-    sg.len = int((len + count - 1) / count + kC - 1) / kC * kC;
-    sg.most = int((len + sg.len - 1) / sg.len);
-    return sg;
+    long per_seq = long(sh.H) * (sh.V / (16 * nw));
+    const long longest = (total + len - 1) / len, most = len / 256;
+    if (sh.kind == SKSSM_MAMBA2 && sh.qkv == SKSSM_BF16 && (nw == 5 || nw == 6) && sh.H / kq_heads_of(sh) % 2 == 0 &&
+        longest * per_seq / 2 * std::max(most, 1l) >= 192) {
+        cut.heads = 2;
+        per_seq /= 2;
+    }
+    const long count = std::min(256 / (longest * per_seq), most);
+    if (count < 2 || count * len < 4096) return cut;
+    if (n_seqs * per_seq * count > 4096) return cut;  // among many short ones most blocks would have no segment
+    cut.sg.len = int((len + count - 1) / count + kC - 1) / kC * kC;
+    cut.sg.most = int((len + cut.sg.len - 1) / cut.sg.len);
+    return cut;
 }
 
 size_t segment_bytes(const sketchssm_shape& sh, const Segments& sg, long n_seqs, long total) {
@@ -1202,25 +1236,27 @@ size_t segment_bytes(const sketchssm_shape& sh, const Segments& sg, long n_seqs,
 }  // namespace
 
 size_t walk_workspace(const sketchssm_shape& sh, long n_seqs, long total, long max_len) {
-    return record_bytes(sh, n_seqs, total) + segment_bytes(sh, segments_of(sh, n_seqs, total, max_len), n_seqs, total);
+    return record_bytes(sh, n_seqs, total) + segment_bytes(sh, cut_of(sh, n_seqs, total, max_len).sg, n_seqs, total);
 }
 
 hipError_t launch_walk(const sketchssm_shape& sh, const RaggedArgs& a, char* ws, hipStream_t s) {
     const bool bf = sh.qkv == SKSSM_BF16;
     const hipError_t e = bf ? launch_prep<Bf16Tag>(sh.kind, a, ws, s) : launch_prep<F32Tag>(sh.kind, a, ws, s);
     if (e != hipSuccess) return e;
-    Segments sg = segments_of(sh, a.n_seqs, a.total, a.max_len);
+    const Cut cut = cut_of(sh, a.n_seqs, a.total, a.max_len);
+    Segments sg = cut.sg;
+    const int heads = cut.heads;
     sg.ends = ws + record_bytes(sh, a.n_seqs, a.total);
     switch (sh.kind) {
         case SKSSM_MAMBA2:
-            return bf ? launch_walk_v<SKSSM_MAMBA2, Bf16Tag>(a, ws, sh.V, sg, s)
-                      : launch_walk_v<SKSSM_MAMBA2, F32Tag>(a, ws, sh.V, sg, s);
+            return bf ? launch_walk_v<SKSSM_MAMBA2, Bf16Tag>(a, ws, sh.V, heads, sg, s)
+                      : launch_walk_v<SKSSM_MAMBA2, F32Tag>(a, ws, sh.V, heads, sg, s);
         case SKSSM_GDN:
-            return bf ? launch_walk_v<SKSSM_GDN, Bf16Tag>(a, ws, sh.V, sg, s)
-                      : launch_walk_v<SKSSM_GDN, F32Tag>(a, ws, sh.V, sg, s);
+            return bf ? launch_walk_v<SKSSM_GDN, Bf16Tag>(a, ws, sh.V, heads, sg, s)
+                      : launch_walk_v<SKSSM_GDN, F32Tag>(a, ws, sh.V, heads, sg, s);
         case SKSSM_KDA:
-            return bf ? launch_walk_v<SKSSM_KDA, Bf16Tag>(a, ws, sh.V, sg, s)
-                      : launch_walk_v<SKSSM_KDA, F32Tag>(a, ws, sh.V, sg, s);
+            return bf ? launch_walk_v<SKSSM_KDA, Bf16Tag>(a, ws, sh.V, heads, sg, s)
+                      : launch_walk_v<SKSSM_KDA, F32Tag>(a, ws, sh.V, heads, sg, s);
     }
     return hipErrorInvalidValue;
 }

@@ -31,19 +31,19 @@ def _slow(d):
     d["a"] = d["a"] ** 0.02
 
 
-def _go(kind, qkv, d, H, Hk, V, S0, rows0, S, rows, y, max_len, stream=None, workspace=None):
+def _go(kind, qkv, d, H, Hk, V, S0, rows0, S, rows, y, max_len, stream=None, workspace=None, cut=True):
     import rank_state_read_amd as lib
     sh = lib.make_shape(S.shape[0], H, 128, V, 16, 1, 79, 49, kind, qkv, Hk)
     n = len(d["offsets"]) - 1
     need = lib.sketchssm_prefill_workspace(sh, n, d["v"].shape[0], max_len)
-    assert need > lib.sketchssm_prefill_workspace(sh, n, d["v"].shape[0], 64), "not cut into segments"
+    assert not cut or need > lib.sketchssm_prefill_workspace(sh, n, d["v"].shape[0], 64), "not cut into segments"
     if workspace is None:
         workspace = torch.full((need,), 255, dtype=torch.uint8, device="cuda")  # NaN wherever it is read unwritten
     lib.sketchssm_prefill(sh, S0, rows0, S, rows, d["offsets"], max_len, d["q"], d["k"], d["v"], d["a"], d["beta"], y,
                           workspace=workspace, stream=stream)
 
 
-def _check(kind, qkv, lens, H, Hk, V, seed=0, edit=_slow, zero=(), max_len=None):
+def _check(kind, qkv, lens, H, Hk, V, seed=0, edit=_slow, zero=(), max_len=None, cut=True):
     n = len(lens)
     d = ref.draw(kind, qkv, lens, H, Hk, V, seed, 3, 5)
     if edit:
@@ -51,7 +51,7 @@ def _check(kind, qkv, lens, H, Hk, V, seed=0, edit=_slow, zero=(), max_len=None)
     rows, rows0 = [(i + 1) % n for i in range(n)], [-1 if i in zero else i for i in range(n)]
     S, y = torch.full((n + 1, H, 128, V), 7.0, device="cuda"), torch.full(d["v"].shape, 9.0, device="cuda")
     print(f"  {kind} {qkv} V={V} H={H}/{Hk} lens={lens}", flush=True)
-    _go(kind, qkv, d, H, Hk, V, d["S0"], _i32(rows0), S, _i32(rows), y, max_len or max(lens))
+    _go(kind, qkv, d, H, Hk, V, d["S0"], _i32(rows0), S, _i32(rows), y, max_len or max(lens), cut=cut)
     torch.cuda.synchronize()
     first = torch.stack([torch.zeros_like(d["S0"][0]) if r < 0 else d["S0"][r] for r in rows0])
     yr, Sr = ref.run(kind, d, lens, first)
@@ -160,3 +160,12 @@ def test_replays_and_streams(kind):
         for i in range(2):
             go(i, stream=streams[i])
         same(f"streams {rep}")
+
+
+@pytest.mark.timeout(300)
+@pytest.mark.parametrize("V", [64, 80, 96, 112])
+@pytest.mark.parametrize("H,Hk", [(48, 8), (16, 2), (12, 4), (20, 1)])
+def test_many_heads_of_a_key_head(H, Hk, V):
+    """Blocks of two heads where widths and numbers allow them, of one elsewhere, cut into segments and not."""
+    for lens in ([1100, 80], [70, 33, 0, 64, 65, 20, 7, 90, 31, 32, 33, 44, 51, 12]):
+        _check("mamba2", "bf16", lens, H, Hk, V, zero=(1,), cut=False)
