@@ -123,31 +123,29 @@ void recur_kernel(RaggedArgs A) {
             const float a_s = KDA ? 1.f : al[j];
             const float bt = be[j];
             const float vc = vs[j * V + v0 + lr];
-            // erase term of this lane's column: k^T S (GDN), k^T diag(a) S (KDA)
+            // erase term of this lane's column: k^T S (GDN), k^T diag(a) S (KDA, whose
+            // state takes its decays here)
             float wc = 0.f;
             if (DELTA) {
 #pragma unroll
                 for (int kt = 0; kt < 8; ++kt) {
                     const f32x4 k4 = *reinterpret_cast<const f32x4*>(kj + 16 * kt);
-                    f32x4 a4 = {1.f, 1.f, 1.f, 1.f};
-                    if (KDA) a4 = *reinterpret_cast<const f32x4*>(aj + 16 * kt);
+                    if (KDA) s[kt] *= *reinterpret_cast<const f32x4*>(aj + 16 * kt);
 #pragma unroll
-                    for (int rr = 0; rr < 4; ++rr) wc = fmaf(KDA ? k4[rr] * a4[rr] : k4[rr], s[kt][rr], wc);
+                    for (int rr = 0; rr < 4; ++rr) wc = fmaf(k4[rr], s[kt][rr], wc);
                     __builtin_amdgcn_sched_barrier(0);
                 }
                 wc = recur_quarter_sum(wc);
             }
-            const float vt = KDA ? vc - wc : DELTA ? vc - a_s * wc : vc;
+            const float u = KDA ? bt * (vc - wc) : DELTA ? bt * (vc - a_s * wc) : vc;
             float yc = 0.f;
 #pragma unroll
             for (int kt = 0; kt < 8; ++kt) {
                 const f32x4 k4 = *reinterpret_cast<const f32x4*>(kj + 16 * kt);
                 const f32x4 q4 = *reinterpret_cast<const f32x4*>(qj + 16 * kt);
-                f32x4 a4 = {a_s, a_s, a_s, a_s};
-                if (KDA) a4 = *reinterpret_cast<const f32x4*>(aj + 16 * kt);
 #pragma unroll
                 for (int rr = 0; rr < 4; ++rr) {
-                    s[kt][rr] = fmaf(a4[rr], s[kt][rr], bt * k4[rr] * vt);
+                    s[kt][rr] = fmaf(k4[rr], u, KDA ? s[kt][rr] : a_s * s[kt][rr]);
                     yc = fmaf(q4[rr], s[kt][rr], yc);
                 }
                 // one tile's operands at a time: within the register budget
