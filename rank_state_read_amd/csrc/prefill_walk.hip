@@ -79,67 +79,60 @@ __device__ __forceinline__ u32x4 load16(__amdgpu_buffer_rsrc_t rs, int off) {
 // T and P of every chunk and head: one wave per (slot, head).
 // ---------------------------------------------------------------------------
 
-// A record from the wave's matrices in LDS: g = -A (strictly lower), gq = P;
-// lane j < 32 and j + 32 hold token j's beta (0 behind the sequence).
-template <bool DELTA>
-__device__ __forceinline__ void put_record(char* rec, float* g, const float* gq, float bj, int lane) {
-    typedef Record R;
-    const int lr = lane & 15, lq = lane >> 4;
-    float b[8];
-    if (DELTA) {
-        // (I + A)^-1: the diagonal blocks of 16 by forward substitution, one lane per
-        // column, then M_10 = M_11 (-A_10) M_00
-        if (lane < 32) {
-            float* d = g + (lane & 16) * (kGS + 1);
-            const int l = lane & 15;
-            float x[16];
+// A wave's matrix in LDS as A operands: three terms, two row tiles.
+__device__ __forceinline__ void put_operands(char* dst, const float* m, const float* scale, int lane) {
 #pragma unroll
-            for (int i = 0; i < 16; ++i) {
-                float s0 = i == l ? 1.f : 0.f, s1 = 0.f;
-#pragma unroll
-                for (int m = 0; m < i; m += 4) {
-                    const f32x4 n4 = *reinterpret_cast<const f32x4*>(d + i * kGS + m);
-#pragma unroll
-                    for (int e = 0; e < 4; ++e)
-                        if (m + e < i) {
-                            if (e & 1) s1 = fmaf(n4[e], x[m + e], s1);
-                            else s0 = fmaf(n4[e], x[m + e], s0);
-                        }
-                }
-                x[i] = s0 + s1;
-            }
-            wave_sync();
-#pragma unroll
-            for (int i = 0; i < 16; ++i) d[i * kGS + l] = x[i];
-        }
-        wave_sync();
-        const f32x4 r10 = block_mul(g + 16 * kGS, g, lr, lq);
-        const f32x4 m10 = block_mul(g + 16 * kGS + 16, r10, lr, lq);
-        wave_sync();
-#pragma unroll
-        for (int r = 0; r < 4; ++r) g[(16 + 4 * lq + r) * kGS + lr] = m10[r];
-        wave_sync();
-#pragma unroll
-        for (int i = 0; i < 8; ++i) b[i] = __shfl(bj, 8 * lq + i, 64);
-    }
-    // P and T = (I + A)^-1 diag(beta) as A operands
-#pragma unroll
-    for (int m = 0; m < 2; ++m) {
+    for (int o = 0; o < 2; ++o) {
         float f[8];
-        const int at = tile_row(m, lr) * kGS + 8 * lq;
-        load8f(gq + at, f);
+        load8f(m + tile_row(o, lane & 15) * kGS + 8 * (lane >> 4), f);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) f[i] *= scale ? scale[i] : 1.f;
         const Split p = split8(f);
 #pragma unroll
-        for (int e = 0; e < 3; ++e) *reinterpret_cast<u32x4*>(rec + R::p + (2 * e + m) * kFrag + lane * 16) = p.t[e];
-        if (DELTA) {
-            load8f(g + at, f);
-#pragma unroll
-            for (int i = 0; i < 8; ++i) f[i] *= b[i];
-            const Split t = split8(f);
-#pragma unroll
-            for (int e = 0; e < 3; ++e) *reinterpret_cast<u32x4*>(rec + R::t + (2 * e + m) * kFrag + lane * 16) = t.t[e];
-        }
+        for (int e = 0; e < 3; ++e) *reinterpret_cast<u32x4*>(dst + (2 * e + o) * kFrag + lane * 16) = p.t[e];
     }
+}
+
+// T = (I + A)^-1 diag(beta) of a record from g = -A (strictly lower) in LDS; lane
+// j < 32 and j + 32 hold token j's beta (0 behind the sequence).
+__device__ __forceinline__ void put_t(char* rec, float* g, float bj, int lane) {
+    const int lr = lane & 15, lq = lane >> 4;
+    float b[8];
+    // (I + A)^-1: the diagonal blocks of 16 by forward substitution, one lane per
+    // column, then M_10 = M_11 (-A_10) M_00
+    if (lane < 32) {
+        float* d = g + (lane & 16) * (kGS + 1);
+        const int l = lane & 15;
+        float x[16];
+#pragma unroll
+        for (int i = 0; i < 16; ++i) {
+            float s0 = i == l ? 1.f : 0.f, s1 = 0.f;
+#pragma unroll
+            for (int m = 0; m < i; m += 4) {
+                const f32x4 n4 = *reinterpret_cast<const f32x4*>(d + i * kGS + m);
+#pragma unroll
+                for (int e = 0; e < 4; ++e)
+                    if (m + e < i) {
+                        if (e & 1) s1 = fmaf(n4[e], x[m + e], s1);
+                        else s0 = fmaf(n4[e], x[m + e], s0);
+                    }
+            }
+            x[i] = s0 + s1;
+        }
+        wave_sync();
+#pragma unroll
+        for (int i = 0; i < 16; ++i) d[i * kGS + l] = x[i];
+    }
+    wave_sync();
+    const f32x4 r10 = block_mul(g + 16 * kGS, g, lr, lq);
+    const f32x4 m10 = block_mul(g + 16 * kGS + 16, r10, lr, lq);
+    wave_sync();
+#pragma unroll
+    for (int r = 0; r < 4; ++r) g[(16 + 4 * lq + r) * kGS + lr] = m10[r];
+    wave_sync();
+#pragma unroll
+    for (int i = 0; i < 8; ++i) b[i] = __shfl(bj, 8 * lq + i, 64);
+    put_operands(rec + Record::t, g, b, lane);
 }
 
 // One decay per token.  k_i . k_j and q_i . k_j first (bf16: exact products on the
@@ -228,7 +221,8 @@ __global__ __launch_bounds__(256) void prep_scalar_kernel(RaggedArgs A, char* ws
         reinterpret_cast<float*>(rec + R::g)[lane] = lane < 32 ? gam : (valid ? d : 0.f);
     }
     wave_sync();
-    put_record<DELTA>(rec, g, gq, bj, lane);
+    put_operands(rec + R::p, gq, nullptr, lane);
+    if (DELTA) put_t(rec, g, bj, lane);
 }
 
 // Mamba-2 with bf16 keys: one wave per (slot, key head) for q_i . k_j, formed
@@ -307,115 +301,96 @@ __global__ __launch_bounds__(256) void prep_mamba2_kernel(RaggedArgs A, char* ws
 //   A_ij ~ sum_c (k_i a_{m+1} .. a_i) (k_j a_{j+1} .. a_m),  m the last token of L
 // in the 2^{b+1}-block of i and j: one 16 x 16 product over the channels per bit,
 // used where i and j share their higher bits.  The partial products of decays
-// over 2^b-blocks follow from those over half blocks.  Lanes hold two channels
-// each; the scaled rows reach the fp32 matrix instruction through LDS.
-constexpr int kPS = kK + 4;  // row stride of the scaled rows, floats
+// over 2^b-blocks follow from those over half blocks.  Two waves share a chunk and
+// head, 64 channels each, one to a lane: with all 128 in one wave the decays' products
+// alone took half its registers, and float32 keys had to be read again for every bit
+// (64 sequences, 16384 tokens, 32 heads, the whole call: 841 us against 1030).  The
+// scaled rows reach the fp32 matrix instruction through LDS, the sums stay in
+// registers until the rows' space is free for them.
+constexpr int kPS = kK / 2 + 4;  // row stride of the scaled rows, floats
 
 template <typename QT>
 __global__ __launch_bounds__(128) void prep_kda_kernel(RaggedArgs A, char* ws) {
     constexpr bool BF = std::is_same<QT, Bf16Tag>::value;
     typedef Record R;
-    __shared__ __align__(16) float tiles[2][2][kC * kGS];
     __shared__ __align__(16) float rows[2][48 * kPS];
+    static_assert(sizeof(rows) >= 2 * kC * kGS * 4, "holds A and P in the end");
     const int w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int lane = threadIdx.x & 63, lr = lane & 15, lq = lane >> 4;
-    const long task = long(blockIdx.x) * 2 + w;
+    const long task = blockIdx.x;
     const long slot = task / A.H;
     const int h = int(task - slot * A.H), hk = h / A.share;
     int t0 = 0;
     const int clen = slot_chunk<kC>(A, slot, lane, t0);
-    if (clen == 0) return;  // no wave waits for another one below
-    float* g = tiles[w][0];
-    float* gq = tiles[w][1];
-    float* sr = rows[w];
+    if (clen == 0) return;  // both waves
 
-    const int j = lane & 31;
-    const bool valid = j < clen;
-    const float bj = valid ? A.beta[(size_t(t0) + j) * A.H + h] : 0.f;
-    // this lane's two channels of every token; pre and suf: the decays' products over
-    // a token's 2^b-block up to it and after it
-    uint32_t kb[BF ? kC : 1], qb[BF ? kC : 1];
-    f32x2 pre[kC], suf[kC];
+    // this lane's channel of every token; pre and suf: the decays' products over a
+    // token's 2^b-block up to it and after it
+    uint32_t kq[kC], q32[BF ? 1 : kC];  // bf16: key and query in one register
+    float pre[kC], suf[kC];
+    {
+        const int c = 64 * w + lane;
+        const size_t kq0 = (size_t(t0) * A.Hk + hk) * kK + c, kqs = size_t(A.Hk) * kK;
+        const float* a0 = A.a + (size_t(t0) * A.H + h) * kK + c;
 #pragma unroll
-    for (int t = 0; t < kC; ++t) {
-        const bool in = t < clen;
-        const size_t tok = size_t(t0) + (in ? t : 0);
-        if constexpr (BF) {
-            const size_t e = (tok * A.Hk + hk) * kK + 2 * lane;
-            const uint32_t kx = *reinterpret_cast<const uint32_t*>(static_cast<const uint16_t*>(A.k) + e);
-            const uint32_t qx = *reinterpret_cast<const uint32_t*>(static_cast<const uint16_t*>(A.q) + e);
-            kb[t] = in ? kx : 0u;
-            qb[t] = in ? qx : 0u;
+        for (int t = 0; t < kC; ++t) {
+            const bool in = t < clen;
+            const size_t at = in ? t : 0;
+            typedef typename std::conditional<BF, uint16_t, uint32_t>::type bits_t;
+            const uint32_t k1 = static_cast<const bits_t*>(A.k)[kq0 + at * kqs];
+            const uint32_t q1 = static_cast<const bits_t*>(A.q)[kq0 + at * kqs];
+            const float a1 = a0[at * A.H * kK];
+            kq[t] = in ? BF ? k1 << 16 | q1 : k1 : 0u;
+            if (!BF) q32[t] = in ? q1 : 0u;
+            pre[t] = in ? a1 : 1.f;
+            suf[t] = 1.f;
         }
-        const f32x2 ax = *reinterpret_cast<const f32x2*>(A.a + (tok * A.H + h) * kK + 2 * lane);
-        pre[t] = in ? ax : f32x2{1.f, 1.f};
-        suf[t] = f32x2{1.f, 1.f};
     }
-    auto value = [&](const void* base, const uint32_t* packed, int t) {
-        if constexpr (BF) {
-            return f32x2{__uint_as_float(packed[t] << 16), __uint_as_float(packed[t] & 0xffff0000u)};
-        } else {  // from memory again every time: registers are short
-            const size_t e = ((size_t(t0) + min(t, clen - 1)) * A.Hk + hk) * kK + 2 * lane;
-            const f32x2 x = *reinterpret_cast<const f32x2*>(static_cast<const float*>(base) + e);
-            return t < clen ? x : f32x2{0.f, 0.f};
-        }
-    };
-    auto key = [&](int t) { return value(A.k, kb, t); };
-    auto query = [&](int t) { return value(A.q, qb, t); };
+    auto key = [&](int t) { return __uint_as_float(BF ? kq[t] & 0xffff0000u : kq[t]); };
+    auto query = [&](int t) { return __uint_as_float(BF ? kq[t] << 16 : q32[t]); };
     // 16 x 16 products of rows x and y of the scaled rows
+    float* su = rows[w];
+    float* sq = su + 16 * kPS;
+    float* sl = su + 32 * kPS;
     auto mul = [&](const float* x, const float* y) {
         f32x4 d = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-        for (int s = 0; s < 8; ++s) {
-            const f32x4 xa = *reinterpret_cast<const f32x4*>(x + lr * kPS + 32 * lq + 4 * s);
-            const f32x4 ya = *reinterpret_cast<const f32x4*>(y + lr * kPS + 32 * lq + 4 * s);
+        for (int s = 0; s < 4; ++s) {
+            const f32x4 xa = *reinterpret_cast<const f32x4*>(x + lr * kPS + 16 * lq + 4 * s);
+            const f32x4 ya = *reinterpret_cast<const f32x4*>(y + lr * kPS + 16 * lq + 4 * s);
 #pragma unroll
             for (int e = 0; e < 4; ++e) d = mfma_16x16x4(xa[e], ya[e], d);
         }
         return d;
     };
-    float* su = sr;
-    float* sq = sr + 16 * kPS;
-    float* sl = sr + 32 * kPS;
-    for (int i = lane; i < kC * kGS; i += 64) g[i] = gq[i] = 0.f;
-    // the diagonal of P: q_i . k_i
+    // the diagonal of P, q_i . k_i: row sums of the products
+    f32x4 diag[2] = {};
 #pragma unroll
-    for (int m = 0; m < 2; ++m) {
+    for (int t = 0; t < kC; ++t) su[t * kPS + lane] = query(t) * key(t);
+    wave_sync();
 #pragma unroll
-        for (int t = 0; t < 16; ++t) {
-            *reinterpret_cast<f32x2*>(sq + t * kPS + 2 * lane) = query(16 * m + t);
-            *reinterpret_cast<f32x2*>(sl + t * kPS + 2 * lane) = key(16 * m + t);
+    for (int m = 0; m < 2; ++m)
+#pragma unroll
+        for (int s = 0; s < 4; ++s) {
+            const f32x4 xa = *reinterpret_cast<const f32x4*>(su + (16 * m + lr) * kPS + 16 * lq + 4 * s);
+#pragma unroll
+            for (int e = 0; e < 4; ++e) diag[m] = mfma_16x16x4(xa[e], 1.f, diag[m]);
         }
-        wave_sync();
-        const f32x4 d = mul(sq, sl);
-#pragma unroll
-        for (int r = 0; r < 4; ++r)
-            if (4 * lq + r == lr) gq[(16 * m + lr) * (kGS + 1)] = d[r];
-        wave_sync();
-    }
+    wave_sync();
+    f32x4 d[5], dq[5];
 #pragma unroll
     for (int b = 0; b < 5; ++b) {
         // pre, suf are over 2^b-blocks here
 #pragma unroll
         for (int t = 0; t < 16; ++t) {
             const int lo = ((t >> b) << (b + 1)) | (t & ((1 << b) - 1)), up = lo | (1 << b);
-            *reinterpret_cast<f32x2*>(su + t * kPS + 2 * lane) = key(up) * pre[up];
-            *reinterpret_cast<f32x2*>(sq + t * kPS + 2 * lane) = query(up) * pre[up];
-            *reinterpret_cast<f32x2*>(sl + t * kPS + 2 * lane) = key(lo) * suf[lo];
+            su[t * kPS + lane] = key(up) * pre[up];
+            sq[t * kPS + lane] = query(up) * pre[up];
+            sl[t * kPS + lane] = key(lo) * suf[lo];
         }
         wave_sync();
-        const f32x4 d = mul(su, sl), dq = mul(sq, sl);
-        const int lj = ((lr >> b) << (b + 1)) | (lr & ((1 << b) - 1));
-#pragma unroll
-        for (int r = 0; r < 4; ++r) {
-            const int t = 4 * lq + r;
-            const int ui = ((t >> b) << (b + 1)) | (t & ((1 << b) - 1)) | (1 << b);
-            const float bi = __shfl(bj, ui, 64);
-            if ((t >> b) == (lr >> b)) {
-                g[ui * kGS + lj] = -bi * d[r];
-                gq[ui * kGS + lj] = dq[r];
-            }
-        }
+        d[b] = mul(su, sl);
+        dq[b] = mul(sq, sl);
         wave_sync();
 #pragma unroll
         for (int t = 0; t < kC; ++t)
@@ -424,7 +399,43 @@ __global__ __launch_bounds__(128) void prep_kda_kernel(RaggedArgs A, char* ws) {
         for (int t = 0; t < kC; ++t)
             if ((t >> b) & 1) pre[t] *= pre[(t & ~((2 << b) - 1)) | ((1 << b) - 1)];
     }
-    put_record<true>(ws + task * R::bytes, g, gq, bj, lane);
+    // A and P, wave 1's part added to wave 0's
+    const int j = lane & 31;
+    const float bj = j < clen ? A.beta[(size_t(t0) + j) * A.H + h] : 0.f;
+    float* g = rows[0];
+    float* gq = g + kC * kGS;
+    __syncthreads();
+    if (w == 0)
+        for (int i = lane; i < kC * kGS; i += 64) g[i] = gq[i] = 0.f;
+#pragma unroll
+    for (int turn = 0; turn < 2; ++turn) {
+        __syncthreads();
+        if (w != turn) continue;
+        wave_sync();
+#pragma unroll
+        for (int b = 0; b < 5; ++b) {
+            const int lj = ((lr >> b) << (b + 1)) | (lr & ((1 << b) - 1));
+#pragma unroll
+            for (int r = 0; r < 4; ++r) {
+                const int t = 4 * lq + r;
+                const int ui = ((t >> b) << (b + 1)) | (t & ((1 << b) - 1)) | (1 << b);
+                const float bi = __shfl(bj, ui, 64);
+                if ((t >> b) == (lr >> b)) {
+                    g[ui * kGS + lj] += -bi * d[b][r];
+                    gq[ui * kGS + lj] += dq[b][r];
+                }
+            }
+        }
+#pragma unroll
+        for (int m = 0; m < 2; ++m)
+#pragma unroll
+            for (int r = 0; r < 4; ++r)
+                if (4 * lq + r == lr) gq[(16 * m + lr) * (kGS + 1)] += diag[m][r];
+    }
+    __syncthreads();
+    char* rec = ws + task * R::bytes;
+    if (w == 0) put_t(rec, g, bj, lane);
+    else put_operands(rec + R::p, gq, nullptr, lane);
 }
 
 }  // namespace
@@ -479,7 +490,8 @@ struct WalkLds {  // bytes
     static constexpr int bytes = gc + (kda ? kK * 4 : 0);
 };
 
-// HB heads of a key head to a block, NW waves each.  ENDS: M and N of segments, no outputs.  The columns of M follow those of N.
+// HB heads of a key head to a block, NW waves each.  ENDS: M and N of segments, no
+// outputs; the columns of M follow those of N.
 template <int KIND, typename QT, int NW, int HB, bool ENDS>
 __global__ __launch_bounds__(HB * NW * 64)
 __attribute__((amdgpu_waves_per_eu(kFormP<KIND, QT> ? 3 : 2)))
@@ -1109,6 +1121,11 @@ __global__ __launch_bounds__(256) void join_kernel(RaggedArgs A, int V, Segments
 
 namespace {
 
+struct Cut {
+    int waves, heads;  // waves of a head and heads of a block
+    Segments sg;
+};
+
 template <int KIND, typename QT, int NW, int HB, bool ENDS>
 hipError_t launch_walk_t(const RaggedArgs& a, const char* ws, int V, const Segments& sg, hipStream_t s) {
     const long slots = prefill_slots<kC>(a.total, a.n_seqs);
@@ -1129,32 +1146,37 @@ hipError_t launch_walk_t(const RaggedArgs& a, const char* ws, int V, const Segme
 
 template <int KIND, typename QT, int NW, int HB>
 hipError_t launch_walk_b(const RaggedArgs& a, const char* ws, int V, const Segments& sg, hipStream_t s) {
-    if (sg.len) {
-        hipError_t e = launch_walk_t<KIND, QT, NW, HB, true>(a, ws, V, sg, s);
-        if (e != hipSuccess) return e;
-        const long blocks = long(a.n_seqs) * a.H * (V / 16);  // at most 8 x 4096
-        hipLaunchKernelGGL((join_kernel<KIND != SKSSM_MAMBA2>), dim3(uint32_t(blocks)), dim3(256), 0, s, a, V, sg);
-        e = hipGetLastError();
-        if (e != hipSuccess) return e;
+    if constexpr (NW < 8) {  // blocks of 8 waves walk no segments
+        if (sg.len) {
+            hipError_t e = launch_walk_t<KIND, QT, NW, HB, true>(a, ws, V, sg, s);
+            if (e != hipSuccess) return e;
+            const long blocks = long(a.n_seqs) * a.H * (V / 16);  // at most 8 x 4096
+            hipLaunchKernelGGL((join_kernel<KIND != SKSSM_MAMBA2>), dim3(uint32_t(blocks)), dim3(256), 0, s, a, V, sg);
+            e = hipGetLastError();
+            if (e != hipSuccess) return e;
+        }
     }
     return launch_walk_t<KIND, QT, NW, HB, false>(a, ws, V, sg, s);
 }
 
 template <int KIND, typename QT, int NW>
-hipError_t launch_walk_n(const RaggedArgs& a, const char* ws, int V, int heads, const Segments& sg, hipStream_t s) {
+hipError_t launch_walk_n(const RaggedArgs& a, const char* ws, int V, const Cut& cut, hipStream_t s) {
     if constexpr (kFormP<KIND, QT> && (NW == 5 || NW == 6))
-        if (heads == 2) return launch_walk_b<KIND, QT, NW, 2>(a, ws, V, sg, s);
-    return launch_walk_b<KIND, QT, NW, 1>(a, ws, V, sg, s);
+        if (cut.heads == 2) return launch_walk_b<KIND, QT, NW, 2>(a, ws, V, cut.sg, s);
+    return launch_walk_b<KIND, QT, NW, 1>(a, ws, V, cut.sg, s);
 }
 
 template <int KIND, typename QT>
-hipError_t launch_walk_v(const RaggedArgs& a, const char* ws, int V, int heads, const Segments& sg, hipStream_t s) {
+hipError_t launch_walk_v(const RaggedArgs& a, const char* ws, int V, const Cut& cut, hipStream_t s) {
     switch (V) {
-        case 64: return launch_walk_n<KIND, QT, 4>(a, ws, V, heads, sg, s);
-        case 80: return launch_walk_n<KIND, QT, 5>(a, ws, V, heads, sg, s);
-        case 96: return launch_walk_n<KIND, QT, 6>(a, ws, V, heads, sg, s);
-        case 112: return launch_walk_n<KIND, QT, 7>(a, ws, V, heads, sg, s);
-        case 128: return launch_walk_n<KIND, QT, 4>(a, ws, V, heads, sg, s);
+        case 64: return launch_walk_n<KIND, QT, 4>(a, ws, V, cut, s);
+        case 80: return launch_walk_n<KIND, QT, 5>(a, ws, V, cut, s);
+        case 96: return launch_walk_n<KIND, QT, 6>(a, ws, V, cut, s);
+        case 112: return launch_walk_n<KIND, QT, 7>(a, ws, V, cut, s);
+        case 128:
+            if constexpr (KIND == SKSSM_KDA || std::is_same<QT, F32Tag>::value)
+                if (cut.waves == 8) return launch_walk_n<KIND, QT, 8>(a, ws, V, cut, s);
+            return launch_walk_n<KIND, QT, 4>(a, ws, V, cut, s);
     }
     return hipErrorInvalidValue;
 }
@@ -1163,12 +1185,12 @@ template <typename QT>
 hipError_t launch_prep(int kind, const RaggedArgs& a, char* ws, hipStream_t s) {
     const long tasks = prefill_slots<kC>(a.total, a.n_seqs) * a.H;
     if (tasks >= (1l << 31)) return hipErrorInvalidConfiguration;
-    const dim3 by4(uint32_t((tasks + 3) / 4)), by2(uint32_t((tasks + 1) / 2));
+    const dim3 by4(uint32_t((tasks + 3) / 4));
     const long units = prefill_slots<kC>(a.total, a.n_seqs) * (a.Hk + (a.H + 1) / 2);
     if (kFormP<SKSSM_MAMBA2, QT> && kind == SKSSM_MAMBA2)
         hipLaunchKernelGGL(prep_mamba2_kernel, dim3(uint32_t((units + 3) / 4)), dim3(256), 0, s, a, ws,
                            prefill_slots<kC>(a.total, a.n_seqs));
-    else if (kind == SKSSM_KDA) hipLaunchKernelGGL((prep_kda_kernel<QT>), by2, dim3(128), 0, s, a, ws);
+    else if (kind == SKSSM_KDA) hipLaunchKernelGGL((prep_kda_kernel<QT>), dim3(uint32_t(tasks)), dim3(128), 0, s, a, ws);
     else if (kind == SKSSM_GDN) hipLaunchKernelGGL((prep_scalar_kernel<true, QT>), by4, dim3(256), 0, s, a, ws);
     else hipLaunchKernelGGL((prep_scalar_kernel<false, QT>), by4, dim3(256), 0, s, a, ws);
     return hipGetLastError();
@@ -1198,22 +1220,23 @@ size_t record_bytes(const sketchssm_shape& sh, long n_seqs, long total) {
 // a pair for three CUs of four, blocks of one head: 512 tokens of one sequence, 128
 // heads of 80, 47, 59.
 //
+// 128 columns are two blocks of 4 waves.  With three terms a CU takes one block, and
+// both form the same planes: one block of 8 waves has less to do, though a chunk of
+// it lasts longer, so it is taken where such blocks fill the CUs.  us with 4 and with
+// 8 waves, 32 heads: KDA, 16384 tokens of 64 sequences 1018, 748, 2000 tokens of 4 153,
+// 172; GDN with float32 keys 759, 580 and 110, 132.
+//
 // Long sequences are cut into segments so that there is a block for each of the 256
 // CUs, in segments of 256 tokens or more, where that is worth the second pass.  One
 // sequence, us without and with: GDN, 32 heads of 128, 4 segments: 4096 tokens 251,
 // 181 and 1024 tokens 75, 76; 64 heads, 2 segments: 4096 tokens 285, 270 and 1024
 // tokens 79, 83; more segments than CUs need (64 heads, 4): 285, 298.  Mamba-2, 16
 // heads of 64, 4096 tokens, 16 segments: 233, 76.
-struct Cut {
-    int heads;  // of a block
-    Segments sg;
-};
-
 Cut cut_of(const sketchssm_shape& sh, long n_seqs, long total, long max_len) {
-    Cut cut = {1, {0, 1, nullptr}};
+    const int nw = sh.V == 128 ? 4 : sh.V / 16;
+    Cut cut = {nw, 1, {0, 1, nullptr}};
     const long len = std::min(max_len, total);
     if (len <= 0) return cut;
-    const int nw = sh.V == 128 ? 4 : sh.V / 16;
     long per_seq = long(sh.H) * (sh.V / (16 * nw));
     const long longest = (total + len - 1) / len, most = len / 256;
     if (sh.kind == SKSSM_MAMBA2 && sh.qkv == SKSSM_BF16 && (nw == 5 || nw == 6) && sh.H / kq_heads_of(sh) % 2 == 0 &&
@@ -1221,6 +1244,7 @@ Cut cut_of(const sketchssm_shape& sh, long n_seqs, long total, long max_len) {
         cut.heads = 2;
         per_seq /= 2;
     }
+    if (sh.V == 128 && (sh.kind == SKSSM_KDA || sh.qkv == SKSSM_F32) && longest * sh.H >= 256) cut.waves = 8;
     const long count = std::min(256 / (longest * per_seq), most);
     if (count < 2 || count * len < 4096) return cut;
     if (n_seqs * per_seq * count > 4096) return cut;  // among many short ones most blocks would have no segment
@@ -1243,20 +1267,18 @@ hipError_t launch_walk(const sketchssm_shape& sh, const RaggedArgs& a, char* ws,
     const bool bf = sh.qkv == SKSSM_BF16;
     const hipError_t e = bf ? launch_prep<Bf16Tag>(sh.kind, a, ws, s) : launch_prep<F32Tag>(sh.kind, a, ws, s);
     if (e != hipSuccess) return e;
-    const Cut cut = cut_of(sh, a.n_seqs, a.total, a.max_len);
-    Segments sg = cut.sg;
-    const int heads = cut.heads;
-    sg.ends = ws + record_bytes(sh, a.n_seqs, a.total);
+    Cut cut = cut_of(sh, a.n_seqs, a.total, a.max_len);
+    cut.sg.ends = ws + record_bytes(sh, a.n_seqs, a.total);
     switch (sh.kind) {
         case SKSSM_MAMBA2:
-            return bf ? launch_walk_v<SKSSM_MAMBA2, Bf16Tag>(a, ws, sh.V, heads, sg, s)
-                      : launch_walk_v<SKSSM_MAMBA2, F32Tag>(a, ws, sh.V, heads, sg, s);
+            return bf ? launch_walk_v<SKSSM_MAMBA2, Bf16Tag>(a, ws, sh.V, cut, s)
+                      : launch_walk_v<SKSSM_MAMBA2, F32Tag>(a, ws, sh.V, cut, s);
         case SKSSM_GDN:
-            return bf ? launch_walk_v<SKSSM_GDN, Bf16Tag>(a, ws, sh.V, heads, sg, s)
-                      : launch_walk_v<SKSSM_GDN, F32Tag>(a, ws, sh.V, heads, sg, s);
+            return bf ? launch_walk_v<SKSSM_GDN, Bf16Tag>(a, ws, sh.V, cut, s)
+                      : launch_walk_v<SKSSM_GDN, F32Tag>(a, ws, sh.V, cut, s);
         case SKSSM_KDA:
-            return bf ? launch_walk_v<SKSSM_KDA, Bf16Tag>(a, ws, sh.V, heads, sg, s)
-                      : launch_walk_v<SKSSM_KDA, F32Tag>(a, ws, sh.V, heads, sg, s);
+            return bf ? launch_walk_v<SKSSM_KDA, Bf16Tag>(a, ws, sh.V, cut, s)
+                      : launch_walk_v<SKSSM_KDA, F32Tag>(a, ws, sh.V, cut, s);
     }
     return hipErrorInvalidValue;
 }

@@ -169,3 +169,10 @@ def test_many_heads_of_a_key_head(H, Hk, V):
     """Blocks of two heads where widths and numbers allow them, of one elsewhere, cut into segments and not."""
     for lens in ([1100, 80], [70, 33, 0, 64, 65, 20, 7, 90, 31, 32, 33, 44, 51, 12]):
         _check("mamba2", "bf16", lens, H, Hk, V, zero=(1,), cut=False)
+
+
+@pytest.mark.timeout(300)
+@pytest.mark.parametrize("kind,qkv", [("kda", "bf16"), ("kda", "f32"), ("gdn", "f32"), ("mamba2", "f32")])
+def test_many_sequences(kind, qkv):
+    """More sequences than a wave has lanes, and enough of them for blocks of all 128 value columns."""
+    _check(kind, qkv, [33 + (7 * i) % 40 for i in range(70)], 6, 6, 128, zero=range(0, 70, 3), cut=False)
