@@ -130,10 +130,12 @@ __device__ __forceinline__ int slot_chunk(const RaggedArgs& A, long slot, int la
 }
 
 // The sequence that the r-th group of blocks takes: the longest first, so that the
-// last blocks to start are short ones.  Up to 64 sequences, one per lane; with more,
-// the order they come in (the blocks of any one are then few among many).
+// last blocks to start are short ones.  In full order up to 64 sequences, one per
+// lane; with more only the long ones go first (us of a GDN layer, 32 heads of 128,
+// 99 sequences of 100 tokens and behind them one of 6000: 539 against 630 in the order
+// they come in; 100 of 160 tokens: 425, 428).
 __device__ __forceinline__ int seq_of_rank(const RaggedArgs& A, int r, int lane) {
-    if (A.n_seqs > 64) return r;
+    if (A.n_seqs > 64) return seq_long_first(A, r, lane);
     const int len = lane < A.n_seqs ? max(A.offsets[lane + 1] - A.offsets[lane], 0) : -1;
     int rank = 0;
     for (int j = 0; j < A.n_seqs; ++j) {

@@ -59,6 +59,31 @@ __device__ __forceinline__ SeqSpan seq_span_uniform(const RaggedArgs& A, int i) 
     return s;
 }
 
+// The sequence that the r-th group of blocks takes where those of more than twice
+// the mean length go first, so that the last blocks to start are short ones.
+__device__ __forceinline__ int seq_long_first(const RaggedArgs& A, int r, int lane) {
+    const int bar = 2 * (A.total / A.n_seqs);
+    auto longs = [&](int c) {  // of sequences c .. c + 63
+        const int i = c + lane;
+        return __ballot(i < A.n_seqs && A.offsets[min(i, A.n_seqs - 1) + 1] > A.offsets[min(i, A.n_seqs - 1)] + bar);
+    };
+    int n = 0;
+    for (int c = 0; c < A.n_seqs; c += 64) n += __popcll(longs(c));
+    const bool first = r < n;
+    if (!first) r -= n;
+    for (int c = 0; c < A.n_seqs; c += 64) {
+        unsigned long long m = longs(c);
+        if (!first) m = ~m & (A.n_seqs - c < 64 ? (1ull << (A.n_seqs - c)) - 1 : ~0ull);
+        n = __popcll(m);
+        if (r < n) {
+            const bool mine = (m >> lane & 1) && __popcll(m & ((1ull << lane) - 1)) == r;
+            return c + __ffsll(__ballot(mine)) - 1;
+        }
+        r -= n;
+    }
+    return 0;  // r >= n_seqs: no such group
+}
+
 // Checks the arguments of a ragged entry point (host) and fills `out`.
 sketchssm_status ragged_args(const sketchssm_shape* shape, const float* S0, int32_t n_rows0, const int32_t* rows0,
                              float* S, const int32_t* rows, const int32_t* offsets, int32_t n_seqs,

@@ -45,11 +45,38 @@ __device__ __forceinline__ float recur_quarter_sum(float x) {
     return x;
 }
 
+// Long sequences, of more than a 16th of the tokens, start before all others, in
+// `kFront` groups of blocks in front of the grid.
+constexpr int kFront = 15;
+
+__device__ __forceinline__ bool is_long(const RaggedArgs& A, int i) {
+    const int t0 = A.offsets[i], t1 = A.offsets[i + 1];
+    return t0 >= 0 && t1 <= A.total && t1 > t0 && t1 - t0 > A.total / 16;
+}
+
+// How many of them have an index below `seq`.
+__device__ __forceinline__ int longs_before(const RaggedArgs& A, int seq, int lane) {
+    int n = 0;
+    for (int c = 0; c < seq; c += 64) n += __popcll(__ballot(c + lane < seq && is_long(A, min(c + lane, seq))));
+    return n;
+}
+
+// The r-th one, or -1.
+__device__ __forceinline__ int long_sequence(const RaggedArgs& A, int r, int lane) {
+    for (int c = 0; c < A.n_seqs; c += 64) {
+        const bool mine = c + lane < A.n_seqs && is_long(A, min(c + lane, A.n_seqs - 1));
+        const unsigned long long m = __ballot(mine);
+        if (r < __popcll(m)) return c + __ffsll(__ballot(mine && __popcll(m & ((1ull << lane) - 1)) == r)) - 1;
+        r -= __popcll(m);
+    }
+    return -1;
+}
+
 }  // namespace
 
 template <int KIND, int V, typename QT>
 __global__ __launch_bounds__(V / 16 * 64) __attribute__((amdgpu_waves_per_eu(6)))
-void recur_kernel(RaggedArgs A) {
+void recur_kernel(RaggedArgs A, int front) {
     constexpr int K = kK;
     constexpr int NT = V / 16 * 64;
     constexpr bool DELTA = KIND != SKSSM_MAMBA2;
@@ -68,11 +95,14 @@ void recur_kernel(RaggedArgs A) {
     const int lr = lane & 15;
     const int lq = lane >> 4;
     const int v0 = 16 * w;
-    const int seq = blockIdx.x / A.H;
-    const int h = blockIdx.x - seq * A.H;
+    const int group = blockIdx.x / A.H;
+    const int h = blockIdx.x - group * A.H;
+    const int seq = group < front ? long_sequence(A, group, lane) : group - front;
+    if (seq < 0) return;
     const int hk = h / A.share;
     const SeqSpan sp = seq_span_uniform(A, seq);
     if (!sp.live) return;
+    if (front && group >= front && is_long(A, seq) && longs_before(A, seq, lane) < front) return;  // in front
 
     f32x4 s[8];
     const int svo = (4 * lq * V + v0 + lr) * 4;
@@ -161,7 +191,11 @@ void recur_kernel(RaggedArgs A) {
 
 template <int KIND, int V, typename QT>
 static hipError_t launch_recur_t(const RaggedArgs& a, hipStream_t s) {
-    hipLaunchKernelGGL((recur_kernel<KIND, V, QT>), dim3(a.n_seqs * a.H), dim3(V / 16 * 64), 0, s, a);
+    // Where there can be a long sequence and more waves are to come than the CUs hold:
+    // us without and with, 96 sequences of a KDA layer, 480 tokens, one of 57: 138, 98;
+    // 192 of a Mamba-2 layer, 500 tokens, one of 99 that starts early anyway: 372, 379.
+    const int front = long(a.max_len) * 16 > a.total && long(a.n_seqs) * a.H * (V / 16) > 256 * 24 ? kFront : 0;
+    hipLaunchKernelGGL((recur_kernel<KIND, V, QT>), dim3((a.n_seqs + front) * a.H), dim3(V / 16 * 64), 0, s, a, front);
     return hipGetLastError();
 }
 
@@ -206,7 +240,7 @@ sketchssm_status ragged_args(const sketchssm_shape* shape, const float* S0, int3
         if ((shape->kind != SKSSM_MAMBA2) != (beta != nullptr)) return SKSSM_EINVAL;
     }
     // block indices, and elements of the first states, stay below 2^31
-    if (double(n_seqs) * shape->H >= 2147483648.0) return SKSSM_ESHAPE;
+    if ((double(n_seqs) + kFront) * shape->H >= 2147483648.0) return SKSSM_ESHAPE;
     if (S0 && double(n_rows0) * shape->H * shape->K * shape->V >= 2147483648.0) return SKSSM_ESHAPE;
     const void* ptrs[] = {S0, S, rows0, rows, offsets, q, k, v, a, beta, y};
     for (const void* ptr : ptrs)
