@@ -60,3 +60,18 @@ def test_every_other_sequence_out_of_range(n, call):
     Sr = torch.stack([ref.run("gdn", d, [T], d["S0"][i:i + 1])[1][0] for i in range(0, n, 2)])
     assert ref.slab_err(S[::2], Sr) <= TOL
     assert (S[1::2] == 7).all()
+
+
+@pytest.mark.timeout(300)
+@pytest.mark.parametrize("kind", KINDS)
+@pytest.mark.parametrize("longest", [15, 16, 17, 27, 28, 29])
+def test_lengths_where_the_form_changes(longest, kind):
+    """The longest prompt decides between the recurrent and the chunked form; a larger max_len changes no result
+    beyond the tolerance."""
+    lens, H, V = [longest, 1, 0, longest - 1], 4, 80
+    d = ref.draw(kind, "bf16", lens, H, H, V, seed=longest)
+    yr, Sr = ref.run(kind, d, lens, d["S0"])
+    for max_len in (longest, 64, 2 ** 31 - 1):
+        S, y = torch.empty(4, H, 128, V, device="cuda"), torch.empty(d["v"].shape, device="cuda")
+        _go("prefill", kind, H, V, d, d["S0"], None, S, None, d["offsets"].tolist(), max_len, y)
+        assert ref.slab_err(S, Sr) <= TOL and ref.slab_err(y, yr) <= TOL
