@@ -7,6 +7,7 @@ this module raises instead of falling back to anything.
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
 import os
 from typing import Optional
@@ -230,22 +231,29 @@ def sketchssm_decode_read_flush(plan: Plan, S, Z, frames, basis, q, k, v, a, bet
                                              _ptr(abuf), _ptr(bbuf), _ptr(y), _stream(stream)))
 
 
-def _want(name, x, dtype, shape, device):
-    """Refuse a tensor whose type, shape or device is not what the call takes (addresses pass through)."""
+def _arg(name, x, dtype, shape, device):
+    """Device address of a tensor, refused where its type, shape or device is not what the call takes (None and
+    addresses pass through)."""
     if x is None or isinstance(x, int):
-        return
-    if x.dtype != dtype or tuple(x.shape) != shape or x.device != device:
+        return x
+    if x.dtype is not dtype or x.shape != shape or x.device != device:
         raise ValueError(f"{name}: expected {dtype} {list(shape)} on {device}, "
                          f"got {x.dtype} {list(x.shape)} on {x.device}")
+    if not x.is_contiguous():
+        raise ValueError(f"{name}: expected a contiguous tensor")
+    return x.data_ptr()
+
+
+_AS_IS = contextlib.nullcontext()
 
 
 def _on_device(device, stream):
     """The context in which a call on tensors of `device` is made: that device current, if it is not."""
-    import contextlib
-
     import torch
-    if device.index is None or device.index == torch.cuda.current_device():
-        return contextlib.nullcontext()
+    if device.type != "cuda":
+        raise ValueError("expected a device tensor")
+    if device.index == torch.cuda.current_device():
+        return _AS_IS
     if stream is not None and not isinstance(stream, int) and stream.device != device:
         raise ValueError(f"the stream is on {stream.device}, the tensors are on {device}")
     return torch.cuda.device(device)
@@ -254,11 +262,9 @@ def _on_device(device, stream):
 def owned_by(stream, device):
     """The context in which a tensor for calls on `stream` is allocated: it belongs to that stream, so torch's
     allocator gives its memory to nothing else before the work queued there is done."""
-    import contextlib
-
     import torch
     if stream is None:
-        return contextlib.nullcontext()
+        return _AS_IS
     return torch.cuda.stream(torch.cuda.ExternalStream(stream, device=device) if isinstance(stream, int) else stream)
 
 
@@ -271,24 +277,15 @@ def _ragged(shape, S0, rows0, S, rows, offsets, max_len, q, k, v, a, beta, y):
     if offsets.dim() != 1 or offsets.numel() < 1:
         raise ValueError("offsets: expected n_seqs + 1 entries")
     n = offsets.numel() - 1
-    _want("S", S, f32, (shape.B, H, K, V), dev)
-    if S0 is not None:
-        _want("S0", S0, f32, (S0.shape[0], H, K, V), dev)
-    for name, x in (("rows0", rows0), ("rows", rows)):
-        _want(name, x, i32, (n,), dev)
     if rows is None and n > shape.B:
         raise ValueError(f"rows: {n} sequences and {shape.B} state rows")
-    _want("offsets", offsets, i32, (n + 1,), dev)
-    _want("q", q, qkv, (T, Hk, K), dev)
-    _want("k", k, qkv, (T, Hk, K), dev)
-    _want("v", v, qkv, (T, H, V), dev)
-    _want("a", a, f32, (T, H, K) if shape.kind == KIND["kda"] else (T, H), dev)
-    _want("beta", beta, f32, (T, H), dev)
-    _want("y", y, f32, (T, H, V), dev)
-    if S0 is None:
-        rows0 = None
-    return [ctypes.byref(shape), _ptr(S0), 0 if S0 is None else S0.shape[0], _ptr(rows0), _ptr(S), _ptr(rows),
-            _ptr(offsets), n, T, int(max_len), _ptr(q), _ptr(k), _ptr(v), _ptr(a), _ptr(beta), _ptr(y)]
+    n0 = 0 if S0 is None else S0.shape[0]
+    return [ctypes.byref(shape), _arg("S0", S0, f32, (n0, H, K, V), dev), n0,
+            _arg("rows0", rows0, i32, (n,), dev) if n0 else None, _arg("S", S, f32, (shape.B, H, K, V), dev),
+            _arg("rows", rows, i32, (n,), dev), _arg("offsets", offsets, i32, (n + 1,), dev), n, T, int(max_len),
+            _arg("q", q, qkv, (T, Hk, K), dev), _arg("k", k, qkv, (T, Hk, K), dev), _arg("v", v, qkv, (T, H, V), dev),
+            _arg("a", a, f32, (T, H, K) if shape.kind == KIND["kda"] else (T, H), dev),
+            _arg("beta", beta, f32, (T, H), dev), _arg("y", y, f32, (T, H, V), dev)]
 
 
 def sketchssm_rmw_seq(shape: Shape, S0, rows0, S, rows, offsets, max_len: int, q, k, v, a, beta, y, stream=None):
@@ -325,17 +322,15 @@ def sketchssm_gated_norm(shape: Shape, y, skip, D, z, weight, norm_heads: int, g
     dev, f32 = y.device, torch.float32
     qkv = torch.bfloat16 if shape.qkv == 0 else f32
     full = (y.shape[0], shape.H, shape.V)
-    _want("y", y, f32, full, dev)
-    for name, x in (("skip", skip), ("z", z), ("out", out)):
-        _want(name, x, qkv, full, dev)
-    _want("D", D, f32, (shape.H,), dev)
     w_heads = 1 if weight.dim() == 1 else weight.shape[0]
-    _want("weight", weight, f32, (shape.V,) if weight.dim() == 1 else (w_heads, shape.V), dev)
+    args = [_arg("y", y, f32, full, dev), _arg("skip", skip, qkv, full, dev), _arg("D", D, f32, (shape.H,), dev),
+            _arg("z", z, qkv, full, dev),
+            _arg("weight", weight, f32, (shape.V,) if weight.dim() == 1 else (w_heads, shape.V), dev)]
     with _on_device(dev, stream):
         _check("sketchssm_gated_norm",
-               lib().sketchssm_gated_norm(ctypes.byref(shape), _ptr(y), _ptr(skip), _ptr(D), _ptr(z), _ptr(weight),
-                                          w_heads, int(norm_heads), GATE[gate] if isinstance(gate, str) else int(gate),
-                                          float(eps), full[0], _ptr(out), _stream(stream)))
+               lib().sketchssm_gated_norm(ctypes.byref(shape), *args, w_heads, int(norm_heads),
+                                          GATE[gate] if isinstance(gate, str) else int(gate), float(eps), full[0],
+                                          _arg("out", out, qkv, full, dev), _stream(stream)))
 
 
 def sketchssm_stream_probe(src, read_bytes: int, dst, write_bytes: int, unroll: int = 8, blocks: int = 0,
