@@ -139,14 +139,29 @@ static hipError_t launch_norm_t(const NormArgs& a, hipStream_t s) {
     return hipGetLastError();
 }
 
+// The team and its steps: few idle lanes, and few barriers per value.  us of the team
+// chosen and of its neighbours, bf16, 64 tokens and then 2^23 values:
+//   width  128: 16 lanes  3.0, 13.8; 64 lanes 3.4, 33.5
+//   width  256: 16 x 2    4.0, 15.6; 64 lanes 3.1, 19.4: by the number of groups
+//   width  512: 64 lanes  3.1, 14.0; 256 lanes 3.3, 27.0; 16 x 4 6.3, 19.0
+//   width  640: 64 x 2    4.3, 19.4; 256 lanes 4.2, 24.7
+//   width 2048: 256 lanes 3.1, 14.0; 64 x 4 6.4, 19.3; 1024 lanes 3.8, 28.1
+//   width 2560: 256 x 2   4.2, 17.3; 1024 lanes 4.1, 24.3 (4096: 4.2, 16.2 and 3.9, 17.9)
+//   width 8192: 1024 lanes 4.2, 14.1; 256 x 4 6.5, 19.0
+//   width 10240: 1024 x 2 6.4, 20.0; 1024 x 4 9.0, 36.0
 template <typename QT>
 static hipError_t launch_norm(const NormArgs& a, hipStream_t s) {
     if (a.width <= 128) return launch_norm_t<16, 1, QT>(a, s);
+    if (a.width <= 256 && a.groups > 8192) return launch_norm_t<16, 2, QT>(a, s);
     if (a.width <= 512) return launch_norm_t<64, 1, QT>(a, s);
+    if (a.width <= 1024) return launch_norm_t<64, 2, QT>(a, s);
     if (a.width <= 2048) return launch_norm_t<256, 1, QT>(a, s);
+    if (a.width <= 4096) return launch_norm_t<256, 2, QT>(a, s);
     if (a.width <= 8192) return launch_norm_t<1024, 1, QT>(a, s);
+    if (a.width <= 16384) return launch_norm_t<1024, 2, QT>(a, s);
     return launch_norm_t<1024, 4, QT>(a, s);
 }
+static_assert(1024 * 4 * 8 >= kMaxHeads * 128, "the widest group");
 
 }  // namespace skssm
 
