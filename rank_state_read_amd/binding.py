@@ -114,7 +114,8 @@ def _ptr(x) -> Optional[int]:
 def _stream(stream):
     if stream is None:
         import torch
-        return torch.cuda.current_stream().cuda_stream
+        # the handle alone: a Stream object around it costs 2.5 us of a call's 14
+        return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device())
     if isinstance(stream, int):
         return stream
     return stream.cuda_stream
