@@ -49,10 +49,13 @@ __device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
     return __builtin_bit_cast(uint32_t, __builtin_convertvector((f32x2{lo, hi}), bf16x2));
 }
 
-// x = term 0 + term 1 + term 2 for 2 N consecutive values, each rounded to bf16.
-// (The remainders could be bf16 dot products with (-1, 0) and (0, -1), one
-// instruction instead of two, but those share the matrix unit: three beside a
-// matrix instruction take 40 cycles, three subtractions 21.)
+// x = term 0 + term 1 + term 2 exactly, for 2 N consecutive values: eight of an fp32
+// number's 24 bits each, cut off.  (Rounded terms leave smaller products to drop, the
+// states of the tests are then nearer by a fifth of 1e-7, but cost a conversion and a
+// shift where these cost a permutation and a mask: mamba2 batch 484 us against 467, gdn
+// long 614 against 584.  The remainders could be bf16 dot products with (-1, 0) and
+// (0, -1), one instruction instead of two, but those share the matrix unit: three
+// beside a matrix instruction take 40 cycles, three subtractions 21.)
 template <int N>
 __device__ __forceinline__ void split3(const float* f, uint32_t (&u)[3][N]) {
 #pragma unroll
@@ -60,10 +63,10 @@ __device__ __forceinline__ void split3(const float* f, uint32_t (&u)[3][N]) {
         float x0 = f[2 * i], x1 = f[2 * i + 1];
 #pragma unroll
         for (int p = 0; p < 3; ++p) {
-            const uint32_t h = pack_bf16(x0, x1);
-            u[p][i] = h;
-            x0 -= __uint_as_float(h << 16);
-            x1 -= __uint_as_float(h & 0xffff0000u);
+            const uint32_t b0 = __float_as_uint(x0), b1 = __float_as_uint(x1);
+            u[p][i] = __builtin_amdgcn_perm(b1, b0, 0x07060302);  // the upper halves
+            x0 -= __uint_as_float(b0 & 0xffff0000u);
+            x1 -= __uint_as_float(b1 & 0xffff0000u);
         }
     }
 }
