@@ -342,7 +342,11 @@ sketchssm_status sketchssm_rmw_seq(const sketchssm_shape* shape, const float* S0
 
 /*
  * The chunked form, for prompts: the same outputs up to rounding, in chunks of
- * tokens whose products run on the matrix cores.
+ * tokens whose products run on the matrix cores.  (Calls whose longest sequence is
+ * shorter than about a chunk take the recurrent form.)  A sequence's tokens share
+ * products with the 31 before and after them, so a value of inf or NaN in one can
+ * reach the outputs of up to 31 tokens before it too; other sequences are not
+ * touched by it.
  *   workspace  device scratch of at least sketchssm_prefill_workspace bytes
  *           (its contents need not be kept between calls; calls that may run at
  *           the same time need one each); NULL if that is 0

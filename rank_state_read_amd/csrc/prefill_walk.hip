@@ -7,6 +7,17 @@
 // little work per value, so its P, one per head, would cost more to move than to
 // form: the first launch leaves q_i . k_j per key head and the decays' products,
 // and the walk forms P from them.
+//
+// us of the two launches, bf16: GDN, 32 heads of 128, 16001 tokens of 9 sequences, 79
+// and 302; Mamba-2, 128 heads of 80, 16003 tokens of 7, 40 and 452; KDA, 32 heads of 128,
+// 8190 tokens of 4, 166 and 519.  The first one is bound by memory for GDN (213 MB of
+// records written, 3.2 TB/s with its reads), by latency and fp32 products for KDA.  The
+// walk runs its bf16 products at 673, 630 and 352 TFLOP/s (a large library product:
+// 1208) with the matrix units busy 46%, 32% and 27% of the time.  What bounds it is the
+// vector work beside them, which cuts the state and w into terms (350 vector
+// instructions to 96 products per wave and chunk of GDN), and for few or uneven
+// sequences the chain of a chunk's steps, as the longest sequence's chunks follow each
+// other (4.5 us each for KDA, 2.2 for GDN).
 #include <hip/hip_runtime.h>
 
 #include <algorithm>
@@ -158,14 +169,16 @@ __global__ __launch_bounds__(256) void prep_scalar_kernel(RaggedArgs A, char* ws
     const size_t tj = size_t(t0) + (valid ? j : 0);
     const float aj = valid ? A.a[tj * A.H + h] : 1.f;
     const float bj = !DELTA ? 1.f : valid ? A.beta[tj * A.H + h] : 0.f;
-    // operands of a row tile: bf16 steps of 32 channels, or fp32 steps of 4 (lane's
-    // channels 32 lq + s)
+    // operands of a row tile: 64 bytes of each of 16 rows a step, for one bf16 product
+    // of 32 channels or four fp32 products of 4 (lane's channels 16 s + 4 lq + e; with
+    // a lane's channels in one run, 32 lq .., a step touches 64 lines instead of 16 and
+    // 3001 tokens of 32 heads take 41 us instead of 30)
     constexpr int NV = BF ? 4 : 8;
     auto row = [&](const void* base, int m, u32x4 (&f)[NV]) {
         const size_t r = (size_t(t0) + min(16 * m + lr, clen - 1)) * A.Hk + hk;
-        const char* src = static_cast<const char*>(base) + (BF ? (r * kK + 8 * lq) * 2 : (r * kK + 32 * lq) * 4);
+        const char* src = static_cast<const char*>(base) + r * (kK * Vec8<QT>::kElemBytes) + 16 * lq;
 #pragma unroll
-        for (int s = 0; s < NV; ++s) f[s] = *reinterpret_cast<const u32x4*>(src + (BF ? 64 : 16) * s);
+        for (int s = 0; s < NV; ++s) f[s] = *reinterpret_cast<const u32x4*>(src + 64 * s);
     };
     auto mul = [&](const u32x4 (&x)[NV], const u32x4 (&y)[NV]) {
         f32x4 d = {0.f, 0.f, 0.f, 0.f};
@@ -1059,7 +1072,8 @@ void walk_kernel(RaggedArgs A, const char* ws, long slots, int V, Segments SG) {
 
 // The state at the end of each segment in turn: S_g = N_g + M_g S_{g-1}.  A block has
 // 16 value columns of one head, the state in LDS; wave w forms rows 32 w ..
-// 32 w + 31 with the fp32 matrix instruction.
+// 32 w + 31 with the fp32 matrix instruction.  Bound by the latency of a segment's
+// loads (3 segments, 32 heads of 128: 17 us; Mamba-2, 128 heads of 80: 13 us).
 template <bool DELTA>
 __global__ __launch_bounds__(256) void join_kernel(RaggedArgs A, int V, Segments SG) {
     constexpr int SS = 16 + 1;
