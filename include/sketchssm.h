@@ -322,7 +322,8 @@ sketchssm_status sketchssm_rmw_step(const sketchssm_shape* shape, float* S, cons
  * The lists are read on the device, so bad values are not reported: a sequence
  * whose row is outside 0 .. B-1, whose first row is n_rows0 or more, whose
  * offsets decrease or leave 0 .. total_tokens, or which is longer than max_len
- * is idle (nothing of it is read or written).  Where S0 is S (or overlaps it),
+ * is idle (nothing of it is read or written); sequences that overlap where
+ * offsets decrease have no defined results.  Where S0 is S (or overlaps it),
  * a sequence must start from its own row, from zero, or from a row that no
  * sequence of the call writes.  No window, plan, sketch or basis is involved:
  * form a written row's sketch with sketchssm_flush_seq (0 tokens) before its

@@ -139,7 +139,8 @@ __device__ __forceinline__ int slot_chunk(const RaggedArgs& A, long slot, int la
 // they come in; 100 of 160 tokens: 425, 428).
 __device__ __forceinline__ int seq_of_rank(const RaggedArgs& A, int r, int lane) {
     if (A.n_seqs > 64) return seq_long_first(A, r, lane);
-    const int len = lane < A.n_seqs ? max(A.offsets[lane + 1] - A.offsets[lane], 0) : -1;
+    const long n = lane < A.n_seqs ? long(A.offsets[lane + 1]) - A.offsets[lane] : -1;
+    const int len = int(min(max(n, lane < A.n_seqs ? 0l : -1l), long(A.total)));  // the lists may hold anything
     int rank = 0;
     for (int j = 0; j < A.n_seqs; ++j) {
         const int other = __builtin_amdgcn_readlane(len, j);

@@ -65,7 +65,8 @@ __device__ __forceinline__ int seq_long_first(const RaggedArgs& A, int r, int la
     const int bar = 2 * (A.total / A.n_seqs);
     auto longs = [&](int c) {  // of sequences c .. c + 63
         const int i = c + lane;
-        return __ballot(i < A.n_seqs && A.offsets[min(i, A.n_seqs - 1) + 1] > A.offsets[min(i, A.n_seqs - 1)] + bar);
+        const int at = min(i, A.n_seqs - 1);
+        return __ballot(i < A.n_seqs && long(A.offsets[at + 1]) - A.offsets[at] > bar);
     };
     int n = 0;
     for (int c = 0; c < A.n_seqs; c += 64) n += __popcll(longs(c));
