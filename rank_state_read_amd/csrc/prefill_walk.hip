@@ -33,7 +33,12 @@ constexpr int kC = 32;               // tokens per chunk
 constexpr int kTri = 3 * 2 * kFrag;  // T or P as A operands: three terms, two row tiles
 constexpr int kPlane = kC * kK * 2;  // one bf16 term of a chunk's keys or queries
 
-// A workspace record of a chunk and head: P, T, gamma and sigma.
+// A workspace record of a chunk and head: P, T, gamma and sigma, in pieces of 1 KB, 16
+// bytes per lane.  P and T are lower triangular, so lanes with 8 columns behind the
+// diagonal's hold zeros: those are neither written nor read, 10 of 16 lanes move.  (All
+// of them: gdn batch 361 us against 350.)
+__device__ __forceinline__ bool record_lane(int lane) { return lane >> 4 <= (lane & 15) >> 2; }
+
 struct Record {
     static constexpr int p = 0;
     static constexpr int t = kTri;
@@ -100,7 +105,8 @@ __device__ __forceinline__ void put_operands(char* dst, const float* m, const fl
         for (int i = 0; i < 8; ++i) f[i] *= scale ? scale[i] : 1.f;
         const Split p = split8(f);
 #pragma unroll
-        for (int e = 0; e < 3; ++e) *reinterpret_cast<u32x4*>(dst + (2 * e + o) * kFrag + lane * 16) = p.t[e];
+        for (int e = 0; e < 3; ++e)
+            if (record_lane(lane)) *reinterpret_cast<u32x4*>(dst + (2 * e + o) * kFrag + lane * 16) = p.t[e];
     }
 }
 
@@ -612,6 +618,7 @@ void walk_kernel(RaggedArgs A, const char* ws, long slots, int V, Segments SG) {
         voff[j] = (at / (16 * E * NW)) * int(cv.stride) + at % (16 * E * NW) + slice * NW * 16 * E;
     }
     __amdgpu_buffer_rsrc_t rsk, rsq, rsv, rsr;
+    const int reclane = record_lane(lane) ? lane * 16 : 1 << 30;  // out of range: reads as 0
     auto aim = [&](int rows) {  // the next chunk, `rows` tokens from its first on
         if (TERMS == 1) {
             const uint32_t n = ck.bytes(rows);
@@ -629,7 +636,7 @@ void walk_kernel(RaggedArgs A, const char* ws, long slots, int V, Segments SG) {
         if (j < NKQ) st[j] = load16(bw + j * NT < 8 ? rsk : rsq, kqoff[j]);
         else if (j >= NKQ + NRW) st[j] = load16(rsv, voff[j - NKQ - NRW]);
         else if (FORMP) st[j] = load16(rsr, DecayRecord::g + (lane & 15) * 16);
-        else st[j] = load16(rsr, RAT + (w + (j - NKQ) * NW) * kFrag + lane * 16);
+        else st[j] = load16(rsr, RAT + (w + (j - NKQ) * NW) * kFrag + reclane);
     };
     auto put = [&](int j, char* kq, char* v, char* rec) {
         const int o = lane * 16;
