@@ -8,10 +8,10 @@
 // form: the first launch leaves q_i . k_j per key head and the decays' products,
 // and the walk forms P from them.
 //
-// us of the two launches, bf16: GDN, 32 heads of 128, 16001 tokens of 9 sequences, 79
+// us of the two launches, bf16: GDN, 32 heads of 128, 16001 tokens of 9 sequences, 71
 // and 302; Mamba-2, 128 heads of 80, 16003 tokens of 7, 40 and 452; KDA, 32 heads of 128,
-// 8190 tokens of 4, 166 and 519.  The first one is bound by memory for GDN (213 MB of
-// records written, 3.2 TB/s with its reads), by latency and fp32 products for KDA.  The
+// 8190 tokens of 4, 166 and 519.  The first one is bound by the chain of a chunk's products and
+// substitution (and writes 130 MB of records for GDN), for KDA also by fp32 products.  The
 // walk runs its bf16 products at 673, 630 and 352 TFLOP/s (a large library product:
 // 1208) with the matrix units busy 46%, 32% and 27% of the time.  What bounds it is the
 // vector work beside them, which cuts the state and w into terms (350 vector
