@@ -12,10 +12,10 @@ namespace {
 // Whether a call takes the chunked kernels, else the recurrent one.  A chunk of 32
 // tokens costs nearly the same however many of them there are, the recurrent form
 // pays for each; three terms make the chunk dearer.  us chunked and recurrent at 16
-// and 24 tokens of 128 sequences: GDN, 32 heads of 128, 198, 201 and 207, 268; Mamba-2,
-// 128 heads of 80, 413, 381 and 433, 499; at 24 and 32 tokens: GDN with float32 keys
-// 276, 270 and 302, 338; KDA 339, 295 and 345, 364.  One sequence crosses at about the
-// same lengths (GDN, 16 and 20 tokens: 14.1, 17.9 and 14.2, 21.6).
+// and 24 tokens of 128 sequences: GDN, 32 heads of 128, 197, 196 and 202, 270; Mamba-2,
+// 128 heads of 80, 408, 383 and 422, 498; at 24 and 32 tokens: GDN with float32 keys
+// 276, 270 and 293, 344; KDA 339, 289 and 346, 371.  One sequence crosses at about the
+// same lengths (GDN, 16 and 20 tokens: 14.1, 17.8 and 14.4, 21.6).
 bool chunked(const sketchssm_shape& sh, int max_len, int total) {
     const bool one_term = sh.qkv == SKSSM_BF16 && sh.kind != SKSSM_KDA;
     return std::min(max_len, total) > (one_term ? 16 : 28);

@@ -135,7 +135,7 @@ __device__ __forceinline__ int slot_chunk(const RaggedArgs& A, long slot, int la
 // The sequence that the r-th group of blocks takes: the longest first, so that the
 // last blocks to start are short ones.  In full order up to 64 sequences, one per
 // lane; with more only the long ones go first (us of a GDN layer, 32 heads of 128,
-// 99 sequences of 100 tokens and behind them one of 6000: 539 against 630 in the order
+// 99 sequences of 100 tokens and behind them one of 6000: 529 against 630 in the order
 // they come in; 100 of 160 tokens: 425, 428).
 __device__ __forceinline__ int seq_of_rank(const RaggedArgs& A, int r, int lane) {
     if (A.n_seqs > 64) return seq_long_first(A, r, lane);

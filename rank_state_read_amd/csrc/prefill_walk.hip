@@ -1230,23 +1230,26 @@ size_t record_bytes(const sketchssm_shape& sh, long n_seqs, long total) {
 // with bf16 keys whose head has 5 or 6 waves: a CU takes one such block of one head,
 // as a SIMD takes 3 of these waves and a block's fifth and sixth go where the next
 // block's would; of two heads it takes 10 or 12 waves.  us apart and together, 16384
-// tokens of 64 sequences: 128 heads of 80 862, 608; 64 heads of 96 460, 361; but 64
+// tokens of 64 sequences: 128 heads of 80 895, 607; 64 heads of 96 461, 350; but 64
 // heads of 64, where a CU takes blocks of 4 waves anyway, 255, 281.  With less than
 // a pair for three CUs of four, blocks of one head: 512 tokens of one sequence, 128
-// heads of 80, 47, 59.
+// heads of 80, 41, 52.
 //
 // 128 columns are two blocks of 4 waves.  With three terms a CU takes one block, and
 // both form the same planes: one block of 8 waves has less to do, though a chunk of
 // it lasts longer, so it is taken where such blocks fill the CUs.  us with 4 and with
-// 8 waves, 32 heads: KDA, 16384 tokens of 64 sequences 1018, 748, 2000 tokens of 4 153,
-// 172; GDN with float32 keys 759, 580 and 110, 132.
+// 8 waves, 32 heads: KDA, 16384 tokens of 64 sequences 1052, 755, 2000 tokens of 4 143,
+// 158; GDN with float32 keys 727, 547 and 103, 121.
 //
 // Long sequences are cut into segments so that there is a block for each of the 256
 // CUs, in segments of 256 tokens or more, where that is worth the second pass.  One
-// sequence, us without and with: GDN, 32 heads of 128, 4 segments: 4096 tokens 251,
-// 181 and 1024 tokens 75, 76; 64 heads, 2 segments: 4096 tokens 285, 270 and 1024
-// tokens 79, 83; more segments than CUs need (64 heads, 4): 285, 298.  Mamba-2, 16
-// heads of 64, 4096 tokens, 16 segments: 233, 76.
+// sequence, us without and with: GDN, 32 heads of 128, 4 segments: 4096 tokens 256,
+// 172 and 1024 tokens 73, 70; 64 heads, 2 segments: 4096 tokens 283, 269 and 1024
+// tokens 78, 82; more segments than CUs need (64 heads, 4): 284, 297.  Mamba-2, 16
+// heads of 64, 4096 tokens, 16 segments: 229, 75.  Where the second pass is cheaper
+// beside the walk, half as many tokens will do: Mamba-2, which has no M, 128 heads of
+// 80, 1024 tokens 93, 70; KDA, 64 heads, 2 segments of 1024 tokens 186, 181; float32 GDN,
+// 32 heads of 96, 2 of 1293 224, 213.
 Cut cut_of(const sketchssm_shape& sh, long n_seqs, long total, long max_len) {
     const int nw = sh.V == 128 ? 4 : sh.V / 16;
     Cut cut = {nw, 1, {0, 1, nullptr}};
