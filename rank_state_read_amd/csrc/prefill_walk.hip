@@ -1165,7 +1165,7 @@ hipError_t launch_walk_b(const RaggedArgs& a, const char* ws, int V, const Segme
         if (sg.len) {
             hipError_t e = launch_walk_t<KIND, QT, NW, HB, true>(a, ws, V, sg, s);
             if (e != hipSuccess) return e;
-            const long blocks = long(a.n_seqs) * a.H * (V / 16);  // at most 8 x 4096
+            const long blocks = long(a.n_seqs) * a.H * (V / 16);  // a few hundred thousand at most: cut_of
             hipLaunchKernelGGL((join_kernel<KIND != SKSSM_MAMBA2>), dim3(uint32_t(blocks)), dim3(256), 0, s, a, V, sg);
             e = hipGetLastError();
             if (e != hipSuccess) return e;
@@ -1249,7 +1249,10 @@ size_t record_bytes(const sketchssm_shape& sh, long n_seqs, long total) {
 // heads of 64, 4096 tokens, 16 segments: 229, 75.  Where the second pass is cheaper
 // beside the walk, half as many tokens will do: Mamba-2, which has no M, 128 heads of
 // 80, 1024 tokens 93, 70; KDA, 64 heads, 2 segments of 1024 tokens 186, 181; float32 GDN,
-// 32 heads of 96, 2 of 1293 224, 213.
+// 32 heads of 96, 2 of 1293 224, 213.  Among many short ones most blocks of both passes
+// have no segment; a sequence of 8192 tokens behind others of 8, GDN, 8 heads: 64
+// others (16640 blocks) 489, 199, 256 others (65792) 498, 638; 32 heads: 64 others (8320)
+// 535, 497, 256 others (32896) 610, 941.
 Cut cut_of(const sketchssm_shape& sh, long n_seqs, long total, long max_len) {
     const int nw = sh.V == 128 ? 4 : sh.V / 16;
     Cut cut = {nw, 1, {0, 1, nullptr}};
@@ -1265,7 +1268,7 @@ Cut cut_of(const sketchssm_shape& sh, long n_seqs, long total, long max_len) {
     if (sh.V == 128 && (sh.kind == SKSSM_KDA || sh.qkv == SKSSM_F32) && longest * sh.H >= 256) cut.waves = 8;
     const long count = std::min(256 / (longest * per_seq), most);
     if (count < 2 || count * len < (sh.kind == SKSSM_GDN && sh.qkv == SKSSM_BF16 ? 4096 : 2048)) return cut;
-    if (n_seqs * per_seq * count > 4096) return cut;  // among many short ones most blocks would have no segment
+    if (n_seqs * per_seq * count > 20000) return cut;  // most blocks would have no segment
     cut.sg.len = int((len + count - 1) / count + kC - 1) / kC * kC;
     cut.sg.most = int((len + cut.sg.len - 1) / cut.sg.len);
     return cut;

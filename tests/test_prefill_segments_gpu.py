@@ -176,3 +176,14 @@ def test_many_heads_of_a_key_head(H, Hk, V):
 def test_many_sequences(kind, qkv):
     """More sequences than a wave has lanes, and enough of them for blocks of all 128 value columns."""
     _check(kind, qkv, [33 + (7 * i) % 40 for i in range(70)], 6, 6, 128, zero=range(0, 70, 3), cut=False)
+
+
+@pytest.mark.timeout(300)
+@pytest.mark.parametrize("kind", KINDS)
+def test_long_sequence_among_many_short_ones(kind):
+    """One sequence cut into segments, the others shorter than one, more of them than a wave has lanes; first, in the
+    middle and last."""
+    for at in (0, 40, 69):
+        lens = [(3 * i) % 11 for i in range(70)]
+        lens[at] = 2049
+        _check(kind, "bf16", lens, 4, 2, 80, zero=range(0, 70, 4))
