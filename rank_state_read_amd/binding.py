@@ -253,10 +253,10 @@ def _on_device(device, stream):
     import torch
     if device.type != "cuda":
         raise ValueError("expected a device tensor")
-    if device.index == torch.cuda.current_device():
-        return _AS_IS
     if stream is not None and not isinstance(stream, int) and stream.device != device:
         raise ValueError(f"the stream is on {stream.device}, the tensors are on {device}")
+    if device.index == torch.cuda.current_device():
+        return _AS_IS
     return torch.cuda.device(device)
 
 
@@ -309,6 +309,8 @@ def sketchssm_prefill(shape: Shape, S0, rows0, S, rows, offsets, max_len: int, q
             if need:
                 with owned_by(stream, S.device):
                     workspace = torch.empty(need, dtype=torch.uint8, device=S.device)
+        elif workspace.device != S.device:
+            raise ValueError(f"workspace: expected a tensor on {S.device}, got one on {workspace.device}")
         size = 0 if workspace is None else workspace.numel() * workspace.element_size()
         _check("sketchssm_prefill", lib().sketchssm_prefill(*args, _ptr(workspace), size, st))
 

@@ -129,6 +129,10 @@ def test_workspace_of_the_callers():
 
     with pytest.raises(lib.SketchSSMError):
         go(work[:need - 1])
+    with pytest.raises(ValueError):
+        go(torch.empty(need, dtype=torch.uint8))  # on the host
+    with pytest.raises(ValueError):
+        go(work[:2 * need:2])
     go(work[:need])
     torch.cuda.synchronize()
     yr, Sr = ref.run("gdn", d, lens, torch.zeros(2, H, 128, V, device="cuda"))
