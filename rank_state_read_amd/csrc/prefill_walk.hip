@@ -8,11 +8,11 @@
 // form: the first launch leaves q_i . k_j per key head and the decays' products,
 // and the walk forms P from them.
 //
-// us of the two launches, bf16: GDN, 32 heads of 128, 16001 tokens of 9 sequences, 71
-// and 302; Mamba-2, 128 heads of 80, 16003 tokens of 7, 40 and 452; KDA, 32 heads of 128,
-// 8190 tokens of 4, 166 and 519.  The first one is bound by the chain of a chunk's products and
-// substitution (and writes 130 MB of records for GDN), for KDA also by fp32 products.  The
-// walk runs its bf16 products at 673, 630 and 352 TFLOP/s (a large library product:
+// us of the two launches, bf16: GDN, 32 heads of 128, 16001 tokens of 9 sequences, 64
+// and 300; Mamba-2, 128 heads of 80, 16003 tokens of 7, 40 and 450; KDA, 32 heads of
+// 128, 8190 tokens of 4, 166 and 519.  The first one is bound by the chain of a chunk's
+// products and substitution (and moves 200 MB for GDN, 3.1 TB/s), for KDA also by fp32
+// products.  The walk runs its bf16 products at 673, 630 and 352 TFLOP/s (a large library product:
 // 1208) with the matrix units busy 46%, 32% and 27% of the time.  What bounds it is the
 // vector work beside them, which cuts the state and w into terms (350 vector
 // instructions to 96 products per wave and chunk of GDN), and for few or uneven
@@ -83,10 +83,6 @@ __device__ __forceinline__ void wave_sync() {
     __builtin_amdgcn_wave_barrier();
 }
 
-__device__ __forceinline__ float lane_value(float x, int i) {
-    return __uint_as_float(__builtin_amdgcn_readlane(__float_as_uint(x), i));
-}
-
 __device__ __forceinline__ u32x4 load16(__amdgpu_buffer_rsrc_t rs, int off) {
     return __builtin_bit_cast(u32x4, __builtin_amdgcn_raw_buffer_load_b128(rs, off, 0, 0));
 }
@@ -95,7 +91,16 @@ __device__ __forceinline__ u32x4 load16(__amdgpu_buffer_rsrc_t rs, int off) {
 // T and P of every chunk and head: one wave per (slot, head).
 // ---------------------------------------------------------------------------
 
-// A wave's matrix in LDS as A operands: three terms, two row tiles.
+// Row tile m of a matrix as A operand in three terms: f is row tile_row(m, lane % 16),
+// columns 8 (lane / 16) .. + 7.
+__device__ __forceinline__ void put_operand(char* dst, int m, const float* f, int lane) {
+    const Split p = split8(f);
+#pragma unroll
+    for (int e = 0; e < 3; ++e)
+        if (record_lane(lane)) *reinterpret_cast<u32x4*>(dst + (2 * e + m) * kFrag + lane * 16) = p.t[e];
+}
+
+// The same of a wave's matrix in LDS, its columns scaled.
 __device__ __forceinline__ void put_operands(char* dst, const float* m, const float* scale, int lane) {
 #pragma unroll
     for (int o = 0; o < 2; ++o) {
@@ -103,10 +108,7 @@ __device__ __forceinline__ void put_operands(char* dst, const float* m, const fl
         load8f(m + tile_row(o, lane & 15) * kGS + 8 * (lane >> 4), f);
 #pragma unroll
         for (int i = 0; i < 8; ++i) f[i] *= scale ? scale[i] : 1.f;
-        const Split p = split8(f);
-#pragma unroll
-        for (int e = 0; e < 3; ++e)
-            if (record_lane(lane)) *reinterpret_cast<u32x4*>(dst + (2 * e + o) * kFrag + lane * 16) = p.t[e];
+        put_operand(dst, o, f, lane);
     }
 }
 
@@ -152,13 +154,48 @@ __device__ __forceinline__ void put_t(char* rec, float* g, float bj, int lane) {
     put_operands(rec + Record::t, g, b, lane);
 }
 
-// One decay per token.  k_i . k_j and q_i . k_j first (bf16: exact products on the
-// bf16 instruction; fp32: the fp32 instruction), then the decays' products.
+// A chunk's decays a_i, one per lane of each half wave: gamma (the product up to token
+// i), sigma (after it) and put(g, F[g][i]) for the 8 groups g of four tokens, F[g][i] =
+// a_{4g+4} .. a_i, 1 for i = 4g + 3 and 0 before.  Decays may be 0: nothing is divided.
+template <typename Put>
+__device__ __forceinline__ void chunk_decays(float av, int lane, float& gamma, float& sigma, Put put) {
+    const int q = lane & 3, b = (lane & 31) >> 2;
+    // within the group: products up to token i, and after it
+    const float p1 = dpp_mov<0x90>(av);  // quad_perm [0,0,1,2]
+    float up = q >= 1 ? av * p1 : av;
+    const float p2 = dpp_mov<0x40>(up);  // quad_perm [0,0,0,1]
+    up = q >= 2 ? up * p2 : up;
+    const float n1 = dpp_mov<0xF9>(av);  // quad_perm [1,2,3,3]
+    const float s1 = q <= 2 ? n1 : 1.f;
+    const float n2 = dpp_mov<0xF9>(s1);
+    float down = q <= 1 ? s1 * n2 : s1;
+    const float n3 = dpp_mov<0xFF>(av);  // quad_perm [3,3,3,3]
+    down = q == 0 ? down * n3 : down;
+    float r = up, sg = down;
+#pragma unroll
+    for (int g = 7; g >= 0; --g) {
+        const float bg = __shfl(up, (lane & 32) + 4 * g + 3, 64);
+        put(g, g > b ? 0.f : g == b ? (q == 3 ? 1.f : 0.f) : r);
+        r = g < b ? r * bg : r;
+        sg = g > b ? sg * bg : sg;
+    }
+    gamma = r;
+    sigma = sg;
+}
+
+// One decay per token.  A wave's four tasks (row tile m, half o of the columns) give
+// k_j . k_i and k_j . q_i with lane = row i = tile_row(m, lr) and columns j = 8 lq + 4 o
+// + r (bf16: exact products on the bf16 instruction; fp32: the fp32 instruction), the
+// layout of P as an operand, and the decays between follow from F as in the walk.
+// Only A goes through LDS, for its inverse.  (With both there, their rows multiplied by
+// the decays one token after the other, 16001 tokens of 32 heads take 71 us instead of
+// 64, and 77 tokens 8.7 instead of 6.8.)
 template <bool DELTA, typename QT>
 __global__ __launch_bounds__(256) void prep_scalar_kernel(RaggedArgs A, char* ws) {
     constexpr bool BF = std::is_same<QT, Bf16Tag>::value;
     typedef Record R;
-    __shared__ __align__(16) float tiles[4][2][kC * kGS];
+    __shared__ __align__(16) float tiles[4][DELTA ? kC * kGS : 4];
+    __shared__ __align__(16) float decays[4][9 * kC];  // F, a
     const int w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int lane = threadIdx.x & 63, lr = lane & 15, lq = lane >> 4;
     const long task = long(blockIdx.x) * 4 + w;
@@ -168,8 +205,8 @@ __global__ __launch_bounds__(256) void prep_scalar_kernel(RaggedArgs A, char* ws
     const int clen = slot_chunk<kC>(A, slot, lane, t0);
     if (clen == 0) return;  // no wave waits for another one below
 
-    float* g = tiles[w][0];
-    float* gq = tiles[w][1];
+    float* g = tiles[w];
+    float* f = decays[w];
     const int j = lane & 31;
     const bool valid = j < clen;
     const size_t tj = size_t(t0) + (valid ? j : 0);
@@ -178,13 +215,14 @@ __global__ __launch_bounds__(256) void prep_scalar_kernel(RaggedArgs A, char* ws
     // operands of a row tile: 64 bytes of each of 16 rows a step, for one bf16 product
     // of 32 channels or four fp32 products of 4 (lane's channels 16 s + 4 lq + e; with
     // a lane's channels in one run, 32 lq .., a step touches 64 lines instead of 16 and
-    // 3001 tokens of 32 heads take 41 us instead of 30)
+    // 3001 tokens of 32 heads took 41 us instead of 30)
     constexpr int NV = BF ? 4 : 8;
-    auto row = [&](const void* base, int m, u32x4 (&f)[NV]) {
-        const size_t r = (size_t(t0) + min(16 * m + lr, clen - 1)) * A.Hk + hk;
-        const char* src = static_cast<const char*>(base) + r * (kK * Vec8<QT>::kElemBytes) + 16 * lq;
+    const Cursor<kC> ck(A.k, t0, A.Hk, hk, kK * Vec8<QT>::kElemBytes), cq(A.q, t0, A.Hk, hk, kK * Vec8<QT>::kElemBytes);
+    const __amdgpu_buffer_rsrc_t rk = ck.rsrc(clen), rq = cq.rsrc(clen);
+    auto row = [&](__amdgpu_buffer_rsrc_t rs, int m, u32x4 (&x)[NV]) {
+        const int at = tile_row(m, lr) * int(ck.stride) + 16 * lq;
 #pragma unroll
-        for (int s = 0; s < NV; ++s) f[s] = *reinterpret_cast<const u32x4*>(src + 64 * s);
+        for (int s = 0; s < NV; ++s) x[s] = load16(rs, at + 64 * s);
     };
     auto mul = [&](const u32x4 (&x)[NV], const u32x4 (&y)[NV]) {
         f32x4 d = {0.f, 0.f, 0.f, 0.f};
@@ -199,49 +237,48 @@ __global__ __launch_bounds__(256) void prep_scalar_kernel(RaggedArgs A, char* ws
         }
         return d;
     };
-    {
-        u32x4 kf[2][NV], qf[NV];
-        row(A.k, 0, kf[0]);
-        row(A.k, 1, kf[1]);
-#pragma unroll
-        for (int m = 0; m < 2; ++m) {
-            row(A.q, m, qf);
-#pragma unroll
-            for (int n = 0; n <= m; ++n) {
-                f32x4 d = {0.f, 0.f, 0.f, 0.f};
-                if (DELTA) d = mul(kf[m], kf[n]);
-                const f32x4 dq = mul(qf, kf[n]);
-#pragma unroll
-                for (int r = 0; r < 4; ++r) {
-                    const int at = (16 * m + 4 * lq + r) * kGS + 16 * n + lr;
-                    if (DELTA) g[at] = d[r];
-                    gq[at] = dq[r];
-                }
-            }
-        }
-    }
-    wave_sync();
-
-    // column j: the decays' products after token j one factor at a time (a decay may
-    // be 0, so nothing is divided); lanes 0 .. 31 take -A, lanes 32 .. 63 take P
+    u32x4 kf[2][NV], qf[NV];
+    row(rk, 0, kf[0]);
+    row(rk, 1, kf[1]);
+    row(rq, 0, qf);
     char* rec = ws + task * R::bytes;
     {
-        float* gt = lane < 32 ? g : gq;
-        float d = 0.f, run = 1.f, gam = 0.f;
-#pragma unroll
-        for (int i = 0; i < kC; ++i) {
-            const float ai = lane_value(aj, i), bi = lane_value(bj, i);
-            d = i == j ? 1.f : d * ai;
-            run *= ai;
-            gam = i == j ? run : gam;
-            const float x = d * gt[i * kGS + j];
-            gt[i * kGS + j] = lane < 32 ? (i > j ? -bi * x : 0.f) : (i >= j && valid ? x : 0.f);
-        }
-        reinterpret_cast<float*>(rec + R::g)[lane] = lane < 32 ? gam : (valid ? d : 0.f);
+        float gam, sig;
+        chunk_decays(aj, lane, gam, sig, [&](int b, float x) {
+            if (lane < 32) f[b * kC + j] = x;
+        });
+        if (lane < 32) f[8 * kC + j] = aj;
+        reinterpret_cast<float*>(rec + R::g)[lane] = lane < 32 ? gam : (valid ? sig : 0.f);
     }
     wave_sync();
-    put_operands(rec + R::p, gq, nullptr, lane);
-    if (DELTA) put_t(rec, g, bj, lane);
+#pragma unroll
+    for (int m = 0; m < 2; ++m) {
+        const int i = tile_row(m, lr);
+        const float bi = __shfl(bj, i, 64);
+        float z[8];
+#pragma unroll
+        for (int o = 0; o < 2; ++o) {
+            const int b = 2 * lq + o;
+            const f32x4 a4 = *reinterpret_cast<const f32x4*>(f + 8 * kC + 4 * b);
+            const f32x4 dq = mul(kf[o], qf);
+            f32x4 d = {0.f, 0.f, 0.f, 0.f};
+            if (DELTA) d = mul(kf[o], kf[m]);
+            float x = f[b * kC + i];
+#pragma unroll
+            for (int r = 3; r >= 0; --r) {
+                if (r < 3) x = i - 4 * b == r ? 1.f : x * a4[r + 1];
+                z[4 * o + r] = dq[r] * x;
+                d[r] *= i - 4 * b == r ? 0.f : -bi * x;
+            }
+            if (DELTA) *reinterpret_cast<f32x4*>(g + i * kGS + 4 * b) = d;
+        }
+        if (m == 0) row(rq, 1, qf);
+        put_operand(rec + R::p, m, z, lane);
+    }
+    if (DELTA) {
+        wave_sync();
+        put_t(rec, g, bj, lane);
+    }
 }
 
 // Mamba-2 with bf16 keys: one wave per (slot, key head) for q_i . k_j, formed
@@ -282,31 +319,15 @@ __global__ __launch_bounds__(256) void prep_mamba2_kernel(RaggedArgs A, char* ws
             }
         return;
     }
-    const int i = lane & 31, q = i & 3, b = i >> 2, h = 2 * (u - A.Hk) + (lane >> 5);
+    const int i = lane & 31, h = 2 * (u - A.Hk) + (lane >> 5);
     const bool in = i < clen && h < A.H;
     const float av = in ? A.a[(size_t(t0) + i) * A.H + h] : 1.f;
-    // within the group: products up to token i, and after it
-    const float p1 = dpp_mov<0x90>(av);  // quad_perm [0,0,1,2]
-    float up = q >= 1 ? av * p1 : av;
-    const float p2 = dpp_mov<0x40>(up);  // quad_perm [0,0,0,1]
-    up = q >= 2 ? up * p2 : up;
-    const float n1 = dpp_mov<0xF9>(av);  // quad_perm [1,2,3,3]
-    const float s1 = q <= 2 ? n1 : 1.f;
-    const float n2 = dpp_mov<0xF9>(s1);
-    float down = q <= 1 ? s1 * n2 : s1;
-    const float n3 = dpp_mov<0xFF>(av);  // quad_perm [3,3,3,3]
-    down = q == 0 ? down * n3 : down;
     char* rec = ws + (slot * A.H + h) * R::bytes;
     float* f = reinterpret_cast<float*>(rec + R::f) + i;
-    float r = up, sg = down;
-#pragma unroll
-    for (int g = 7; g >= 0; --g) {
-        const float bg = __shfl(up, (lane & 32) + 4 * g + 3, 64);
-        const float x = g > b ? 0.f : g == b ? (q == 3 ? 1.f : 0.f) : r;
+    float r, sg;
+    chunk_decays(av, lane, r, sg, [&](int g, float x) {
         if (h < A.H) f[g * kC] = x;
-        r = g < b ? r * bg : r;
-        sg = g > b ? sg * bg : sg;
-    }
+    });
     if (h < A.H) {
         reinterpret_cast<float*>(rec + R::a)[i] = av;
         reinterpret_cast<float*>(rec + R::g)[i] = r;
