@@ -156,7 +156,7 @@ def _own_seq(s):
     from rank_state_read_amd import sketchssm_prefill, sketchssm_rmw_seq
     c = s["case"]
     call = sketchssm_prefill if c["op"] == "prefill" else sketchssm_rmw_seq
-    call(_shape(c, c["n"]), s["S0"], s["rows0"], s["S"], s["rows"], s["offsets"], s["max_len"],
+    call(_shape(c, c["n"]), s["S0"], None if s["S0"] is None else s["rows0"], s["S"], s["rows"], s["offsets"], s["max_len"],
          s["q"], s["k"], s["v"], s["a"], s["beta"], s["y"])
     return {"y": s["y"], "S": s["S"]}
 
