@@ -281,8 +281,10 @@ def _ragged(shape, S0, rows0, S, rows, offsets, max_len, q, k, v, a, beta, y):
     if rows is None and n > shape.B:
         raise ValueError(f"rows: {n} sequences and {shape.B} state rows")
     n0 = 0 if S0 is None else S0.shape[0]
+    if rows0 is not None and n0 == 0:
+        raise ValueError("rows0: first rows of no states (S0 is None or empty)")
     return [ctypes.byref(shape), _arg("S0", S0, f32, (n0, H, K, V), dev), n0,
-            _arg("rows0", rows0, i32, (n,), dev) if n0 else None, _arg("S", S, f32, (shape.B, H, K, V), dev),
+            _arg("rows0", rows0, i32, (n,), dev), _arg("S", S, f32, (shape.B, H, K, V), dev),
             _arg("rows", rows, i32, (n,), dev), _arg("offsets", offsets, i32, (n + 1,), dev), n, T, int(max_len),
             _arg("q", q, qkv, (T, Hk, K), dev), _arg("k", k, qkv, (T, Hk, K), dev), _arg("v", v, qkv, (T, H, V), dev),
             _arg("a", a, f32, (T, H, K) if shape.kind == KIND["kda"] else (T, H), dev),

@@ -151,7 +151,8 @@ class SketchLayer:
                 y=None, workspace=None, stream=None) -> torch.Tensor:
         """Prompts of the listed rows (device int32; None: sequence i is row i), packed in one token axis:
         writes each row's state after its prompt and returns y of every token.  The rows start from zero
-        (``fresh``), go on from their own states, or start from rows0 of S0 (negative: zero)."""
+        (``fresh``), go on from their own states, or start from rows0 of S0 (negative: zero; with
+        ``fresh=False`` and no S0, of this layer's states)."""
         y = self._new(v.shape, torch.float32, stream) if y is None else y
         if S0 is None and not fresh:
             S0 = self.S
