@@ -378,8 +378,10 @@ typedef enum {
  * norm(x) = x / sqrt(mean(x^2) + eps) over groups of norm_heads consecutive heads.
  * Sums and products in fp32, one rounding to the qkv dtype at the end.
  *   y       device [n_tokens,H,V] fp32
- *   skip    device [n_tokens,H,V] qkv dtype or NULL (a Mamba-2 layer's D skip
- *           adds its v); D device [H] fp32, NULL without skip
+ *   skip    device [n_tokens,H,V] qkv dtype or NULL; D device [H] fp32, NULL
+ *           without skip.  (A Mamba-2 layer h <- exp(dt A) h + B (dt x)^T,
+ *           y = C^T h + D x has a = exp(dt A), k = B, v = dt x, q = C: its
+ *           skip is x, not v.)
  *   z       device [n_tokens,H,V] qkv dtype; NULL for SKSSM_GATE_NONE
  *   weight  device [H,V] fp32 (weight_heads = H) or [V] (weight_heads = 1, every
  *           head the same)

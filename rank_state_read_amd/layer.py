@@ -161,14 +161,16 @@ class SketchLayer:
         return y
 
     def set_norm(self, weight, norm_heads: int, gate: str, eps: float = 1e-5, D=None):
-        """The gated norm behind this layer's output: weight [H, V] or [V], D [H] the skip of v (Mamba-2) or None."""
+        """The gated norm behind this layer's output: weight [H, V] or [V], D [H] the skip (Mamba-2's
+        D x) or None."""
         f32 = torch.float32
         self.norm = (_to_device(weight, f32, self.device), int(norm_heads), gate, float(eps),
                      None if D is None else _to_device(D, f32, self.device))
 
     def gated_norm(self, y, z, v=None, out=None, stream=None) -> torch.Tensor:
         """The output that goes to the layer's projection: y [n, H, V] through ``set_norm``'s gated norm,
-        with the tokens' gate z and, where the layer has a skip, their values v."""
+        with the tokens' gate z and, where the layer has a skip, as v the values that D multiplies: a Mamba-2
+        layer's x, which is not the v = dt x of its update unless there is no step size."""
         if self.norm is None:
             raise ValueError("the layer has no norm: call set_norm first")
         weight, heads, gate, eps, D = self.norm

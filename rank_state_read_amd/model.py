@@ -11,7 +11,10 @@ C entry points: at window position 0 .. W-2 each layer's read, at W-1 each
 layer's last read fused into its flush.  All layers share one window phase,
 since every layer sees every token.  ``prefill`` runs the sequences' prompts
 through the layers first.  Where a layer has a gated norm (``set_norm``) and its
-token inputs hold a gate ``z``, its output is the normed one.
+token inputs hold a gate ``z``, its output is the normed one.  A norm with a skip
+``D`` (Mamba-2: y = S^T q + D x) takes the token's ``x``; without that key it takes
+``v``, which is x only where no step size is in it (a layer whose heads share keys
+holds dt in v = dt x).
 
 Only the recurrent part of a layer is here: the projections that produce a
 layer's q, k, v, decay and beta from the previous layer's output are not part of
@@ -67,7 +70,8 @@ class SketchModel:
 
     @staticmethod
     def _normed(L, y, d, stream):
-        return y if d.get("z") is None else L.gated_norm(y, d["z"], d["v"], stream=stream)
+        x = d["v"] if d.get("x") is None else d["x"]
+        return y if d.get("z") is None else L.gated_norm(y, d["z"], x, stream=stream)
 
     def decode_step(self, tokens: Sequence[Dict[str, Optional[torch.Tensor]]], stream=None) -> List[torch.Tensor]:
         """One token through every layer.  ``tokens[i]`` holds layer i's device
