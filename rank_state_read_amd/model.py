@@ -10,8 +10,9 @@ recurrent layer, all with the same window length) and runs that loop over the
 C entry points: at window position 0 .. W-2 each layer's read, at W-1 each
 layer's last read fused into its flush.  All layers share one window phase,
 since every layer sees every token.  ``prefill`` runs the sequences' prompts
-through the layers first.  Where a layer has a gated norm (``set_norm``) and its
-token inputs hold a gate ``z``, its output is the normed one.  A norm with a skip
+through the layers first.  A layer with a gated norm (``set_norm``) returns the
+normed output; its token inputs hold the gate ``z``, unless the norm has none.
+A layer without one returns its y.  A norm with a skip
 ``D`` (Mamba-2: y = S^T q + D x) takes the token's ``x``; without that key it takes
 ``v``, which is x only where no step size is in it (a layer whose heads share keys
 holds dt in v = dt x).
@@ -27,6 +28,7 @@ from typing import Dict, List, Optional, Sequence
 
 import torch
 
+from .binding import GATE
 from .layer import SketchLayer
 
 
@@ -57,8 +59,7 @@ class SketchModel:
         tokens offsets[b] .. offsets[b+1]-1 of layer i's packed inputs
         ``tokens[i]`` are sequence b's.  Writes every state and first sketch,
         restarts the window and returns the layers' outputs for all tokens."""
-        if len(tokens) != len(self.layers):
-            raise ValueError("one token input per layer")
+        self._check_tokens(tokens)
         if offsets.numel() != self.layers[0].B + 1:
             raise ValueError("one prompt per sequence")
         out = []
@@ -68,18 +69,29 @@ class SketchModel:
         self.start(stream)
         return out
 
+    def _check_tokens(self, tokens):
+        """Before any layer's state or window changes."""
+        if len(tokens) != len(self.layers):
+            raise ValueError("one token input per layer")
+        for i, (L, d) in enumerate(zip(self.layers, tokens)):
+            norm = getattr(L, "norm", None)
+            if norm is not None and (d.get("z") is None) != (norm[2] in ("none", GATE["none"])):
+                raise ValueError(f"layer {i}: " + ("no gate z for its gated norm" if d.get("z") is None else
+                                                   "a gate z, and its norm takes none"))
+
     @staticmethod
     def _normed(L, y, d, stream):
-        x = d["v"] if d.get("x") is None else d["x"]
-        return y if d.get("z") is None else L.gated_norm(y, d["z"], x, stream=stream)
+        z = d.get("z")
+        if getattr(L, "norm", z) is None:  # (a layer type of another kind without that attribute: by its tokens)
+            return y
+        return L.gated_norm(y, z, d["v"] if d.get("x") is None else d["x"], stream=stream)
 
     def decode_step(self, tokens: Sequence[Dict[str, Optional[torch.Tensor]]], stream=None) -> List[torch.Tensor]:
         """One token through every layer.  ``tokens[i]`` holds layer i's device
         inputs (``q``, ``k``, ``v``, ``a`` and, for the delta rule, ``beta``);
         returns the layers' output buffers (each layer's ``y``, overwritten by
-        the next step; with a gate ``z``, a new tensor of the normed output)."""
-        if len(tokens) != len(self.layers):
-            raise ValueError("one token input per layer")
+        the next step; of a layer with a norm, a new tensor of the normed output)."""
+        self._check_tokens(tokens)
         last = self.pos == self.W - 1
         out = []
         for L, d in zip(self.layers, tokens):
