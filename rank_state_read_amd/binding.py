@@ -266,7 +266,9 @@ def owned_by(stream, device):
     import torch
     if stream is None:
         return _AS_IS
-    return torch.cuda.stream(torch.cuda.ExternalStream(stream, device=device) if isinstance(stream, int) else stream)
+    if isinstance(stream, int):  # (a handle of 0, the null stream's, would make ExternalStream take one of torch's pool)
+        stream = torch.cuda.ExternalStream(stream, device=device) if stream else torch.cuda.default_stream(device)
+    return torch.cuda.stream(stream)
 
 
 def _ragged(shape, S0, rows0, S, rows, offsets, max_len, q, k, v, a, beta, y):
