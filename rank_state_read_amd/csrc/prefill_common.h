@@ -96,40 +96,74 @@ __device__ __forceinline__ int row_swizzle(int r) { return (r & 3) | (((r >> 3) 
 __device__ constexpr int kTermA[6] = {2, 0, 1, 1, 0, 0};
 __device__ constexpr int kTermB[6] = {0, 2, 1, 0, 1, 0};
 
-// Chunk c of a sequence has slot off / C + seq + c of the workspace: a sequence
-// of len tokens has at most (off + len) / C - off / C + 1 chunks, so sequences
-// that do not overlap never share a slot.
+// A sequence's chunks have consecutive slots of the workspace, behind those of the live
+// sequences before it in the list.  Sequences that do not overlap have at most
+// total / C + n_seqs chunks together, whatever their order.  (Slots counted from a
+// sequence's first token, t0 / C + seq, need no sums but hold only where the offsets
+// never decrease.)  Lists with sequences that overlap may ask for more: those that no
+// slot is left for take part no further.  Sums are modulo 2^32, which such lists alone
+// can reach.
 template <int C>
-__host__ __device__ inline long first_slot(long t0, long seq) {
-    return t0 / C + seq;
-}
-template <int C>
-inline long prefill_slots(long total, long n_seqs) {
+__host__ __device__ inline long prefill_slots(long total, long n_seqs) {
     return total / C + n_seqs;
 }
-
-// The sequence and chunk of a workspace slot: first token and tokens, none: 0.
 template <int C>
-__device__ __forceinline__ int slot_chunk(const RaggedArgs& A, long slot, int lane, int& t0) {
+__device__ __forceinline__ uint32_t chunks_of(uint32_t tokens) {
+    return (tokens + C - 1) / C;
+}
+template <int C>
+__device__ __forceinline__ bool has_room(const RaggedArgs& A, uint32_t first, uint32_t n) {
+    const uint32_t slots = uint32_t(prefill_slots<C>(A.total, A.n_seqs));
+    return first <= slots && n <= slots - first;
+}
+
+template <int CTRL, int ROWS>
+__device__ __forceinline__ uint32_t dpp_mov_u32(uint32_t x) {  // 0 where there is no source
+    return uint32_t(__builtin_amdgcn_update_dpp(0, int(x), CTRL, ROWS, 0xF, false));
+}
+// Sum over the lanes up to this one.
+__device__ __forceinline__ uint32_t wave_scan(uint32_t x) {
+    x += dpp_mov_u32<0x111, 0xF>(x);  // row_shr 1, 2, 4, 8
+    x += dpp_mov_u32<0x112, 0xF>(x);
+    x += dpp_mov_u32<0x114, 0xF>(x);
+    x += dpp_mov_u32<0x118, 0xF>(x);
+    x += dpp_mov_u32<0x142, 0xA>(x);  // row_bcast 15 into rows 1 and 3
+    x += dpp_mov_u32<0x143, 0xC>(x);  // row_bcast 31 into rows 2 and 3
+    return x;
+}
+
+// The sequence and chunk of a workspace slot: first token and tokens, none: 0.  One wave
+// of each slot notes its sequence's first slot for the launches behind (`note`).
+template <int C>
+__device__ __forceinline__ int slot_chunk(const RaggedArgs& A, long slot, int lane, bool note, int& t0) {
+    uint32_t before = 0;
     for (int s0 = 0; s0 < A.n_seqs; s0 += 64) {
         const int s = s0 + lane;
-        bool hit = false;
-        int tc = 0, cl = 0;
-        if (s < A.n_seqs) {
-            const SeqSpan sp = seq_span(A, s);
-            const long c = slot - first_slot<C>(sp.t0, s);
-            hit = sp.live && c >= 0 && c * C < sp.len;
-            tc = sp.t0 + int(c) * C;
-            cl = min(C, sp.len - int(c) * C);
-        }
+        const SeqSpan sp = seq_span(A, min(s, A.n_seqs - 1));
+        const uint32_t n = s < A.n_seqs && sp.live ? chunks_of<C>(sp.len) : 0;
+        const uint32_t upto = before + wave_scan(n), first = upto - n, c = uint32_t(slot) - first;
+        const bool hit = c < n && has_room<C>(A, first, n);
         const unsigned long long m = __ballot(hit);
         if (m) {
-            const int f = __ffsll(m) - 1;
-            t0 = __builtin_amdgcn_readlane(tc, f);
-            return __builtin_amdgcn_readlane(cl, f);
+            if (note && hit && c == 0) A.firsts[s] = first;
+            const int f = __ffsll(m) - 1, at = hit ? int(c) * C : 0;
+            t0 = __builtin_amdgcn_readlane(sp.t0 + at, f);
+            return __builtin_amdgcn_readlane(min(C, sp.len - at), f);
         }
+        before = __builtin_amdgcn_readlane(upto, 63);
     }
     return 0;
+}
+
+// The first slot of live sequence `seq` of `tokens` tokens.  (An empty one has none, and
+// one that found no room whatever the workspace held: out of range, or undefined as
+// the results of lists with overlaps are.)
+template <int C>
+__device__ __forceinline__ bool first_slot(const RaggedArgs& A, int seq, int tokens, uint32_t& first) {
+    first = 0;
+    if (tokens == 0) return true;
+    if (seq > 0) first = __builtin_amdgcn_readfirstlane(A.firsts[seq]);
+    return has_room<C>(A, first, chunks_of<C>(tokens));
 }
 
 // The sequence that the r-th group of blocks takes: the longest first, so that the

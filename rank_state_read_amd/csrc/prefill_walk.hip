@@ -202,7 +202,7 @@ __global__ __launch_bounds__(256) void prep_scalar_kernel(RaggedArgs A, char* ws
     const long slot = task / A.H;
     const int h = int(task - slot * A.H), hk = h / A.share;
     int t0 = 0;
-    const int clen = slot_chunk<kC>(A, slot, lane, t0);
+    const int clen = slot_chunk<kC>(A, slot, lane, h == 0, t0);
     if (clen == 0) return;  // no wave waits for another one below
 
     float* g = tiles[w];
@@ -293,7 +293,7 @@ __global__ __launch_bounds__(256) void prep_mamba2_kernel(RaggedArgs A, char* ws
     const long slot = task / units;
     const int u = int(task - slot * units);
     int t0 = 0;
-    const int clen = slot_chunk<kC>(A, slot, lane, t0);
+    const int clen = slot_chunk<kC>(A, slot, lane, u == 0, t0);
     if (clen == 0) return;  // no wave waits for another one below
     if (u < A.Hk) {
         const Cursor<kC> ck(A.k, t0, A.Hk, u, kK * 2), cq(A.q, t0, A.Hk, u, kK * 2);
@@ -361,7 +361,7 @@ __global__ __launch_bounds__(128) void prep_kda_kernel(RaggedArgs A, char* ws) {
     const long slot = task / A.H;
     const int h = int(task - slot * A.H), hk = h / A.share;
     int t0 = 0;
-    const int clen = slot_chunk<kC>(A, slot, lane, t0);
+    const int clen = slot_chunk<kC>(A, slot, lane, h == 0 && w == 0, t0);
     if (clen == 0) return;  // both waves
 
     // this lane's channel of every token; pre and suf: the decays' products over a
@@ -493,8 +493,10 @@ struct Segments {
     int len;     // tokens, a multiple of C; 0: none
     int most;    // segments of the longest sequence
     char* ends;  // per segment and head N [K, V], which becomes the state at its end, and M [K, K]
-    __device__ __forceinline__ float* n_of(long t0, int seq, int seg, int H, int h, int V) const {
-        return reinterpret_cast<float*>(ends) + ((t0 / len + seq + seg) * H + h) * long(kK * V + kK * kK);
+    // (first: the sequence's first chunk, in slots; those of sequences do not overlap)
+    __device__ __forceinline__ float* n_of(uint32_t first, int seq, int seg, int H, int h, int V) const {
+        return reinterpret_cast<float*>(ends) +
+               ((long(first / uint32_t(len / kC)) + seq + seg) * H + h) * long(kK * V + kK * kK);
     }
 };
 
@@ -561,6 +563,8 @@ void walk_kernel(RaggedArgs A, const char* ws, long slots, int V, Segments SG) {
     const int hk = h / A.share, seq = seq_of_rank(A, rest, lane);
     SeqSpan sp = seq_span_uniform(A, seq);
     if (!sp.live) return;
+    uint32_t first;
+    if (!first_slot<kC>(A, seq, sp.len, first)) return;
     // the segment's part of the sequence
     const int seq_t0 = sp.t0;
     bool at_end = true;
@@ -582,7 +586,7 @@ void walk_kernel(RaggedArgs A, const char* ws, long slots, int V, Segments SG) {
     const int svo = (8 * lq * V + col) * 4;
     // (the last segment's state may take S0's place while the first one starts: it starts from a copy)
     if (seg > 0 ? !ENDS : sp.row0 >= 0) {
-        const float* from = !ENDS && n > 1 ? SG.n_of(seq_t0, seq, seg > 0 ? seg - 1 : n - 1, A.H, h, V)
+        const float* from = !ENDS && n > 1 ? SG.n_of(first, seq, seg > 0 ? seg - 1 : n - 1, A.H, h, V)
                                            : A.S0 + (size_t(sp.row0) * A.H + h) * (kK * V);
         const __amdgpu_buffer_rsrc_t s0 = buffer_rsrc(from, kK * V * 4);
 #pragma unroll
@@ -598,7 +602,7 @@ void walk_kernel(RaggedArgs A, const char* ws, long slots, int V, Segments SG) {
                 S[t][r] = is_m && 32 * (t >> 1) + 8 * lq + 4 * (t & 1) + r == mcol ? 1.f : 0.f;
     }
     if (ENDS && seg == 0) {
-        const __amdgpu_buffer_rsrc_t s0 = buffer_rsrc(SG.n_of(seq_t0, seq, n - 1, A.H, h, V), kK * V * 4);
+        const __amdgpu_buffer_rsrc_t s0 = buffer_rsrc(SG.n_of(first, seq, n - 1, A.H, h, V), kK * V * 4);
 #pragma unroll
         for (int t = 0; t < 8; ++t)
 #pragma unroll
@@ -615,7 +619,7 @@ void walk_kernel(RaggedArgs A, const char* ws, long slots, int V, Segments SG) {
     Cursor<kC> cv(A.v, sp.t0, A.H, h, vrow), cy(A.y, sp.t0, A.H, h, uint32_t(V) * 4);
     Cursor<kC> ca(A.a, sp.t0, A.H, h, kK * 4);  // KDA
     constexpr int RB = FORMP ? DecayRecord::bytes : R::bytes;
-    const long slot0 = first_slot<kC>(seq_t0, seq) + (sp.t0 - seq_t0) / kC;
+    const long slot0 = long(first) + (sp.t0 - seq_t0) / kC;
     uint64_t crec = reinterpret_cast<uint64_t>(ws) + (slot0 * A.H + h) * RB;
 
     // Pieces of 1 KB, on their way from memory to LDS through a wave's registers:
@@ -1088,7 +1092,7 @@ void walk_kernel(RaggedArgs A, const char* ws, long slots, int V, Segments SG) {
     if (ENDS ? is_m && mcol >= kK : !at_end) return;
     const int cols = is_m ? kK : V;
     float* to = !ENDS ? A.S + (size_t(sp.row) * A.H + h) * (kK * V)
-                      : SG.n_of(seq_t0, seq, seg, A.H, h, V) + (is_m ? kK * V : 0);
+                      : SG.n_of(first, seq, seg, A.H, h, V) + (is_m ? kK * V : 0);
     if (ENDS && !DELTA && slice == 0 && w == 0 && lane == 0) to[kK * V] = through;
     const __amdgpu_buffer_rsrc_t so = buffer_rsrc(to, kK * cols * 4);
     const int wo = (8 * lq * cols + (is_m ? mcol : col)) * 4;
@@ -1115,11 +1119,13 @@ __global__ __launch_bounds__(256) void join_kernel(RaggedArgs A, int V, Segments
     const int h = rest % A.H, seq = rest / A.H;
     const SeqSpan sp = seq_span_uniform(A, seq);
     if (!sp.live) return;
+    uint32_t first;
+    if (!first_slot<kC>(A, seq, sp.len, first)) return;
     const int n = (sp.len + SG.len - 1) / SG.len;
     const int col = 16 * slice + lr, row = 32 * w + 4 * lq;  // rows row + 16 o + r
     f32x4 c[2];
     for (int g = 0; g < n - 1; ++g) {
-        float* at = SG.n_of(sp.t0, seq, g, A.H, h, V);
+        float* at = SG.n_of(first, seq, g, A.H, h, V);
         if (!DELTA) {
             const float m = at[kK * V];
 #pragma unroll
@@ -1244,6 +1250,9 @@ size_t record_bytes(const sketchssm_shape& sh, long n_seqs, long total) {
     return (n + 255) / 256 * 256;
 }
 
+// The workspace: the chunks' records, each sequence's first slot, the segments' ends.
+size_t list_bytes(long n_seqs) { return (size_t(n_seqs) * sizeof(uint32_t) + 255) / 256 * 256; }
+
 // How the walk is cut into blocks.  With few sequences the longest decides: blocks
 // are counted as though all were as long as it.
 //
@@ -1296,21 +1305,26 @@ Cut cut_of(const sketchssm_shape& sh, long n_seqs, long total, long max_len) {
 }
 
 size_t segment_bytes(const sketchssm_shape& sh, const Segments& sg, long n_seqs, long total) {
-    return sg.len ? size_t(total / sg.len + n_seqs) * sh.H * (kK * sh.V + kK * kK) * 4 : 0;
+    if (!sg.len) return 0;
+    return (size_t(prefill_slots<kC>(total, n_seqs)) / (sg.len / kC) + n_seqs) * sh.H * (kK * sh.V + kK * kK) * 4;
 }
 
 }  // namespace
 
 size_t walk_workspace(const sketchssm_shape& sh, long n_seqs, long total, long max_len) {
-    return record_bytes(sh, n_seqs, total) + segment_bytes(sh, cut_of(sh, n_seqs, total, max_len).sg, n_seqs, total);
+    return record_bytes(sh, n_seqs, total) + list_bytes(n_seqs) +
+           segment_bytes(sh, cut_of(sh, n_seqs, total, max_len).sg, n_seqs, total);
 }
 
-hipError_t launch_walk(const sketchssm_shape& sh, const RaggedArgs& a, char* ws, hipStream_t s) {
+hipError_t launch_walk(const sketchssm_shape& sh, const RaggedArgs& args, char* ws, hipStream_t s) {
     const bool bf = sh.qkv == SKSSM_BF16;
+    RaggedArgs a = args;
+    char* const list = ws + record_bytes(sh, a.n_seqs, a.total);
+    a.firsts = reinterpret_cast<uint32_t*>(list);
     const hipError_t e = bf ? launch_prep<Bf16Tag>(sh.kind, a, ws, s) : launch_prep<F32Tag>(sh.kind, a, ws, s);
     if (e != hipSuccess) return e;
     Cut cut = cut_of(sh, a.n_seqs, a.total, a.max_len);
-    cut.sg.ends = ws + record_bytes(sh, a.n_seqs, a.total);
+    cut.sg.ends = list + list_bytes(a.n_seqs);
     switch (sh.kind) {
         case SKSSM_MAMBA2:
             return bf ? launch_walk_v<SKSSM_MAMBA2, Bf16Tag>(a, ws, sh.V, cut, s)

@@ -23,6 +23,7 @@ struct RaggedArgs {
     float* y;
     int B0, B, n_seqs, total, max_len;
     int H, Hk, share;  // key/query heads; each serves `share` consecutive heads
+    uint32_t* firsts;  // chunked form: each sequence's first slot of the workspace
 };
 
 struct SeqSpan {

@@ -271,6 +271,7 @@ sketchssm_status ragged_args(const sketchssm_shape* shape, const float* S0, int3
     A.H = shape->H;
     A.Hk = kq_heads_of(*shape);
     A.share = shape->H / A.Hk;
+    A.firsts = nullptr;
     return SKSSM_OK;
 }
 
