@@ -10,10 +10,16 @@
 //
 // Products run on the bf16 matrix instruction (16x16x32, fp32 sums) and keep
 // fp32 precision: an fp32 operand x is written as hi + mid + lo, three bf16
-// numbers of 8 significant bits each.  q, k, v in bf16 are exact operands, so
-// their products with an fp32 operand take three instructions, products of two
-// fp32 operands six (the terms below 2^-24 are left out).  The fp32 matrix
-// instruction has 1/16 of the bf16 rate.
+// numbers of 8 significant bits each, without a rest.  q, k, v in bf16 are exact
+// operands, so their products with an fp32 operand take three instructions, products
+// of two fp32 operands six: hi hi, hi mid, mid hi, mid mid, hi lo, lo hi.  The rest is
+// left out, two products of mid and lo of up to 2^-22 of hi hi each and lo lo.  The A
+// operand's terms (T, P, the planes of keys and queries) are rounded, so that mid and lo
+// have either sign and what is left out has a mean of 0; the B operand's (the state, w),
+// cut on the chain of a walk's steps, are cut off.  Relative to the product, over normal
+// values: mean 0, mean square (1.8e-8)^2, at most 1.5e-7 (both cut off: mean -4.1e-8,
+// mean square (6.0e-8)^2, at most 4.0e-7; a rounding to fp32: (2.5e-8)^2, 6.0e-8).  The
+// fp32 matrix instruction has 1/16 of the bf16 rate.
 //
 // Value columns are independent of each other.  In the walk over a sequence's
 // chunks one wave owns 16 of them for all 128 key channels, so that nothing it
@@ -50,12 +56,11 @@ __device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
 }
 
 // x = term 0 + term 1 + term 2 exactly, for 2 N consecutive values: eight of an fp32
-// number's 24 bits each, cut off.  (Rounded terms leave smaller products to drop, the
-// states of the tests are then nearer by a fifth of 1e-7, but cost a conversion and a
-// shift where these cost a permutation and a mask: mamba2 batch 484 us against 467, gdn
-// long 614 against 584.  The remainders could be bf16 dot products with (-1, 0) and
-// (0, -1), one instruction instead of two, but those share the matrix unit: three
-// beside a matrix instruction take 40 cycles, three subtractions 21.)
+// number's 24 bits each, cut off.  (Rounded terms, as below, cost a conversion and a
+// shift where these cost a permutation and a mask; with those here too: mamba2 batch
+// 484 us against 467, gdn long 614 against 584.  The remainders could be bf16 dot
+// products with (-1, 0) and (0, -1), one instruction instead of two, but those share the
+// matrix unit: three beside a matrix instruction take 40 cycles, three subtractions 21.)
 template <int N>
 __device__ __forceinline__ void split3(const float* f, uint32_t (&u)[3][N]) {
 #pragma unroll
@@ -67,6 +72,23 @@ __device__ __forceinline__ void split3(const float* f, uint32_t (&u)[3][N]) {
             u[p][i] = __builtin_amdgcn_perm(b1, b0, 0x07060302);  // the upper halves
             x0 -= __uint_as_float(b0 & 0xffff0000u);
             x1 -= __uint_as_float(b1 & 0xffff0000u);
+        }
+    }
+}
+
+// The same with rounded terms, exact as well.  (A finite value beyond bf16's largest,
+// 3.39e38, becomes inf.)
+template <int N>
+__device__ __forceinline__ void split3_rounded(const float* f, uint32_t (&u)[3][N]) {
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+        float x0 = f[2 * i], x1 = f[2 * i + 1];
+#pragma unroll
+        for (int p = 0; p < 3; ++p) {
+            const uint32_t h = pack_bf16(x0, x1);
+            u[p][i] = h;
+            x0 -= __uint_as_float(h << 16);
+            x1 -= __uint_as_float(h & 0xffff0000u);
         }
     }
 }

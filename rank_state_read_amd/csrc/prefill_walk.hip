@@ -94,10 +94,12 @@ __device__ __forceinline__ u32x4 load16(__amdgpu_buffer_rsrc_t rs, int off) {
 // Row tile m of a matrix as A operand in three terms: f is row tile_row(m, lane % 16),
 // columns 8 (lane / 16) .. + 7.
 __device__ __forceinline__ void put_operand(char* dst, int m, const float* f, int lane) {
-    const Split p = split8(f);
+    uint32_t u[3][4];
+    split3_rounded<4>(f, u);
 #pragma unroll
     for (int e = 0; e < 3; ++e)
-        if (record_lane(lane)) *reinterpret_cast<u32x4*>(dst + (2 * e + m) * kFrag + lane * 16) = p.t[e];
+        if (record_lane(lane))
+            *reinterpret_cast<u32x4*>(dst + (2 * e + m) * kFrag + lane * 16) = u32x4{u[e][0], u[e][1], u[e][2], u[e][3]};
 }
 
 // The same of a wave's matrix in LDS, its columns scaled.
@@ -789,7 +791,7 @@ void walk_kernel(RaggedArgs A, const char* ws, long slots, int V, Segments SG) {
                 auto three = [&](char* dst, f32x2 x) {
                     const float f[2] = {x[0], x[1]};
                     uint32_t u[3][1];
-                    split3<1>(f, u);
+                    split3_rounded<1>(f, u);
 #pragma unroll
                     for (int e = 0; e < 3; ++e) *reinterpret_cast<uint32_t*>(dst + e * kPlane) = u[e][0];
                 };
