@@ -35,6 +35,9 @@
  *   - calls are asynchronous on `stream` (a hipStream_t; NULL = null stream);
  *   - arguments are checked on the host before anything is launched and a
  *     status is returned; nothing throws across this boundary;
+ *   - a call that would take 2^32 GPU threads or more gives SKSSM_ESHAPE (the ragged
+ *     calls from an n_seqs H V of about 2^30 on or, in chunks, a total_tokens H of
+ *     2^30; the gated norm from 2^28 norms over one head on);
  *   - all arrays are dense row-major with the layouts written beside them.
  * Supported shapes: K = 128, W = 16, V a multiple of 16 from 64 to 128 (the
  * Nano layer's 80, GDN/KDA's 128), 1 <= H <= 256,

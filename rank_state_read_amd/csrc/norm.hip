@@ -139,6 +139,7 @@ template <int LANES, int STEPS, typename QT>
 static hipError_t launch_norm_t(const NormArgs& a, hipStream_t s) {
     constexpr int NT = LANES > 256 ? LANES : 256;
     constexpr uint32_t teams = NT / LANES;
+    if (!launch_fits((a.groups + teams - 1) / teams, NT)) return hipErrorInvalidConfiguration;
     hipLaunchKernelGGL((gated_norm_kernel<LANES, STEPS, QT>), dim3((a.groups + teams - 1) / teams), dim3(NT), 0, s, a);
     return hipGetLastError();
 }
@@ -206,5 +207,6 @@ extern "C" sketchssm_status sketchssm_gated_norm(const sketchssm_shape* shape, c
     A.eps = eps;
     hipStream_t s = static_cast<hipStream_t>(stream);
     const hipError_t e = shape->qkv == SKSSM_BF16 ? launch_norm<Bf16Tag>(A, s) : launch_norm<F32Tag>(A, s);
+    if (e == hipErrorInvalidConfiguration) return SKSSM_ESHAPE;  // more threads than a launch takes
     return e == hipSuccess ? SKSSM_OK : SKSSM_ELAUNCH;
 }

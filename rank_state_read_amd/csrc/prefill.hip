@@ -53,6 +53,6 @@ extern "C" sketchssm_status sketchssm_prefill(const sketchssm_shape* shape, cons
     hipError_t e;
     if (!chunked(*shape, max_len, total_tokens)) e = launch_recur(*shape, A, s);
     else e = launch_walk(*shape, A, static_cast<char*>(workspace), s);
-    if (e == hipErrorInvalidConfiguration) return SKSSM_ESHAPE;  // more blocks than a launch takes
+    if (e == hipErrorInvalidConfiguration) return SKSSM_ESHAPE;  // more threads than a launch takes
     return e == hipSuccess ? SKSSM_OK : SKSSM_ELAUNCH;
 }

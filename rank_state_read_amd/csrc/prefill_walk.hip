@@ -1182,7 +1182,6 @@ hipError_t launch_walk_t(const RaggedArgs& a, const char* ws, int V, const Segme
     }
     const int slices = V / (16 * NW) + (ENDS && KIND != SKSSM_MAMBA2 ? (kK / 16 + NW - 1) / NW : 0);
     const long blocks = long(a.n_seqs) * (sg.len ? sg.most : 1) * ((a.H / HB + 7) / 8) * 8 * slices;
-    if (blocks >= (1l << 31)) return hipErrorInvalidConfiguration;
     hipLaunchKernelGGL((walk_kernel<KIND, QT, NW, HB, ENDS>), dim3(uint32_t(blocks)), dim3(HB * NW * 64), lds, s, a, ws, slots, V,
                        sg);
     return hipGetLastError();
@@ -1228,7 +1227,6 @@ hipError_t launch_walk_v(const RaggedArgs& a, const char* ws, int V, const Cut& 
 template <typename QT>
 hipError_t launch_prep(int kind, const RaggedArgs& a, char* ws, hipStream_t s) {
     const long tasks = prefill_slots<kC>(a.total, a.n_seqs) * a.H;
-    if (tasks >= (1l << 31)) return hipErrorInvalidConfiguration;
     const dim3 by4(uint32_t((tasks + 3) / 4));
     const long units = prefill_slots<kC>(a.total, a.n_seqs) * (a.Hk + (a.H + 1) / 2);
     if (kFormP<SKSSM_MAMBA2, QT> && kind == SKSSM_MAMBA2)
@@ -1306,6 +1304,17 @@ Cut cut_of(const sketchssm_shape& sh, long n_seqs, long total, long max_len) {
     return cut;
 }
 
+// Whether every launch of a call is within bounds, asked before the first one.  (The
+// segments' launches are of 20000 blocks and the same again for M at most.)
+bool fits(const sketchssm_shape& sh, const Cut& cut, long n_seqs, long total) {
+    const int per_xcd = (sh.H / cut.heads + 7) / 8;  // of the walk's blocks, of `heads` heads each
+    const int waves = sh.kind == SKSSM_KDA ? 2 * sh.H
+                      : sh.kind == SKSSM_MAMBA2 && sh.qkv == SKSSM_BF16 ? kq_heads_of(sh) + (sh.H + 1) / 2
+                                                                        : sh.H;  // of a chunk's preparation
+    return launch_fits(double(prefill_slots<kC>(total, n_seqs)) * waves + 4, 64) &&
+           launch_fits(double(n_seqs) * cut.sg.most * per_xcd * 8 * cut.heads, sh.V / 16 * 64);
+}
+
 size_t segment_bytes(const sketchssm_shape& sh, const Segments& sg, long n_seqs, long total) {
     if (!sg.len) return 0;
     return (size_t(prefill_slots<kC>(total, n_seqs)) / (sg.len / kC) + n_seqs) * sh.H * (kK * sh.V + kK * kK) * 4;
@@ -1314,18 +1323,20 @@ size_t segment_bytes(const sketchssm_shape& sh, const Segments& sg, long n_seqs,
 }  // namespace
 
 size_t walk_workspace(const sketchssm_shape& sh, long n_seqs, long total, long max_len) {
-    return record_bytes(sh, n_seqs, total) + list_bytes(n_seqs) +
-           segment_bytes(sh, cut_of(sh, n_seqs, total, max_len).sg, n_seqs, total);
+    const Cut cut = cut_of(sh, n_seqs, total, max_len);
+    if (!fits(sh, cut, n_seqs, total)) return 0;
+    return record_bytes(sh, n_seqs, total) + list_bytes(n_seqs) + segment_bytes(sh, cut.sg, n_seqs, total);
 }
 
 hipError_t launch_walk(const sketchssm_shape& sh, const RaggedArgs& args, char* ws, hipStream_t s) {
     const bool bf = sh.qkv == SKSSM_BF16;
     RaggedArgs a = args;
+    Cut cut = cut_of(sh, a.n_seqs, a.total, a.max_len);
+    if (!fits(sh, cut, a.n_seqs, a.total)) return hipErrorInvalidConfiguration;
     char* const list = ws + record_bytes(sh, a.n_seqs, a.total);
     a.firsts = reinterpret_cast<uint32_t*>(list);
     const hipError_t e = bf ? launch_prep<Bf16Tag>(sh.kind, a, ws, s) : launch_prep<F32Tag>(sh.kind, a, ws, s);
     if (e != hipSuccess) return e;
-    Cut cut = cut_of(sh, a.n_seqs, a.total, a.max_len);
     cut.sg.ends = list + list_bytes(a.n_seqs);
     switch (sh.kind) {
         case SKSSM_MAMBA2:

@@ -201,6 +201,7 @@ static hipError_t launch_recur_t(const RaggedArgs& a, hipStream_t s) {
     // us without and with, 96 sequences of a KDA layer, 480 tokens, one of 57: 138, 98;
     // 192 of a Mamba-2 layer, 500 tokens, one of 99 that starts early anyway: 372, 379.
     const int front = long(a.max_len) * 16 > a.total && long(a.n_seqs) * a.H * (V / 16) > 256 * 24 ? kFront : 0;
+    if (!launch_fits(double(a.n_seqs + front) * a.H, V / 16 * 64)) return hipErrorInvalidConfiguration;
     hipLaunchKernelGGL((recur_kernel<KIND, V, QT>), dim3((a.n_seqs + front) * a.H), dim3(V / 16 * 64), 0, s, a, front);
     return hipGetLastError();
 }
@@ -289,5 +290,7 @@ extern "C" sketchssm_status sketchssm_rmw_seq(const sketchssm_shape* shape, cons
                                             q, k, v, a, beta, y, &A);
     if (st != SKSSM_OK) return st;
     if (n_seqs == 0) return SKSSM_OK;
-    return launch_recur(*shape, A, static_cast<hipStream_t>(stream)) == hipSuccess ? SKSSM_OK : SKSSM_ELAUNCH;
+    const hipError_t e = launch_recur(*shape, A, static_cast<hipStream_t>(stream));
+    if (e == hipErrorInvalidConfiguration) return SKSSM_ESHAPE;  // more threads than a launch takes
+    return e == hipSuccess ? SKSSM_OK : SKSSM_ELAUNCH;
 }
