@@ -245,6 +245,14 @@ def _arg(name, x, dtype, shape, device):
     return x.data_ptr()
 
 
+def _int32(name, x):
+    """A number as a C call takes it (ctypes would cut it to 32 bits without a word)."""
+    x = int(x)
+    if not -2 ** 31 <= x < 2 ** 31:
+        raise ValueError(f"{name}: {x} does not fit 32 bits")
+    return x
+
+
 _AS_IS = contextlib.nullcontext()
 
 
@@ -287,7 +295,7 @@ def _ragged(shape, S0, rows0, S, rows, offsets, max_len, q, k, v, a, beta, y):
         raise ValueError("rows0: first rows of no states (S0 is None or empty)")
     return [ctypes.byref(shape), _arg("S0", S0, f32, (n0, H, K, V), dev), n0,
             _arg("rows0", rows0, i32, (n,), dev), _arg("S", S, f32, (shape.B, H, K, V), dev),
-            _arg("rows", rows, i32, (n,), dev), _arg("offsets", offsets, i32, (n + 1,), dev), n, T, int(max_len),
+            _arg("rows", rows, i32, (n,), dev), _arg("offsets", offsets, i32, (n + 1,), dev), n, T, _int32("max_len", max_len),
             _arg("q", q, qkv, (T, Hk, K), dev), _arg("k", k, qkv, (T, Hk, K), dev), _arg("v", v, qkv, (T, H, V), dev),
             _arg("a", a, f32, (T, H, K) if shape.kind == KIND["kda"] else (T, H), dev),
             _arg("beta", beta, f32, (T, H), dev), _arg("y", y, f32, (T, H, V), dev)]
@@ -320,7 +328,8 @@ def sketchssm_prefill(shape: Shape, S0, rows0, S, rows, offsets, max_len: int, q
 
 
 def sketchssm_prefill_workspace(shape: Shape, n_seqs: int, total_tokens: int, max_len: int) -> int:
-    return int(lib().sketchssm_prefill_workspace(ctypes.byref(shape), int(n_seqs), int(total_tokens), int(max_len)))
+    return int(lib().sketchssm_prefill_workspace(ctypes.byref(shape), _int32("n_seqs", n_seqs),
+                                                 _int32("total_tokens", total_tokens), _int32("max_len", max_len)))
 
 
 def sketchssm_gated_norm(shape: Shape, y, skip, D, z, weight, norm_heads: int, gate, eps: float, out, stream=None):
