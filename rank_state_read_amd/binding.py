@@ -274,7 +274,7 @@ def owned_by(stream, device):
     import torch
     if stream is None:
         return _AS_IS
-    if isinstance(stream, int):  # (a handle of 0, the null stream's, would make ExternalStream take one of torch's pool)
+    if isinstance(stream, int):  # (with 0, the null stream's handle, ExternalStream takes a stream of torch's pool)
         stream = torch.cuda.ExternalStream(stream, device=device) if stream else torch.cuda.default_stream(device)
     return torch.cuda.stream(stream)
 
@@ -295,8 +295,9 @@ def _ragged(shape, S0, rows0, S, rows, offsets, max_len, q, k, v, a, beta, y):
         raise ValueError("rows0: first rows of no states (S0 is None or empty)")
     return [ctypes.byref(shape), _arg("S0", S0, f32, (n0, H, K, V), dev), n0,
             _arg("rows0", rows0, i32, (n,), dev), _arg("S", S, f32, (shape.B, H, K, V), dev),
-            _arg("rows", rows, i32, (n,), dev), _arg("offsets", offsets, i32, (n + 1,), dev), n, T, _int32("max_len", max_len),
-            _arg("q", q, qkv, (T, Hk, K), dev), _arg("k", k, qkv, (T, Hk, K), dev), _arg("v", v, qkv, (T, H, V), dev),
+            _arg("rows", rows, i32, (n,), dev), _arg("offsets", offsets, i32, (n + 1,), dev), n, T,
+            _int32("max_len", max_len), _arg("q", q, qkv, (T, Hk, K), dev), _arg("k", k, qkv, (T, Hk, K), dev),
+            _arg("v", v, qkv, (T, H, V), dev),
             _arg("a", a, f32, (T, H, K) if shape.kind == KIND["kda"] else (T, H), dev),
             _arg("beta", beta, f32, (T, H), dev), _arg("y", y, f32, (T, H, V), dev)]
 

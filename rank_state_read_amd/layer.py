@@ -49,6 +49,7 @@ class SketchLayer:
         self.layout = self.plan.export()
         dev = self.device
         self.S = torch.empty((B, H, K, V), dtype=torch.float32, device=dev)
+        dev = self.device = self.S.device  # "cuda" stands for the device that is current now
         if S_init is not None:
             self.S.copy_(_to_device(S_init, torch.float32, dev))
         nz = self.plan.z_elems
