@@ -16,7 +16,8 @@
 // left out, two products of mid and lo of up to 2^-22 of hi hi each and lo lo.  The A
 // operand's terms (T, P, the planes of keys and queries) are rounded, so that mid and lo
 // have either sign and what is left out has a mean of 0; the B operand's (the state, w),
-// cut on the chain of a walk's steps, are cut off.  Relative to the product, over normal
+// formed on the chain of a walk's steps, are cut off, and so is a P beside bf16 values,
+// where nothing is left out.  Relative to the product, over normal
 // values: mean 0, mean square (1.8e-8)^2, at most 1.5e-7 (both cut off: mean -4.1e-8,
 // mean square (6.0e-8)^2, at most 4.0e-7; a rounding to fp32: (2.5e-8)^2, 6.0e-8).  The
 // fp32 matrix instruction has 1/16 of the bf16 rate.
