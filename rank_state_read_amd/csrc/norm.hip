@@ -14,7 +14,7 @@
 // one head, a wave, a quarter block or a block for wider groups.
 //
 // Bound by memory: 16001 tokens of 32 heads of 128, gate behind the norm, 91 us, 5.8
-// TB/s (part of it from the last-level cache; a large copy runs at 4.6 TB/s); 256 tokens
+// TB/s (a plain stream that writes as much as it reads: 5.9 to 6.2); 256 tokens
 // of 128 heads of 80 in groups of 16 heads 7.9 us, mostly latency.
 #include <hip/hip_runtime.h>
 

@@ -10,10 +10,13 @@
 //
 // us of the two launches, bf16: GDN, 32 heads of 128, 16001 tokens of 9 sequences, 64
 // and 300; Mamba-2, 128 heads of 80, 16003 tokens of 7, 40 and 450; KDA, 32 heads of
-// 128, 8190 tokens of 4, 166 and 519.  The first one is bound by the chain of a chunk's
-// products and substitution (and moves 200 MB for GDN, 3.1 TB/s), for KDA also by fp32
-// products.  The walk runs its bf16 products at 673, 630 and 352 TFLOP/s (a large library product:
-// 1208) with the matrix units busy 46%, 32% and 27% of the time.  What bounds it is the
+// 128, 8190 tokens of 4, 166 and 520.  For GDN the first one moves 260 MB (131 of keys and
+// queries, 129 of records), 4.1 TB/s, two thirds of a plain stream's 6.2, while its waves
+// wait for data 32% and for their turn 52% of the time: the chain of a chunk's products
+// and substitution.  With a key head per head it is 400 MB in 73 us, 5.4 TB/s, nearly the
+// stream's.  For KDA fp32 products come on top.  The walk runs its bf16 products at 673,
+// 630 and 352 TFLOP/s (a large library product: 1208 to 1343, box to box) with the matrix
+// units busy 45%, 32% and 27% of the time.  What bounds it is the
 // vector work beside them, which cuts the state and w into terms (350 vector
 // instructions to 96 products per wave and chunk of GDN), and for few or uneven
 // sequences the chain of a chunk's steps, as the longest sequence's chunks follow each

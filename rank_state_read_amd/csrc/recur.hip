@@ -14,9 +14,10 @@
 // quarter-waves.  Tokens are staged in LDS eight at a time as fp32, so the
 // token loop has no barrier inside.
 //
-// Measured: 192 sequences of a Mamba-2 layer (128 heads of 80, 500 tokens) 376 us, 5.4
+// Measured: 192 sequences of a Mamba-2 layer (128 heads of 80, 500 tokens) 378 us, 5.4
 // TB/s of states and tokens; 96 of a KDA layer (32 heads of 128, 480 tokens, one
-// sequence of 57) 98 us, 4.4 TB/s; a copy of a large buffer runs at 4.6 TB/s.  One
+// sequence of 57) 98 us, 4.4 TB/s; float32 tokens 383 and 112 us.  A plain stream that
+// writes as much as it reads runs at 5.9 to 6.2 TB/s (torch's copy at 4.8 to 5.3).  One
 // token of one GDN layer's row takes 5.6 us, the latency of its loads.  Registers: 72,
 // six waves per SIMD (budgets of 5 and 4 with k kept between its two uses ran the same).
 #include <hip/hip_runtime.h>

@@ -142,7 +142,8 @@ class SketchLayer:
     def rmw_seq(self, offsets, max_len: int, q, k, v, a, beta=None, rows=None, S0=None, rows0=None, y=None,
                 stream=None) -> torch.Tensor:
         """A few tokens of each listed row, token by token on this layer's state (no window, no sketch).
-        The rows go on from their own states, or from rows0 of S0 (negative: zero)."""
+        The rows go on from their own states, or from rows0 of S0 (negative: zero).  A y taken here holds nothing
+        defined for tokens of no sequence."""
         y = self._new(v.shape, torch.float32, stream) if y is None else y
         _b.sketchssm_rmw_seq(self.shape, self.S if S0 is None else S0, rows0, self.S, rows, offsets, max_len, q, k, v,
                             a, beta, y, stream)
@@ -153,7 +154,8 @@ class SketchLayer:
         """Prompts of the listed rows (device int32; None: sequence i is row i), packed in one token axis:
         writes each row's state after its prompt and returns y of every token.  The rows start from zero
         (``fresh``), go on from their own states, or start from rows0 of S0 (negative: zero; with
-        ``fresh=False`` and no S0, of this layer's states)."""
+        ``fresh=False`` and no S0, of this layer's states).  A sequence longer than max_len is left out; a max_len
+        far above the longest length costs time.  A y taken here holds nothing defined for tokens of no sequence."""
         y = self._new(v.shape, torch.float32, stream) if y is None else y
         if S0 is None and not fresh:
             S0 = self.S

@@ -57,8 +57,9 @@ class SketchModel:
                 stream=None) -> List[torch.Tensor]:
         """The prompts of all sequences through every layer, from empty states:
         tokens offsets[b] .. offsets[b+1]-1 of layer i's packed inputs
-        ``tokens[i]`` are sequence b's.  Writes every state and first sketch,
-        restarts the window and returns the layers' outputs for all tokens."""
+        ``tokens[i]`` are sequence b's, at most max_len of them.  Writes every state
+        and first sketch, restarts the window and returns the layers' outputs
+        for all tokens."""
         self._check_tokens(tokens)
         if offsets.numel() != self.layers[0].B + 1:
             raise ValueError("one prompt per sequence")
