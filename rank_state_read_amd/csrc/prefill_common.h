@@ -77,20 +77,21 @@ __device__ __forceinline__ void split3(const float* f, uint32_t (&u)[3][N]) {
     }
 }
 
-// The same with rounded terms, exact as well.  (A finite value beyond bf16's largest,
-// 3.39e38, becomes inf.)
+// The same with rounded terms, exact as well: what two of them leave has at most 7 bits.
+// (A finite value beyond bf16's largest, 3.39e38, becomes inf.)
 template <int N>
 __device__ __forceinline__ void split3_rounded(const float* f, uint32_t (&u)[3][N]) {
 #pragma unroll
     for (int i = 0; i < N; ++i) {
         float x0 = f[2 * i], x1 = f[2 * i + 1];
 #pragma unroll
-        for (int p = 0; p < 3; ++p) {
+        for (int p = 0; p < 2; ++p) {
             const uint32_t h = pack_bf16(x0, x1);
             u[p][i] = h;
             x0 -= __uint_as_float(h << 16);
             x1 -= __uint_as_float(h & 0xffff0000u);
         }
+        u[2][i] = __builtin_amdgcn_perm(__float_as_uint(x1), __float_as_uint(x0), 0x07060302);
     }
 }
 
