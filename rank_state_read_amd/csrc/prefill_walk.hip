@@ -9,18 +9,18 @@
 // and the walk forms P from them.
 //
 // us of the two launches, bf16: GDN, 32 heads of 128, 16001 tokens of 9 sequences, 64
-// and 300; Mamba-2, 128 heads of 80, 16003 tokens of 7, 40 and 450; KDA, 32 heads of
-// 128, 8190 tokens of 4, 166 and 520.  For GDN the first one moves 260 MB (131 of keys and
+// and 292; Mamba-2, 128 heads of 80, 16003 tokens of 7, 41 and 446; KDA, 32 heads of
+// 128, 8190 tokens of 4, 162 and 508.  For GDN the first one moves 260 MB (131 of keys and
 // queries, 129 of records), 4.1 TB/s, two thirds of a plain stream's 6.2, while its waves
-// wait for data 32% and for their turn 52% of the time: the chain of a chunk's products
-// and substitution.  With a key head per head it is 400 MB in 73 us, 5.4 TB/s, nearly the
-// stream's.  For KDA fp32 products come on top.  The walk runs its bf16 products at 673,
-// 630 and 352 TFLOP/s (a large library product: 1208 to 1343, box to box) with the matrix
-// units busy 45%, 32% and 27% of the time.  What bounds it is the
+// wait for data 31% and for their turn 53% of the time: the chain of a chunk's products
+// and substitution.  With a key head per head it is 400 MB in 72 us, 5.5 TB/s, nearly the
+// stream's.  For KDA fp32 products come on top.  The walk runs its bf16 products at 690,
+// 635 and 355 TFLOP/s (a large library product: 1208 to 1343, box to box) with the matrix
+// units busy 45%, 31% and 27% of the time.  What bounds it is the
 // vector work beside them, which cuts the state and w into terms (350 vector
 // instructions to 96 products per wave and chunk of GDN), and for few or uneven
 // sequences the chain of a chunk's steps, as the longest sequence's chunks follow each
-// other (4.5 us each for KDA, 2.2 for GDN).
+// other (4.2 us each for KDA, 2.2 for GDN).
 #include <hip/hip_runtime.h>
 
 #include <algorithm>
