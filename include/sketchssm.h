@@ -411,6 +411,116 @@ sketchssm_status sketchssm_gated_norm(const sketchssm_shape* shape, const float*
                                       int32_t weight_heads, int32_t norm_heads, int32_t gate, float eps,
                                       int32_t n_tokens, void* out, void* stream);
 
+/*
+ * Trees of drafted tokens.  Of each listed sequence a tree of tokens is read over
+ * the row's cache, the state or sketch of the last flush and the window's
+ * held-back tokens, without changing any of it: y of a node is what the decode
+ * reads above would give after the window's tokens and the node's ancestors, root
+ * first, itself last (page "SketchSSM: Write to the Full State, Read from a Compact
+ * Sketch", Abstract: a decode step reads the stored sketch, held-back keys and
+ * values are exact).  The tokens that the model then accepts are appended to the
+ * window by sketchssm_tree_accept.
+ *   S, Z, frames  as in sketchssm_decode_read; a plan whose ranks are all 0 verifies
+ *           on the full state
+ *   kbuf, vbuf, abuf, bbuf   the window (layouts as in sketchssm_flush), read only;
+ *           bbuf NULL for Mamba-2, all NULL allowed without pos
+ *   pos     device [B] int32: state row b has pos[b] held-back tokens in slots
+ *           0 .. pos[b]-1; 0 .. W (a full window need not be flushed before); NULL:
+ *           no row has any
+ *   rows    device [n_seqs] int32: the state row of each sequence; several sequences
+ *           may name one row.  NULL: sequence i is row i
+ *   offsets device [n_seqs + 1] int32: sequence i's nodes are offsets[i] ..
+ *           offsets[i+1]-1 of the arrays below
+ *   n_seqs  >= 0; 0 does nothing
+ *   total_nodes  nodes in the arrays below; those of no sequence are not read and
+ *           their y is left as it was
+ *   max_nodes    0 .. 64, the caller's bound on a tree's nodes (how a call is cut into
+ *           blocks goes by it: one far above the largest tree costs time)
+ *   parents device [total_nodes] int32: each node's parent, counted within its
+ *           sequence, below the node's own index; -1: the node follows the window's
+ *           last token.  A chain of drafted tokens is -1, 0, 1, ...
+ *   q, k    device [total_nodes,Hk,K] qkv dtype;  v device [total_nodes,H,V]
+ *   a       device [total_nodes,H] fp32 (Mamba-2, GDN) or [total_nodes,H,K] (KDA)
+ *   beta    device [total_nodes,H] fp32 (GDN, KDA); NULL for Mamba-2
+ *   y       device [total_nodes,H,V] fp32, out
+ * The lists are read on the device, so bad values are not reported: a sequence
+ * whose row is outside 0 .. B-1, whose pos is outside 0 .. W, whose offsets
+ * decrease or leave 0 .. total_nodes or whose tree has more than max_nodes nodes is
+ * idle, and so is a node on whose path a parent is not below its child or below -1
+ * (its y is left as it was).  Values of tokens that are not on a node's path, an
+ * infinity or NaN among them, do not reach it, nor do window slots from pos on.
+ */
+sketchssm_status sketchssm_tree_read(const sketchssm_plan* plan, const float* S, const float* Z,
+                                     const float* frames, const void* kbuf, const void* vbuf,
+                                     const float* abuf, const float* bbuf, const int32_t* pos,
+                                     const int32_t* rows, const int32_t* offsets, int32_t n_seqs,
+                                     int32_t total_nodes, int32_t max_nodes, const int32_t* parents,
+                                     const void* q, const void* k, const void* v, const float* a,
+                                     const float* beta, float* y, void* stream);
+
+/*
+ * The accepted path of each tree is kept: the tokens from the root to node
+ * accepted[i] (counted within the sequence; negative: none) go, in that order, to
+ * row rows[i]'s window slots from pos on, and new_pos[row] is pos[row] plus their
+ * number.  A row must have room: flush it before (sketchssm_flush_seq with its
+ * pos[row] tokens, then pos[row] = 0) where pos + the path could exceed W.
+ *   kbuf, vbuf, abuf, bbuf   the window, in/out
+ *   pos     device [B] int32; new_pos device [B] int32, out, another array: also the
+ *           entries of rows that no sequence names are copied
+ *   rows    device [n_seqs] int32, each row at most once per call; NULL: sequence i
+ *           is row i
+ *   accepted  device [n_seqs] int32
+ *   offsets, parents, k, v, a, beta   as in sketchssm_tree_read
+ * Lists are read on the device: a sequence is idle, and its row's position stays,
+ * where an entry is out of range as above, where accepted[i] is not a node of it,
+ * where a parent on its path is none, and where its path does not fit the window.
+ */
+sketchssm_status sketchssm_tree_accept(const sketchssm_shape* shape, void* kbuf, void* vbuf,
+                                       float* abuf, float* bbuf, const int32_t* pos, int32_t* new_pos,
+                                       const int32_t* rows, const int32_t* offsets, int32_t n_seqs,
+                                       int32_t total_nodes, const int32_t* parents,
+                                       const int32_t* accepted, const void* k, const void* v,
+                                       const float* a, const float* beta, void* stream);
+
+typedef enum {
+    SKSSM_CACHE_I8 = 0,   /* whole numbers -127 .. 127; steps even over a key row */
+    SKSSM_CACHE_E4M3 = 1  /* 8-bit floats of 3 mantissa bits (OCP e4m3fn) */
+} sketchssm_cache_format;
+
+/*
+ * States cached in 8 bits: copies of listed rows' states, to start other sequences
+ * from (prefixes of prompts, forks), in a quarter of their bytes.  Each key row of V
+ * values has one scale s, a bf16 number: for SKSSM_CACHE_I8 the least s >= 2^-100
+ * with 127 s >= max|x| and codes x / s rounded to whole numbers, for
+ * SKSSM_CACHE_E4M3 the least power of two s >= 2^-100 with 448 s >= max|x| and
+ * codes x / s rounded to e4m3; both to nearest, ties to even.  A value reads back as
+ * code s, off by at most s / 2 (i8) or by 2^-4 of itself and 2^-10 s (e4m3).  A
+ * key row with an infinity or NaN gets the scale NaN and reads back as NaN; values
+ * whose code s passes fp32's range (states above 3.3e38) read back as infinity.
+ * The window is not stored: flush a row (sketchssm_flush_seq) before storing it.
+ * After a load, form the row's sketch with sketchssm_flush_seq (0 tokens).
+ *   S       device [B,H,K,V] fp32
+ *   codes   device [n_slots,H,K,V], one byte each: the slots of the cache
+ *   scales  device [n_slots,H,K] bf16
+ *   rows, slots   device [n] int32: pair i copies state row rows[i] to slot slots[i]
+ *           (store; each slot at most once per call) or slot slots[i] to row rows[i]
+ *           (load; each row at most once, a slot may feed several rows, and a
+ *           negative slot sets the row's state to zero).  NULL: pair i has row or
+ *           slot i
+ *   n       >= 0; 0 does nothing
+ *   format  sketchssm_cache_format
+ * A pair with a row outside 0 .. B-1 or a slot outside 0 .. n_slots-1 (load: of
+ * n_slots or more) is idle.  Of the shape, B, H, K and V are used.  The size of a
+ * cache is not limited to that of a layer's state.
+ */
+sketchssm_status sketchssm_cache_store(const sketchssm_shape* shape, const float* S, const int32_t* rows,
+                                       void* codes, uint16_t* scales, const int32_t* slots,
+                                       int32_t n_slots, int32_t n, int32_t format, void* stream);
+sketchssm_status sketchssm_cache_load(const sketchssm_shape* shape, const void* codes,
+                                      const uint16_t* scales, const int32_t* slots, int32_t n_slots,
+                                      float* S, const int32_t* rows, int32_t n, int32_t format,
+                                      void* stream);
+
 /* Static English text for a status code. */
 const char* sketchssm_status_string(sketchssm_status status);
 

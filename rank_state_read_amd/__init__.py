@@ -4,6 +4,7 @@ The HIP library does all the work; this package only loads it and marshals
 arguments.  Import fails loudly at first use if the library is not built.
 """
 from .binding import (  # noqa: F401
+    CACHE,
     DTYPE,
     GATE,
     KIND,
@@ -13,6 +14,8 @@ from .binding import (  # noqa: F401
     SketchSSMError,
     lib,
     make_shape,
+    sketchssm_cache_load,
+    sketchssm_cache_store,
     sketchssm_decode_read,
     sketchssm_decode_read_flush,
     sketchssm_decode_read_seq,
@@ -25,5 +28,7 @@ from .binding import (  # noqa: F401
     sketchssm_rmw_seq,
     sketchssm_rmw_step,
     sketchssm_stream_probe,
+    sketchssm_tree_accept,
+    sketchssm_tree_read,
     status_string,
 )

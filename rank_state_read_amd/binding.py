@@ -19,6 +19,7 @@ LIB_PATH = os.path.join(_HERE, "libsketchssm.so")
 
 KIND = {"mamba2": 0, "gdn": 1, "kda": 2}
 DTYPE = {"bf16": 0, "f32": 1}
+CACHE = {"i8": 0, "e4m3": 1}
 GATE = {"none": 0, "silu_first": 1, "silu": 2, "sigmoid": 3}
 STATUS = {0: "SKSSM_OK", 1: "SKSSM_EINVAL", 2: "SKSSM_ESHAPE", 3: "SKSSM_EALIGN",
           4: "SKSSM_ENOMEM", 5: "SKSSM_EDEVICE", 6: "SKSSM_ELAUNCH"}
@@ -63,6 +64,10 @@ _PROTOS = {
     "sketchssm_prefill_workspace": (ctypes.c_size_t, [ctypes.POINTER(Shape)] + [c_i32] * 3),
     "sketchssm_gated_norm": (c_i32, [ctypes.POINTER(Shape)] + [c_vp] * 5 + [c_i32] * 3 + [ctypes.c_float, c_i32]
                              + [c_vp] * 2),
+    "sketchssm_tree_read": (c_i32, [c_vp] * 11 + [c_i32] * 3 + [c_vp] * 8),
+    "sketchssm_tree_accept": (c_i32, [ctypes.POINTER(Shape)] + [c_vp] * 8 + [c_i32] * 2 + [c_vp] * 7),
+    "sketchssm_cache_store": (c_i32, [ctypes.POINTER(Shape)] + [c_vp] * 5 + [c_i32] * 3 + [c_vp]),
+    "sketchssm_cache_load": (c_i32, [ctypes.POINTER(Shape)] + [c_vp] * 3 + [c_i32] + [c_vp] * 2 + [c_i32] * 2 + [c_vp]),
     "sketchssm_status_string": (ctypes.c_char_p, [c_i32]),
     "sketchssm_stream_probe": (c_i32, [c_vp, ctypes.c_size_t, c_vp, ctypes.c_size_t, c_i32, c_i32, c_i32, c_vp]),
 }
@@ -348,6 +353,101 @@ def sketchssm_gated_norm(shape: Shape, y, skip, D, z, weight, norm_heads: int, g
                lib().sketchssm_gated_norm(ctypes.byref(shape), *args, w_heads, int(norm_heads),
                                           GATE[gate] if isinstance(gate, str) else int(gate), float(eps), full[0],
                                           _arg("out", out, qkv, full, dev), _stream(stream)))
+
+
+def _tree(shape, rows, offsets, parents, k, v, a, beta, kbuf, vbuf, abuf, bbuf, pos, dev):
+    """Checks of what both tree calls take: (window, lists, n_seqs, n_nodes, tokens)."""
+    import torch
+    i32, f32 = torch.int32, torch.float32
+    B, H, K, V, W, Hk = shape.B, shape.H, shape.K, shape.V, shape.W, shape.kq_heads or shape.H
+    T, kda = v.shape[0], shape.kind == KIND["kda"]
+    qkv = torch.bfloat16 if shape.qkv == 0 else f32
+    if offsets.dim() != 1 or offsets.numel() < 1:
+        raise ValueError("offsets: expected n_seqs + 1 entries")
+    n = offsets.numel() - 1
+    if rows is None and n > B:
+        raise ValueError(f"rows: {n} sequences and {B} state rows")
+    window = [_arg("kbuf", kbuf, qkv, (W, Hk, B, K), dev), _arg("vbuf", vbuf, qkv, (W, H, B, V), dev),
+              _arg("abuf", abuf, f32, (W, H, B, K) if kda else (W, H, B), dev), _arg("bbuf", bbuf, f32, (W, H, B), dev)]
+    lists = [_arg("pos", pos, i32, (B,), dev), _arg("rows", rows, i32, (n,), dev),
+             _arg("offsets", offsets, i32, (n + 1,), dev), _arg("parents", parents, i32, (T,), dev)]
+    tokens = [_arg("k", k, qkv, (T, Hk, K), dev), _arg("v", v, qkv, (T, H, V), dev),
+              _arg("a", a, f32, (T, H, K) if kda else (T, H), dev), _arg("beta", beta, f32, (T, H), dev)]
+    return window, lists, n, T, tokens
+
+
+def sketchssm_tree_read(plan: Plan, S, Z, frames, kbuf, vbuf, abuf, bbuf, pos, rows, offsets, max_nodes: int, parents, q, k,
+                        v, a, beta, y, stream=None):
+    """Trees of drafted tokens over listed rows' sketch (or state) and window; only y is written."""
+    import torch
+    sh, dev, f32 = plan.shape, v.device, torch.float32
+    window, lists, n, T, tokens = _tree(sh, rows, offsets, parents, k, v, a, beta, kbuf, vbuf, abuf, bbuf, pos, dev)
+    cache = [_arg("S", S, f32, (sh.B, sh.H, sh.K, sh.V), dev), _flat("Z", Z, plan.z_elems, dev),
+             _flat("frames", frames, plan.frame_elems, dev)]
+    qq = _arg("q", q, k.dtype, k.shape, dev)
+    yy = _arg("y", y, f32, v.shape, dev)
+    with _on_device(dev, stream):
+        _check("sketchssm_tree_read",
+               lib().sketchssm_tree_read(plan.handle, *cache, *window, *lists[:3], n, T, _int32("max_nodes", max_nodes),
+                                         lists[3], qq, *tokens, yy, _stream(stream)))
+
+
+def sketchssm_tree_accept(shape: Shape, kbuf, vbuf, abuf, bbuf, pos, new_pos, rows, offsets, parents, accepted, k, v, a,
+                          beta, stream=None):
+    """The accepted path of each tree, appended to its row's window; new_pos: every row's held-back tokens then."""
+    import torch
+    dev, i32 = v.device, torch.int32
+    window, lists, n, T, tokens = _tree(shape, rows, offsets, parents, k, v, a, beta, kbuf, vbuf, abuf, bbuf, pos, dev)
+    new = _arg("new_pos", new_pos, i32, (shape.B,), dev)
+    acc = _arg("accepted", accepted, i32, (n,), dev)
+    with _on_device(dev, stream):
+        _check("sketchssm_tree_accept",
+               lib().sketchssm_tree_accept(ctypes.byref(shape), *window, lists[0], new, *lists[1:3], n, T, lists[3], acc,
+                                           *tokens, _stream(stream)))
+
+
+def _flat(name, x, elems, device):
+    """Device address of a float32 array of at least so many elements, whatever its shape."""
+    import torch
+    if x is None or isinstance(x, int):
+        return x
+    if x.dtype is not torch.float32 or x.numel() < elems or x.device != device or not x.is_contiguous():
+        raise ValueError(f"{name}: expected at least {elems} contiguous {torch.float32} on {device}, "
+                         f"got {x.dtype} {list(x.shape)} on {x.device}")
+    return x.data_ptr()
+
+
+def _cache(shape, S, rows, codes, scales, slots, fmt):
+    """Checks of the cache calls: (state, rows, codes, scales, slots, n_slots, pairs, format)."""
+    import torch
+    dev, i32 = S.device, torch.int32
+    f = CACHE[fmt] if isinstance(fmt, str) else _int32("format", fmt)
+    n_slots, H, K, V = codes.shape[0], shape.H, shape.K, shape.V
+    lists = [x for x in (rows, slots) if x is not None]
+    n = lists[0].numel() if lists else n_slots
+    for name, x, most in (("rows", rows, shape.B), ("slots", slots, n_slots)):
+        if x is None and n > most:
+            raise ValueError(f"{name}: {n} pairs and {most} {name}")
+    kind = torch.float8_e4m3fn if f == CACHE["e4m3"] else torch.int8
+    return [_arg("S", S, torch.float32, (shape.B, H, K, V), dev), _arg("rows", rows, i32, (n,), dev),
+            _arg("codes", codes, kind, (n_slots, H, K, V), dev),
+            _arg("scales", scales, torch.bfloat16, (n_slots, H, K), dev), _arg("slots", slots, i32, (n,), dev),
+            _int32("n_slots", n_slots), _int32("n", n), f]
+
+
+def sketchssm_cache_store(shape: Shape, S, rows, codes, scales, slots, format, stream=None):
+    """States of listed rows to slots of an 8-bit cache (``format``: a key of ``CACHE`` or its value)."""
+    args = _cache(shape, S, rows, codes, scales, slots, format)
+    with _on_device(S.device, stream):
+        _check("sketchssm_cache_store", lib().sketchssm_cache_store(ctypes.byref(shape), *args, _stream(stream)))
+
+
+def sketchssm_cache_load(shape: Shape, codes, scales, slots, S, rows, format, stream=None):
+    """Slots of an 8-bit cache back to listed state rows (a negative slot: the zero state)."""
+    st, rw, cd, sc, sl, n_slots, n, f = _cache(shape, S, rows, codes, scales, slots, format)
+    with _on_device(S.device, stream):
+        _check("sketchssm_cache_load",
+               lib().sketchssm_cache_load(ctypes.byref(shape), cd, sc, sl, n_slots, st, rw, n, f, _stream(stream)))
 
 
 def sketchssm_stream_probe(src, read_bytes: int, dst, write_bytes: int, unroll: int = 8, blocks: int = 0,

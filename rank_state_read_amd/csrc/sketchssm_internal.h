@@ -14,6 +14,7 @@ constexpr int kK = 128;         // key dim the kernels are written for
 constexpr int kW = 16;          // window length (one MFMA M-tile of tokens)
 constexpr int kMaxHeads = 256;  // head index fits a byte
 constexpr int kMaxRank = 64;    // four 16-row MFMA tiles of sketch rows
+constexpr int kMaxNodes = 64;   // nodes of a drafted tree: four 16-row MFMA tiles
 
 // Per-launch-position head table, passed to the kernels by value (no device
 // allocation is ever needed for it).  Entry p describes head order[p].

@@ -27,6 +27,18 @@ def bf16_tensor(bits: np.ndarray, device) -> torch.Tensor:
     return t.to(device).view(torch.bfloat16)
 
 
+class StateCache:
+    """Slots for 8-bit copies of a layer's states (``sketchssm_cache_store``): ``codes`` [n_slots, H, K, V] and
+    ``scales`` [n_slots, H, K]; ``format`` is a key of ``binding.CACHE``."""
+
+    def __init__(self, n_slots: int, H: int, K: int, V: int, format: str = "i8", device="cuda"):
+        _b.CACHE[format]  # a name it does not know is refused here
+        kind = torch.int8 if format == "i8" else torch.float8_e4m3fn
+        self.format = format
+        self.codes = torch.zeros((n_slots, H, K, V), dtype=torch.int8, device=device).view(kind)
+        self.scales = torch.zeros((n_slots, H, K), dtype=torch.bfloat16, device=device)
+
+
 class SketchLayer:
     """One layer's buffers for ``sketchssm_flush`` / ``sketchssm_decode_read``.
 
@@ -78,6 +90,11 @@ class SketchLayer:
     def _new(self, shape, dtype, stream):
         with _b.owned_by(stream, self.device):
             return torch.empty(shape, dtype=dtype, device=self.device)
+
+    def zeros_like(self, x, stream=None) -> torch.Tensor:
+        """Zeros of x's size and type for calls on `stream`, written there."""
+        with _b.owned_by(stream, self.device):
+            return torch.zeros_like(x)
 
     # -- inputs ------------------------------------------------------------
     def upload_step(self, st: dict) -> dict:
@@ -162,6 +179,41 @@ class SketchLayer:
         _b.sketchssm_prefill(self.shape, S0, rows0, self.S, rows, offsets, max_len, q, k, v, a, beta, y, workspace,
                             stream)
         return y
+
+    # -- trees of drafted tokens, cached states ------------------------------
+    def tree_read(self, offsets, max_nodes: int, parents, q, k, v, a, beta=None, pos=None, rows=None, y=None, plan=None,
+                  stream=None) -> torch.Tensor:
+        """Every node's y of the listed rows' trees, over the row's sketch (or state) and its pos[row] held-back
+        tokens (device int32 [B]; None: no row has any).  Nothing of the layer changes.  ``plan``: e.g. an all-dense
+        plan, to verify on the full state.  A y taken here holds nothing defined for nodes of no sequence."""
+        y = self._new(v.shape, torch.float32, stream) if y is None else y
+        pl = self.plan if plan is None else plan
+        _b.sketchssm_tree_read(pl, self.S, self.Z if plan is None else None, self.frames if plan is None else None,
+                              self.kbuf, self.vbuf, self.abuf, self.bbuf, pos, rows, offsets, max_nodes, parents, q, k,
+                              v, a, beta, y, stream)
+        return y
+
+    def tree_accept(self, offsets, parents, accepted, k, v, a, beta=None, *, pos, rows=None, new_pos=None,
+                    stream=None) -> torch.Tensor:
+        """Appends each tree's path to its node accepted[i] (device int32; negative: none) to the row's window, which
+        must have room, and returns the rows' held-back tokens then (a new tensor unless given)."""
+        new_pos = self._new(pos.shape, torch.int32, stream) if new_pos is None else new_pos
+        _b.sketchssm_tree_accept(self.shape, self.kbuf, self.vbuf, self.abuf, self.bbuf, pos, new_pos, rows, offsets,
+                                parents, accepted, k, v, a, beta, stream)
+        return new_pos
+
+    def new_cache(self, n_slots: int, format: str = "i8") -> StateCache:
+        """An empty cache of this layer's states."""
+        return StateCache(n_slots, self.H, self.K, self.V, format, self.device)
+
+    def cache_store(self, cache: StateCache, rows=None, slots=None, stream=None):
+        """States of the listed rows (their windows flushed before) to slots of the cache."""
+        _b.sketchssm_cache_store(self.shape, self.S, rows, cache.codes, cache.scales, slots, cache.format, stream)
+
+    def cache_load(self, cache: StateCache, slots=None, rows=None, stream=None):
+        """Slots of the cache (negative: the zero state) back to rows' states; the rows' sketches are formed by
+        ``flush_seq`` with 0 tokens."""
+        _b.sketchssm_cache_load(self.shape, cache.codes, cache.scales, slots, self.S, rows, cache.format, stream)
 
     def set_norm(self, weight, norm_heads: int, gate: str, eps: float = 1e-5, D=None):
         """The gated norm behind this layer's output: weight [H, V] or [V], D [H] the skip (Mamba-2's

@@ -17,6 +17,13 @@ A layer without one returns its y.  A norm with a skip
 ``v``, which is x only where no step size is in it (a layer whose heads share keys
 holds dt in v = dt x).
 
+Drafted tokens are verified by ``tree_read``: trees of tokens of listed rows, read
+over what every layer holds; ``tree_accept`` keeps the accepted paths.  Rows then
+stand at window positions of their own, which the caller keeps in a device array
+(``flush_seq`` empties the windows of listed rows); the common position of
+``decode_step`` is for batches that move in step.  ``cache_store`` and
+``cache_load`` copy rows' states of all layers to an 8-bit cache and back.
+
 Only the recurrent part of a layer is here: the projections that produce a
 layer's q, k, v, decay and beta from the previous layer's output are not part of
 the decode path this library implements, so the caller supplies each layer's
@@ -103,3 +110,57 @@ class SketchModel:
             out.append(self._normed(L, y, d, stream))
         self.pos = (self.pos + 1) % self.W
         return out
+
+    # -- rows at window positions of their own -----------------------------------
+    def tree_read(self, tokens: Sequence[Dict[str, Optional[torch.Tensor]]], parents: torch.Tensor,
+                  offsets: torch.Tensor, max_nodes: int, pos: Optional[torch.Tensor] = None,
+                  rows: Optional[torch.Tensor] = None, stream=None) -> List[torch.Tensor]:
+        """Trees of drafted tokens through every layer: nodes offsets[i] .. offsets[i+1]-1 of layer j's packed inputs
+        ``tokens[j]`` are sequence i's, ``parents`` each one's parent within its tree (-1: none), ``pos`` every row's
+        held-back tokens.  Returns the layers' (normed) outputs of all nodes; no layer changes."""
+        self._check_tokens(tokens)
+        out = []
+        for L, d in zip(self.layers, tokens):
+            y = L.tree_read(offsets, max_nodes, parents, d["q"], d["k"], d["v"], d["a"], d.get("beta"), pos=pos, rows=rows,
+                            stream=stream)
+            out.append(self._normed(L, y, d, stream))
+        return out
+
+    def tree_accept(self, tokens: Sequence[Dict[str, Optional[torch.Tensor]]], parents: torch.Tensor,
+                    offsets: torch.Tensor, accepted: torch.Tensor, pos: torch.Tensor,
+                    rows: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
+        """The path to node accepted[i] of each tree goes to every layer's window; returns the rows' held-back tokens
+        then.  ``tokens``, ``parents``, ``offsets``, ``pos`` and ``rows`` as they were read."""
+        if len(tokens) != len(self.layers):
+            raise ValueError("one token input per layer")
+        new_pos = None
+        for L, d in zip(self.layers, tokens):
+            new_pos = L.tree_accept(offsets, parents, accepted, d["k"], d["v"], d["a"], d.get("beta"), pos=pos, rows=rows,
+                                    new_pos=new_pos, stream=stream)
+        return new_pos
+
+    def flush_seq(self, rows: torch.Tensor, n_tokens: torch.Tensor, stream=None):
+        """Every layer's flush of the listed rows, which hold n_tokens tokens back (0 .. W)."""
+        for L in self.layers:
+            L.flush_seq(rows, n_tokens, stream=stream)
+
+    def new_cache(self, n_slots: int, format: str = "i8") -> list:
+        """An empty cache of states per layer."""
+        return [L.new_cache(n_slots, format) for L in self.layers]
+
+    def cache_store(self, caches: Sequence, rows: torch.Tensor, slots: torch.Tensor, stream=None):
+        """Every layer's states of the listed rows (their windows flushed before) to slots of its cache."""
+        if len(caches) != len(self.layers):
+            raise ValueError("one cache per layer")
+        for L, c in zip(self.layers, caches):
+            L.cache_store(c, rows, slots, stream=stream)
+
+    def cache_load(self, caches: Sequence, slots: torch.Tensor, rows: torch.Tensor, stream=None):
+        """Slots (negative: the zero state) back to the listed rows of every layer, with their first sketches: the
+        rows then hold no tokens back."""
+        if len(caches) != len(self.layers):
+            raise ValueError("one cache per layer")
+        none = self.layers[0].zeros_like(rows, stream)
+        for L, c in zip(self.layers, caches):
+            L.cache_load(c, slots, rows, stream=stream)
+            L.flush_seq(rows, none, stream=stream)
