@@ -59,131 +59,413 @@ __device__ __forceinline__ TreeSpan tree_span(const TreeArgs& A, int i) {
     return s;
 }
 
-// One token past the carried query of a 16-lane row (lane l owns key elements
-// 8l .. 8l+7 and, for l < V/8, value elements 8l .. 8l+7).
-template <int KIND, int V, typename QT>
-__device__ __forceinline__ void walk_token(const void* kp, size_t ke, const void* vp, size_t ve, const float* ap,
-                                           size_t ae, float beta, int l, float (&x)[8], float (&acc)[8]) {
-    constexpr bool KDA = KIND == SKSSM_KDA;
-    float kf[8], vf[8], af[8];
-    Vec8<QT>::unpack(Vec8<QT>::load(kp, ke + 8 * l), kf);
-    Vec8<QT>::unpack(Vec8<QT>::load(vp, ve + (l < V / 8 ? 8 * l : 0)), vf);
-    if (KDA) load8f(ap + ae * kK + 8 * l, af);
-    else af[0] = ap[ae];
-    const float s = beta * row_sum16(dot8(kf, x));
+// A tree's tokens as rows: 0 .. 15 the window's slots, 16 + n node n.  `up` of a row is
+// the row before it on a path, -1 at the window's start, kNoRow where a parent is none.
+constexpr int kNoRow = -2;
+
+// Rows of CH 16-byte chunks on their way to LDS, through registers.  Rows behind the
+// window's or the tree's last one repeat that one: nothing points to them.
+template <int CH, int MT>
+struct RowRegs {
+    static constexpr int PER = 256 / CH;  // rows per load of the block
+    static constexpr int N = 16 * (1 + MT) / PER;
+    u32x4 r[N];
+
+    __device__ __forceinline__ void load(const char* win, size_t wstride, int p, const char* node, size_t nstride,
+                                         int len) {
+        const int row = threadIdx.x / CH;
+        const size_t c = 16 * (threadIdx.x % CH);
 #pragma unroll
-    for (int e = 0; e < 8; ++e) {
-        acc[e] = fmaf(s, vf[e], acc[e]);
-        if (KIND != SKSSM_MAMBA2) x[e] = fmaf(-s, kf[e], x[e]);
-        x[e] *= KDA ? af[e] : af[0];
+        for (int i = 0; i < N; ++i) {
+            r[i] = u32x4{0u, 0u, 0u, 0u};
+            if (i * PER < 16) {
+                if (i * PER < p) r[i] = *reinterpret_cast<const u32x4*>(win + min(i * PER + row, p - 1) * wstride + c);
+            } else if (i * PER - 16 < len) {
+                r[i] = *reinterpret_cast<const u32x4*>(node + min(i * PER - 16 + row, len - 1) * nstride + c);
+            }
+        }
     }
+    __device__ __forceinline__ void store(char* lds) const {
+#pragma unroll
+        for (int i = 0; i < N; ++i)
+            *reinterpret_cast<u32x4*>(lds + (i * 256 + threadIdx.x) * 16) = r[i];
+    }
+};
+
+// One lane's part of a matrix operand whose rows are V wide: of one row the columns
+// 4j .. 4j+3 (column tiles 0 .. 3) and, of those past 64, R j .. R j + R-1 (tiles 4 ..),
+// so that a row's first 64 values are one load of 16 lanes.
+template <int V>
+__device__ __forceinline__ void load_cols(const float* p, int j, float (&f)[V / 16]) {
+    constexpr int R = V / 16 - 4;
+    const float4 c = *reinterpret_cast<const float4*>(p + 4 * j);
+    f[0] = c.x; f[1] = c.y; f[2] = c.z; f[3] = c.w;
+#pragma unroll
+    for (int i = 0; i < R; ++i) f[4 + i] = p[64 + R * j + i];
 }
 
-// Walks node n of a sequence back to the last flush; false if its path holds a
-// parent that is none (the node is then left alone).
-template <int KIND, int V, typename QT>
-__device__ __forceinline__ bool walk(const TreeArgs& A, const TreeSpan& sp, int n, int h, int l, float (&x)[8],
-                                     float (&acc)[8]) {
-    constexpr bool DELTA = KIND != SKSSM_MAMBA2;
-    const int hk = h / A.share;
-    Vec8<QT>::unpack(Vec8<QT>::load(A.q, (size_t(sp.t0 + n) * A.Hk + hk) * kK + 8 * l), x);
+// The same of a row of the qkv dtype, as it is stored.
+template <int V, typename QT>
+struct ValueCols;
+template <int V>
+struct ValueCols<V, F32Tag> {
+    float f[V / 16];
+    __device__ __forceinline__ void zero() {
 #pragma unroll
-    for (int e = 0; e < 8; ++e) acc[e] = 0.f;
-    bool ok = true;
-    for (int m = n; m >= 0;) {
-        const size_t t = size_t(sp.t0) + m;
-        const size_t th = t * A.H + h;
-        walk_token<KIND, V, QT>(A.k, (t * A.Hk + hk) * kK, A.v, th * V, A.a, th, DELTA ? A.beta[th] : 1.f, l, x, acc);
-        const int up = A.parents[t];
-        ok = ok && up < m && up >= -1;
-        m = ok ? up : -1;
+        for (int c = 0; c < V / 16; ++c) f[c] = 0.f;
     }
-    for (int j = sp.p - 1; j >= 0; --j) {
-        const size_t at = (size_t(j) * A.H + h) * A.B + sp.row;
-        walk_token<KIND, V, QT>(A.kbuf, ((size_t(j) * A.Hk + hk) * A.B + sp.row) * kK, A.vbuf, at * V, A.abuf, at,
-                                DELTA ? A.bbuf[at] : 1.f, l, x, acc);
+    __device__ __forceinline__ void load(const void* base, size_t e, int j) {
+        load_cols<V>(static_cast<const float*>(base) + e, j, f);
     }
-    return ok;
-}
+    __device__ __forceinline__ float get(int c) const { return f[c]; }
+    __device__ __forceinline__ void drop(int c) { f[c] = 0.f; }
+};
+template <int V>
+struct ValueCols<V, Bf16Tag> {
+    static constexpr int R = V / 16 - 4;
+    uint32_t u[2 + (R + 1) / 2];
+    __device__ __forceinline__ void zero() {
+#pragma unroll
+        for (int c = 0; c < 2 + (R + 1) / 2; ++c) u[c] = 0u;
+    }
+    __device__ __forceinline__ void load(const void* base, size_t e, int j) {
+        const uint16_t* p = static_cast<const uint16_t*>(base) + e;
+        const uint2 c = *reinterpret_cast<const uint2*>(p + 4 * j);
+        u[0] = c.x;
+        u[1] = c.y;
+        p += 64 + R * j;
+        if constexpr (R == 4) {
+            const uint2 d = *reinterpret_cast<const uint2*>(p);
+            u[2] = d.x;
+            u[3] = d.y;
+        } else if constexpr (R == 2) {
+            u[2] = *reinterpret_cast<const uint32_t*>(p);
+        } else if constexpr (R > 0) {
+            u[2] = p[0];
+            if constexpr (R == 3) {
+                u[2] |= uint32_t(p[1]) << 16;
+                u[3] = p[2];
+            }
+        }
+    }
+    __device__ __forceinline__ float get(int c) const {
+        return __uint_as_float(c % 2 ? u[c / 2] & 0xffff0000u : u[c / 2] << 16);
+    }
+    __device__ __forceinline__ void drop(int c) { u[c / 2] &= c % 2 ? 0xffffu : 0xffff0000u; }
+};
+
+template <int KIND, int V, typename QT, int MT>
+struct TreeLds {
+    static constexpr bool DELTA = KIND != SKSSM_MAMBA2;
+    static constexpr bool KDA = KIND == SKSSM_KDA;
+    static constexpr int NT = 16 * MT, L = 16 + NT;
+    static constexpr int LP = L + 4;   // row of P; 4 rows apart in the banks
+    static constexpr int XS = kK + 4;  // row of x
+    static constexpr int kKeyBytes = kK * Vec8<QT>::kElemBytes;
+    // what the walk uses, then the waves' sums over it
+    static constexpr int keys = 0;
+    static constexpr int dec = keys + (DELTA ? L * kKeyBytes : 0);
+    static constexpr int x = dec + (KDA ? L * kK * 4 : 0);
+    static constexpr int gram = x;                                             // Mamba-2
+    static constexpr int cs = DELTA ? keys : x + NT * LP * 4;                  // coefficients of 16 ranks
+    static constexpr int cs_end = cs + 4 * 16 * 20 * 4;
+    static constexpr int x_end = x + NT * XS * 4;
+    static constexpr int walk_end = DELTA ? x_end : cs_end;
+    static constexpr int red_end = 4 * 16 * V * 4;
+    static constexpr int p = walk_end > red_end ? walk_end : red_end;
+    static constexpr int a = p + NT * LP * 4;  // decays; Mamba-2: its window's become products
+    static constexpr int beta = a + L * 4;
+    static constexpr int up = beta + L * 4;
+    static constexpr int g = up + L * 4;       // per node: Mamba-2's product of decays
+    static constexpr int flag = g + NT * 4;
+    static constexpr int bytes = flag + 16;
+    static_assert(!DELTA || cs_end <= x, "the coefficients' sums fit the keys' place");
+};
 
 }  // namespace
 
-// Sketch heads: a 16-lane row per node, 16 nodes of one sequence and head per block.
-template <int KIND, int V, typename QT>
-__global__ __launch_bounds__(256) void tree_sketch_kernel(TreeArgs A, HeadTable T, int tiles) {
-    const int seq = blockIdx.x / tiles % A.n_seqs;
-    const int tile = blockIdx.x % tiles;
-    const int at = A.n_dense + blockIdx.x / tiles / A.n_seqs;
-    const int h = T.head[at], r = T.rank[at];
-    const int l = threadIdx.x & 15, n = 16 * tile + (threadIdx.x >> 4);
-    const TreeSpan sp = tree_span(A, seq);
-    if (!sp.live || n >= sp.len) return;
-    float x[8], acc[8];
-    if (!walk<KIND, V, QT>(A, sp, n, h, l, x, acc)) return;
-    const float* F = A.frames + size_t(T.frow[at]) * kK;
-    const float* Z = A.Z + (size_t(T.zrow[at]) * A.B + size_t(sp.row) * r) * V;
-    for (int i = 0; i < r; ++i) {
-        float f[8], z[8];
-        load8f(F + i * kK + 8 * l, f);
-        load8f(Z + i * V + (l < V / 8 ? 8 * l : 0), z);
-        const float c = row_sum16(dot8(f, x));
-#pragma unroll
-        for (int e = 0; e < 8; ++e) acc[e] = fmaf(c, z[e], acc[e]);
-    }
-    if (l < V / 8) store8f(A.y + (size_t(sp.t0 + n) * A.H + h) * V + 8 * l, acc);
-}
-
-// Dense heads: a block per (sequence, head), MT tiles of 16 nodes.  The block's four
-// waves take 32 key rows of the state each, in registers; x of all nodes goes through
-// LDS to the fp32 matrix instruction, the waves' sums through LDS to the nodes' rows.
+// A block per (sequence, head), MT tiles of 16 nodes; dense heads first.
 template <int KIND, int V, typename QT, int MT>
-__global__ __launch_bounds__(256) void tree_dense_kernel(TreeArgs A, HeadTable T) {
-    constexpr int CT = V / 16;  // column tiles
-    constexpr int R = CT - 4;   // those past column 64
-    constexpr int XS = kK + 4;
-    constexpr int kX = MT * 16 * XS, kRed = 4 * 16 * V;
-    __shared__ __align__(16) float lds[kX > kRed ? kX : kRed];
-    const int seq = blockIdx.x % A.n_seqs;
-    const int h = T.head[blockIdx.x / A.n_seqs];
+__global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(MT == 1 ? (V <= 96 ? 4 : 3) : 2)))
+void tree_kernel(TreeArgs A, HeadTable T) {
+    typedef TreeLds<KIND, V, QT, MT> Lds;
+    constexpr bool DELTA = Lds::DELTA, KDA = Lds::KDA;
+    constexpr int CT = V / 16, R = CT - 4, E = Vec8<QT>::kElemBytes;
+    constexpr int L = Lds::L, LP = Lds::LP, XS = Lds::XS, NT = Lds::NT;
+    extern __shared__ __align__(16) char lds[];
+    float* red = reinterpret_cast<float*>(lds);
+    float* xs = reinterpret_cast<float*>(lds + Lds::x);
+    float* gram = reinterpret_cast<float*>(lds + Lds::gram);
+    float* ps = reinterpret_cast<float*>(lds + Lds::p);
+    float* as = reinterpret_cast<float*>(lds + Lds::a);
+    float* bs = reinterpret_cast<float*>(lds + Lds::beta);
+    int* up = reinterpret_cast<int*>(lds + Lds::up);
+    float* gs = reinterpret_cast<float*>(lds + Lds::g);
+    int* flag = reinterpret_cast<int*>(lds + Lds::flag);
+
+    const int seq = blockIdx.x % A.n_seqs, at = blockIdx.x / A.n_seqs;
+    const int h = T.head[at], rank = T.rank[at], hk = h / A.share;
     const TreeSpan sp = tree_span(A, seq);
     if (!sp.live) return;
-    const int lane = threadIdx.x & 63, w = threadIdx.x >> 6;
+    const int tid = threadIdx.x, lane = tid & 63, w = tid >> 6;
     const int j = lane & 15, kk = lane >> 4;
-    float s[8][CT];
-    const float* S = A.S + (size_t(sp.row) * A.H + h) * (kK * V) + (32 * w + 8 * kk) * V;
-#pragma unroll
-    for (int t = 0; t < 8; ++t) {
-        const float4 c = *reinterpret_cast<const float4*>(S + t * V + 4 * j);
-        s[t][0] = c.x; s[t][1] = c.y; s[t][2] = c.z; s[t][3] = c.w;
-#pragma unroll
-        for (int i = 0; i < R; ++i) s[t][4 + i] = S[t * V + 64 + R * j + i];
+    const int rrow = tid >> 4, l = tid & 15;
+
+    // ---- loads, in the order of their use --------------------------------------
+    const size_t win = size_t(h) * A.B + sp.row, wslot = size_t(A.H) * A.B;  // an item's window entry, a slot
+    const size_t node = size_t(sp.t0) * A.H + h;
+    const size_t kwin = size_t(hk) * A.B + sp.row, kslot = size_t(A.Hk) * A.B;
+    const size_t knode = size_t(sp.t0) * A.Hk + hk;
+    float a_r = 1.f, b_r = 1.f;
+    int up_r = kNoRow;
+    if (tid < 16) {
+        if (tid < sp.p) {
+            if (!KDA) a_r = A.abuf[win + tid * wslot];
+            if (DELTA) b_r = A.bbuf[win + tid * wslot];
+            up_r = tid - 1;
+        }
+    } else if (tid < L && tid - 16 < sp.len) {
+        const int n = tid - 16;
+        if (!KDA) a_r = A.a[node + size_t(n) * A.H];
+        if (DELTA) b_r = A.beta[node + size_t(n) * A.H];
+        const int up = A.parents[sp.t0 + n];
+        up_r = up >= n || up < -1 ? kNoRow : up < 0 ? sp.p - 1 : 16 + up;
     }
-    const int rrow = threadIdx.x >> 4, l = threadIdx.x & 15;
-    float acc[MT][8];
-    bool ok[MT];
+    RowRegs<kK * E / 16, MT> kr;
+    RowRegs<kK * 4 / 16, MT> ar;
+    typename Vec8<QT>::raw_t qr[MT];
+    if constexpr (DELTA) {
+        kr.load(static_cast<const char*>(A.kbuf) + kwin * kK * E, kslot * kK * E, sp.p,
+                static_cast<const char*>(A.k) + knode * kK * E, size_t(A.Hk) * kK * E, sp.len);
+        if constexpr (KDA)
+            ar.load(reinterpret_cast<const char*>(A.abuf) + win * kK * 4, wslot * kK * 4, sp.p,
+                    reinterpret_cast<const char*>(A.a) + node * kK * 4, size_t(A.H) * kK * 4, sp.len);
 #pragma unroll
-    for (int m = 0; m < MT; ++m) {
-        const int n = 16 * m + rrow;
-        ok[m] = false;
-        if (n < sp.len) {
-            float x[8];
-            ok[m] = walk<KIND, V, QT>(A, sp, n, h, l, x, acc[m]);
-            store8f(lds + n * XS + 8 * l, x);
+        for (int m = 0; m < MT; ++m)
+            if (16 * m < sp.len)
+                qr[m] = Vec8<QT>::load(A.q, (knode + size_t(min(16 * m + rrow, sp.len - 1)) * A.Hk) * kK + 8 * l);
+    }
+    // values: of each 16 rows this wave takes 4
+    ValueCols<V, QT> vr[1 + MT];
+#pragma unroll
+    for (int u = 0; u <= MT; ++u) {
+        const int row = 4 * w + kk + 16 * (u > 0 ? u - 1 : 0);
+        const bool on = row < (u ? sp.len : sp.p);
+        vr[u].zero();
+        if (on)
+            vr[u].load(u ? A.v : A.vbuf, (u ? node + size_t(row) * A.H : win + row * wslot) * V, j);
+    }
+    float s[8][CT];
+    if (rank == 0) {
+        const float* S = A.S + (size_t(sp.row) * A.H + h) * (kK * V) + (32 * w + 8 * kk) * V;
+#pragma unroll
+        for (int t = 0; t < 8; ++t) load_cols<V>(S + t * V, j, s[t]);
+    }
+    __builtin_amdgcn_sched_barrier(0);
+
+    // ---- to LDS --------------------------------------------------------------------
+    if (tid < L) {
+        as[tid] = a_r;
+        bs[tid] = b_r;
+        up[tid] = up_r;
+    }
+    if (tid == 0) *flag = 0;
+    for (int i = tid; i < NT * LP; i += 256) ps[i] = 0.f;
+    if constexpr (DELTA) {
+        kr.store(lds + Lds::keys);
+        if constexpr (KDA) ar.store(lds + Lds::dec);
+    } else {  // products q k of all nodes and rows
+        for (int tile = w; tile < MT * (1 + MT); tile += 4) {
+            const int m = tile / (1 + MT), u = tile % (1 + MT);
+            if (16 * m >= sp.len || (u ? 16 * (u - 1) >= sp.len : sp.p == 0)) continue;
+            const size_t qe = (knode + size_t(min(16 * m + j, sp.len - 1)) * A.Hk) * kK + 8 * kk;
+            const void* kb = u ? A.k : A.kbuf;
+            const size_t ke = (u ? knode + size_t(min(16 * (u - 1) + j, sp.len - 1)) * A.Hk
+                                 : kwin + min(j, sp.p - 1) * kslot) * kK + 8 * kk;
+            f32x4 d = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+            for (int c = 0; c < 4; ++c) {
+                const auto qv = Vec8<QT>::load(A.q, qe + 32 * c);
+                const auto kv = Vec8<QT>::load(kb, ke + 32 * c);
+                if constexpr (E == 2) {
+                    typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
+                    d = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, qv.w),
+                                                                __builtin_bit_cast(bf16x8, kv.w), d, 0, 0, 0);
+                } else {
+                    float qf[8], kf[8];
+                    Vec8<QT>::unpack(qv, qf);
+                    Vec8<QT>::unpack(kv, kf);
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) d = mfma_16x16x4(qf[e], kf[e], d);
+                }
+            }
+#pragma unroll
+            for (int i = 0; i < 4; ++i) gram[(16 * m + 4 * kk + i) * LP + 16 * u + j] = d[i];
+        }
+    }
+    __syncthreads();
+
+    // a value that is no number must not meet the zeros of other nodes' rows: it is
+    // left out of the products and joins the nodes below it at the end
+    bool odd = false;
+#pragma unroll
+    for (int u = 0; u <= MT; ++u)
+#pragma unroll
+        for (int c = 0; c < CT; ++c)
+            if (!isfinite(vr[u].get(c))) {
+                odd = true;
+                vr[u].drop(c);
+            }
+    if (odd) *flag = 1;
+
+    // ---- the walk --------------------------------------------------------------------
+    bool ok[MT];
+    if constexpr (DELTA) {
+#pragma unroll
+        for (int m = 0; m < MT; ++m) {
+            const int n = 16 * m + rrow;
+            ok[m] = false;
+            if (n < sp.len) {
+                float x[8], g = 1.f;
+                Vec8<QT>::unpack(qr[m], x);
+                int row = 16 + n;
+                while (row >= 0) {
+                    float kf[8];
+                    Vec8<QT>::unpack(Vec8<QT>::load(lds + Lds::keys, row * kK + 8 * l), kf);
+                    const float c = bs[row] * row_sum16(dot8(kf, x));
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) x[e] = fmaf(-c, kf[e], x[e]);
+                    if constexpr (KDA) {
+                        float af[8];
+                        load8f(reinterpret_cast<const float*>(lds + Lds::dec) + row * kK + 8 * l, af);
+#pragma unroll
+                        for (int e = 0; e < 8; ++e) x[e] *= af[e];
+                    }
+                    if (l == 0) ps[n * LP + row] = g * c;
+                    if constexpr (!KDA) g *= as[row];
+                    row = up[row];
+                }
+                ok[m] = row == -1;
+                if constexpr (!KDA) {
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) x[e] *= g;
+                }
+                store8f(xs + n * XS + 8 * l, x);
+            }
+        }
+    } else {
+        if (tid < sp.len) {  // the nodes of the path
+            float g = 1.f;
+            int row = 16 + tid;
+            while (row >= 16) {
+                ps[tid * LP + row] = g * gram[tid * LP + row];
+                g *= as[row];
+                row = up[row];
+            }
+            gs[tid] = g;
+            if (row == kNoRow) up[16 + tid] = kNoRow;  // (a walk that meets this entry meets the other one too)
         }
     }
     __syncthreads();
     f32x4 d[MT][CT];
+    if constexpr (!DELTA) {
 #pragma unroll
-    for (int m = 0; m < MT; ++m) {
+        for (int m = 0; m < MT; ++m) ok[m] = 16 * m + rrow < sp.len && up[16 + 16 * m + rrow] != kNoRow;
+    }
+    // products of the decays from each slot's successor to the window's end
+    float after = 1.f, all = 1.f;
+    if constexpr (!DELTA) {
+        for (int i = sp.p - 1; i >= 0; --i) {
+            if (i == 4 * w + kk) after = all;
+            all *= as[i];
+        }
+    }
+
+    // ---- the state, or the sketch ----------------------------------------------------
+#pragma unroll
+    for (int m = 0; m < MT; ++m)
 #pragma unroll
         for (int c = 0; c < CT; ++c) d[m][c] = f32x4{0.f, 0.f, 0.f, 0.f};
-        if (16 * m >= sp.len) continue;
-        float x[8];
-        load8f(lds + (16 * m + j) * XS + 32 * w + 8 * kk, x);
+    auto x_of = [&](int m, float (&x)[8]) {  // node 16 m + j, key elements 32 w + 8 kk ..
+        if constexpr (DELTA) load8f(xs + (16 * m + j) * XS + 32 * w + 8 * kk, x);
+        else Vec8<QT>::unpack(Vec8<QT>::load(A.q, (knode + size_t(min(16 * m + j, sp.len - 1)) * A.Hk) * kK + 32 * w + 8 * kk), x);
+    };
+    if (rank == 0) {
 #pragma unroll
-        for (int t = 0; t < 8; ++t)
+        for (int m = 0; m < MT; ++m) {
+            if (16 * m >= sp.len) continue;
+            float x[8];
+            x_of(m, x);
 #pragma unroll
-            for (int c = 0; c < CT; ++c) d[m][c] = mfma_16x16x4(x[t], s[t][c], d[m][c]);
+            for (int t = 0; t < 8; ++t)
+#pragma unroll
+                for (int c = 0; c < CT; ++c) d[m][c] = mfma_16x16x4(x[t], s[t][c], d[m][c]);
+        }
+    } else {
+        const float* F = A.frames + size_t(T.frow[at]) * kK;
+        const float* Z = A.Z + (size_t(T.zrow[at]) * A.B + size_t(sp.row) * rank) * V;
+        f32x4 c[MT];
+#pragma unroll 1
+        for (int r0 = 0; r0 < rank; r0 += 16) {
+            float f[8], z[CT];
+            load8f(F + min(r0 + j, rank - 1) * kK + 32 * w + 8 * kk, f);
+#pragma unroll
+            for (int i = 0; i < CT; ++i) z[i] = 0.f;
+            if (r0 + 4 * w + kk < rank) load_cols<V>(Z + (r0 + 4 * w + kk) * V, j, z);
+#pragma unroll
+            for (int m = 0; m < MT; ++m) {
+                c[m] = f32x4{0.f, 0.f, 0.f, 0.f};
+                if (16 * m >= sp.len) continue;
+                float x[8];
+                x_of(m, x);
+#pragma unroll
+                for (int t = 0; t < 8; ++t) c[m] = mfma_16x16x4(x[t], f[t], c[m]);
+            }
+            // c's sums over the waves' keys
+            float* cs = reinterpret_cast<float*>(lds + Lds::cs);
+#pragma unroll
+            for (int m = 0; m < MT; ++m) {
+                if (16 * m >= sp.len) break;
+                __syncthreads();
+#pragma unroll
+                for (int i = 0; i < 4; ++i) cs[(w * 16 + 4 * kk + i) * 20 + j] = c[m][i];
+                __syncthreads();
+                float y = 0.f;
+#pragma unroll
+                for (int i = 0; i < 4; ++i) y += cs[(i * 16 + j) * 20 + 4 * w + kk];
+                if (r0 + 4 * w + kk >= rank) y = 0.f;
+#pragma unroll
+                for (int i = 0; i < CT; ++i) d[m][i] = mfma_16x16x4(y, z[i], d[m][i]);
+            }
+        }
+    }
+
+    // ---- the path's values, the waves' sums ---------------------------------------
+#pragma unroll
+    for (int m = 0; m < MT; ++m) {
+        if (16 * m >= sp.len) break;
+        if constexpr (!DELTA) {  // what the state gave decays over the whole path
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const float g = all * gs[16 * m + 4 * kk + i];
+#pragma unroll
+                for (int c = 0; c < CT; ++c) d[m][c][i] *= g;
+            }
+        }
+#pragma unroll
+        for (int u = 0; u <= MT; ++u) {
+            if (u ? 16 * (u - 1) >= sp.len : sp.p == 0) continue;
+            const int n = 16 * m + j, row = 16 * u + 4 * w + kk;
+            float pv;
+            if (!DELTA && u == 0) {
+                pv = row < sp.p && n < sp.len ? gs[n] * after * gram[n * LP + row] : 0.f;
+                ps[n * LP + row] = pv;
+            } else {
+                pv = ps[n * LP + row];
+            }
+#pragma unroll
+            for (int c = 0; c < CT; ++c) d[m][c] = mfma_16x16x4(pv, vr[u].get(c), d[m][c]);
+        }
     }
 #pragma unroll
     for (int m = 0; m < MT; ++m) {
@@ -191,21 +473,34 @@ __global__ __launch_bounds__(256) void tree_dense_kernel(TreeArgs A, HeadTable T
         __syncthreads();
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-            float* to = lds + (w * 16 + 4 * kk + i) * V;
+            float* to = red + (w * 16 + 4 * kk + i) * V;
             *reinterpret_cast<float4*>(to + 4 * j) = make_float4(d[m][0][i], d[m][1][i], d[m][2][i], d[m][3][i]);
 #pragma unroll
             for (int c = 0; c < R; ++c) to[64 + R * j + c] = d[m][4 + c][i];
         }
         __syncthreads();
         if (ok[m] && l < V / 8) {
+            const int n = 16 * m + rrow;
+            float y[8];
+            load8f(red + rrow * V + 8 * l, y);
 #pragma unroll
-            for (int u = 0; u < 4; ++u) {
+            for (int u = 1; u < 4; ++u) {
                 float f[8];
-                load8f(lds + (u * 16 + rrow) * V + 8 * l, f);
+                load8f(red + (u * 16 + rrow) * V + 8 * l, f);
 #pragma unroll
-                for (int e = 0; e < 8; ++e) acc[m][e] += f[e];
+                for (int e = 0; e < 8; ++e) y[e] += f[e];
             }
-            store8f(A.y + (size_t(sp.t0 + 16 * m + rrow) * A.H + h) * V + 8 * l, acc[m]);
+            if (*flag) {
+                for (int row = 16 + n; row >= 0; row = up[row]) {
+                    float f[8];
+                    Vec8<QT>::unpack(row < 16 ? Vec8<QT>::load(A.vbuf, (win + row * wslot) * V + 8 * l)
+                                              : Vec8<QT>::load(A.v, (node + size_t(row - 16) * A.H) * V + 8 * l), f);
+#pragma unroll
+                    for (int e = 0; e < 8; ++e)
+                        if (!isfinite(f[e])) y[e] = fmaf(ps[n * LP + row], f[e], y[e]);
+                }
+            }
+            store8f(A.y + (node + size_t(n) * A.H) * V + 8 * l, y);
         }
     }
 }
@@ -319,27 +614,23 @@ __global__ __launch_bounds__(256) void tree_accept_kernel(AcceptArgs A, int grou
 namespace {
 
 template <int KIND, int V, typename QT, int MT>
-hipError_t launch_dense(const TreeArgs& a, const HeadTable& t, hipStream_t s) {
-    if (!launch_fits(double(a.n_seqs) * a.n_dense, 256)) return hipErrorInvalidConfiguration;
-    hipLaunchKernelGGL((tree_dense_kernel<KIND, V, QT, MT>), dim3(a.n_seqs * a.n_dense), dim3(256), 0, s, a, t);
+hipError_t launch_tree_m(const TreeArgs& a, const HeadTable& t, hipStream_t s) {
+    constexpr int bytes = TreeLds<KIND, V, QT, MT>::bytes;
+    if (!launch_fits(double(a.n_seqs) * a.H, 256)) return hipErrorInvalidConfiguration;
+    if (bytes > 65536) {
+        const hipError_t e = hipFuncSetAttribute(reinterpret_cast<const void*>(tree_kernel<KIND, V, QT, MT>),
+                                                 hipFuncAttributeMaxDynamicSharedMemorySize, bytes);
+        if (e != hipSuccess) return e;
+    }
+    hipLaunchKernelGGL((tree_kernel<KIND, V, QT, MT>), dim3(a.n_seqs * a.H), dim3(256), bytes, s, a, t);
     return hipGetLastError();
 }
 
 template <int KIND, int V, typename QT>
 hipError_t launch_tree_t(const TreeArgs& a, const HeadTable& t, hipStream_t s) {
-    const int tiles = (a.max_nodes + 15) / 16;
-    const int sketch = a.H - a.n_dense;
-    if (!launch_fits(double(a.n_seqs) * sketch * tiles, 256)) return hipErrorInvalidConfiguration;
-    if (a.n_dense) {
-        const hipError_t e = tiles == 1 ? launch_dense<KIND, V, QT, 1>(a, t, s)
-                             : tiles == 2 ? launch_dense<KIND, V, QT, 2>(a, t, s)
-                                          : launch_dense<KIND, V, QT, 4>(a, t, s);
-        if (e != hipSuccess) return e;
-    }
-    if (sketch)
-        hipLaunchKernelGGL((tree_sketch_kernel<KIND, V, QT>), dim3(a.n_seqs * sketch * tiles), dim3(256), 0, s, a, t,
-                           tiles);
-    return hipGetLastError();
+    if (a.max_nodes <= 16) return launch_tree_m<KIND, V, QT, 1>(a, t, s);
+    if (a.max_nodes <= 32) return launch_tree_m<KIND, V, QT, 2>(a, t, s);
+    return launch_tree_m<KIND, V, QT, 4>(a, t, s);
 }
 
 template <int KIND, typename QT>
