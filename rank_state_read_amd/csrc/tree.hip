@@ -36,7 +36,8 @@ struct TreeArgs {
     const float* beta;
     float* y;
     int B, n_seqs, total, max_nodes;
-    int H, Hk, share;
+    int H, Hk;
+    uint32_t per_share;  // 2^16 / (heads of a key head), rounded up: h / share is h per_share >> 16 below 256
     int n_dense;  // dense heads lead the head table
 };
 
@@ -59,93 +60,147 @@ __device__ __forceinline__ TreeSpan tree_span(const TreeArgs& A, int i) {
     return s;
 }
 
-// A tree's tokens as rows: 0 .. 15 the window's slots, 16 + n node n.  `up` of a row is
-// the row before it on a path, -1 at the window's start, kNoRow where a parent is none.
-constexpr int kNoRow = -2;
+// A tree's tokens as rows: 0 .. 15 the window's slots, 16 + n node n, and behind them
+// two that end a path: `rows` behind the window's first slot, `rows` + 1 where a parent
+// is none.  Every row says which one stands before it on a path.
+struct __align__(16) RowInfo {
+    int up;
+    float beta, a;
+    int pad;
+};
 
-// Rows of CH 16-byte chunks on their way to LDS, through registers.  Rows behind the
-// window's or the tree's last one repeat that one: nothing points to them.
-template <int CH, int MT>
+// A load at a per-lane 32-bit byte offset from a base that all lanes share.
+template <typename T>
+__device__ __forceinline__ T load_at(const void* base, uint32_t off) {
+    return *reinterpret_cast<const T*>(static_cast<const char*>(base) + off);
+}
+
+// A block's rows of CH 16-byte chunks, through registers to LDS.  All loads are made,
+// without a branch to wait behind: rows behind the window's or the tree's last one
+// repeat it, and nothing points to them.
+template <int CH, int MT, int NTH>
 struct RowRegs {
-    static constexpr int PER = 256 / CH;  // rows per load of the block
-    static constexpr int N = 16 * (1 + MT) / PER;
+    static constexpr int PER = NTH / CH;  // rows per load of the block
+    static constexpr int W = 16 / PER > 0 ? 16 / PER : 1, N = (16 * (1 + MT) + PER - 1) / PER;
     u32x4 r[N];
 
-    __device__ __forceinline__ void load(const char* win, size_t wstride, int p, const char* node, size_t nstride,
-                                         int len) {
+    __device__ __forceinline__ void load(const void* node, uint32_t nstep, int len, const void* win, uint32_t wstep,
+                                         int p) {
         const int row = threadIdx.x / CH;
-        const size_t c = 16 * (threadIdx.x % CH);
+        const uint32_t c = 16 * (threadIdx.x % CH);
 #pragma unroll
         for (int i = 0; i < N; ++i) {
-            r[i] = u32x4{0u, 0u, 0u, 0u};
-            if (i * PER < 16) {
-                if (i * PER < p) r[i] = *reinterpret_cast<const u32x4*>(win + min(i * PER + row, p - 1) * wstride + c);
-            } else if (i * PER - 16 < len) {
-                r[i] = *reinterpret_cast<const u32x4*>(node + min(i * PER - 16 + row, len - 1) * nstride + c);
+            if constexpr (PER <= 16) {
+                if (i < W) r[i] = load_at<u32x4>(win, max(min(i * PER + row, p - 1), 0) * wstep + c);
+                else r[i] = load_at<u32x4>(node, min(i * PER - 16 + row, len - 1) * nstep + c);
+            } else {  // the first load's threads take both
+                const int at = i * PER + row;
+                const bool w = i == 0 && row < 16;
+                r[i] = load_at<u32x4>(w ? win : node,
+                                      (w ? max(min(at, p - 1), 0) * wstep : min(at - 16, len - 1) * nstep) + c);
             }
         }
     }
-    __device__ __forceinline__ void store(char* lds) const {
+    __device__ __forceinline__ void store(char* lds, int rows) const {
 #pragma unroll
         for (int i = 0; i < N; ++i)
-            *reinterpret_cast<u32x4*>(lds + (i * 256 + threadIdx.x) * 16) = r[i];
+            if (int(i * PER + threadIdx.x / CH) < rows)
+                *reinterpret_cast<u32x4*>(lds + (i * NTH + threadIdx.x) * 16) = r[i];
     }
 };
 
-// One lane's part of a matrix operand whose rows are V wide: of one row the columns
-// 4j .. 4j+3 (column tiles 0 .. 3) and, of those past 64, R j .. R j + R-1 (tiles 4 ..),
-// so that a row's first 64 values are one load of 16 lanes.
+// A matrix operand whose rows are V wide goes to lanes by columns: a wave has half of
+// them, lane j of 16 columns C j .. C j + C-1 of that half, each in a column tile of its
+// own, so that a row is one contiguous load.  Columns past V repeat others; their
+// results are not stored.
 template <int V>
-__device__ __forceinline__ void load_cols(const float* p, int j, float (&f)[V / 16]) {
-    constexpr int R = V / 16 - 4;
-    const float4 c = *reinterpret_cast<const float4*>(p + 4 * j);
-    f[0] = c.x; f[1] = c.y; f[2] = c.z; f[3] = c.w;
-#pragma unroll
-    for (int i = 0; i < R; ++i) f[4 + i] = p[64 + R * j + i];
-}
+struct Cols {
+    static constexpr int C = (V / 16 + 1) / 2;
+    static constexpr bool kFull = 2 * 16 * C == V;
+    __device__ static __forceinline__ int first(int wc, int j) { return 16 * C * wc + C * j; }
+    __device__ static __forceinline__ bool stored(int wc, int j, int c) { return kFull || first(wc, j) + c < V; }
 
-// The same of a row of the qkv dtype, as it is stored.
+    // of the row at element e of a shared base
+    __device__ static __forceinline__ void load(const float* base, uint32_t e, int wc, int j, float (&f)[C]) {
+        const int at = first(wc, j);
+        if constexpr (C == 4) {
+            const float4 v = load_at<float4>(base, 4 * (e + (kFull ? at : min(at, V - 4))));
+            f[0] = v.x; f[1] = v.y; f[2] = v.z; f[3] = v.w;
+        } else if constexpr (C == 2) {
+            const float2 v = load_at<float2>(base, 4 * (e + at));
+            f[0] = v.x; f[1] = v.y;
+        } else {
+#pragma unroll
+            for (int c = 0; c < C; ++c) f[c] = load_at<float>(base, 4 * (e + (kFull ? at + c : min(at + c, V - 1))));
+        }
+    }
+    // from a buffer whose reads past the end give 0
+    __device__ static __forceinline__ void load_buf(__amdgpu_buffer_rsrc_t rs, int voff, int soff, float (&f)[C]) {
+        if constexpr (C == 4) {
+            const uint4 v = buffer_load_u4(rs, voff, soff);
+            f[0] = __uint_as_float(v.x); f[1] = __uint_as_float(v.y);
+            f[2] = __uint_as_float(v.z); f[3] = __uint_as_float(v.w);
+        } else if constexpr (C == 3) {
+            typedef unsigned u32x3 __attribute__((ext_vector_type(3)));
+            const u32x3 v = __builtin_bit_cast(u32x3, __builtin_amdgcn_raw_buffer_load_b96(rs, voff, soff, 0));
+            f[0] = __uint_as_float(v.x); f[1] = __uint_as_float(v.y); f[2] = __uint_as_float(v.z);
+        } else {
+            typedef unsigned u32x2 __attribute__((ext_vector_type(2)));
+            const u32x2 v = __builtin_bit_cast(u32x2, __builtin_amdgcn_raw_buffer_load_b64(rs, voff, soff, 0));
+            f[0] = __uint_as_float(v.x); f[1] = __uint_as_float(v.y);
+        }
+    }
+    __device__ static __forceinline__ void store(float* p, int wc, int j, const float (&f)[C]) {
+        const int at = first(wc, j);
+        if constexpr (C == 4) {
+            if (stored(wc, j, 0)) *reinterpret_cast<float4*>(p + at) = make_float4(f[0], f[1], f[2], f[3]);
+        } else if constexpr (C == 2) {
+            *reinterpret_cast<float2*>(p + at) = make_float2(f[0], f[1]);
+        } else {
+#pragma unroll
+            for (int c = 0; c < C; ++c)
+                if (stored(wc, j, c)) p[at + c] = f[c];
+        }
+    }
+};
+
+// The same columns of a row of values, as they are stored.
 template <int V, typename QT>
 struct ValueCols;
 template <int V>
 struct ValueCols<V, F32Tag> {
-    float f[V / 16];
-    __device__ __forceinline__ void zero() {
-#pragma unroll
-        for (int c = 0; c < V / 16; ++c) f[c] = 0.f;
-    }
-    __device__ __forceinline__ void load(const void* base, size_t e, int j) {
-        load_cols<V>(static_cast<const float*>(base) + e, j, f);
+    static constexpr int C = Cols<V>::C;
+    float f[C];
+    __device__ __forceinline__ void load(const void* base, uint32_t e, int wc, int j) {
+        Cols<V>::load(static_cast<const float*>(base), e, wc, j, f);
     }
     __device__ __forceinline__ float get(int c) const { return f[c]; }
     __device__ __forceinline__ void drop(int c) { f[c] = 0.f; }
+    __device__ __forceinline__ void keep(bool on) {
+#pragma unroll
+        for (int c = 0; c < C; ++c) f[c] = on ? f[c] : 0.f;
+    }
 };
 template <int V>
 struct ValueCols<V, Bf16Tag> {
-    static constexpr int R = V / 16 - 4;
-    uint32_t u[2 + (R + 1) / 2];
-    __device__ __forceinline__ void zero() {
+    static constexpr int C = Cols<V>::C;
+    uint32_t u[(C + 1) / 2];
+    __device__ __forceinline__ void keep(bool on) {
 #pragma unroll
-        for (int c = 0; c < 2 + (R + 1) / 2; ++c) u[c] = 0u;
+        for (int c = 0; c < (C + 1) / 2; ++c) u[c] = on ? u[c] : 0u;
     }
-    __device__ __forceinline__ void load(const void* base, size_t e, int j) {
-        const uint16_t* p = static_cast<const uint16_t*>(base) + e;
-        const uint2 c = *reinterpret_cast<const uint2*>(p + 4 * j);
-        u[0] = c.x;
-        u[1] = c.y;
-        p += 64 + R * j;
-        if constexpr (R == 4) {
-            const uint2 d = *reinterpret_cast<const uint2*>(p);
-            u[2] = d.x;
-            u[3] = d.y;
-        } else if constexpr (R == 2) {
-            u[2] = *reinterpret_cast<const uint32_t*>(p);
-        } else if constexpr (R > 0) {
-            u[2] = p[0];
-            if constexpr (R == 3) {
-                u[2] |= uint32_t(p[1]) << 16;
-                u[3] = p[2];
-            }
+    __device__ __forceinline__ void load(const void* base, uint32_t e, int wc, int j) {
+        const int at = Cols<V>::first(wc, j);
+        if constexpr (C == 4) {
+            const uint2 c = load_at<uint2>(base, 2 * (e + (Cols<V>::kFull ? at : min(at, V - 4))));
+            u[0] = c.x;
+            u[1] = c.y;
+        } else if constexpr (C == 2) {
+            u[0] = load_at<uint32_t>(base, 2 * (e + at));
+        } else {
+            auto one = [&](int c) { return uint32_t(load_at<uint16_t>(base, 2 * (e + min(at + c, V - 1)))); };
+            u[0] = one(0) | one(1) << 16;
+            u[1] = one(2);
         }
     }
     __device__ __forceinline__ float get(int c) const {
@@ -154,354 +209,403 @@ struct ValueCols<V, Bf16Tag> {
     __device__ __forceinline__ void drop(int c) { u[c / 2] &= c % 2 ? 0xffffu : 0xffff0000u; }
 };
 
-template <int KIND, int V, typename QT, int MT>
+// Four waves a block, two by two: wave (wk, wc) has keys 64 wk .. 64 wk + 63 and half wc of
+// the columns.
+constexpr int kTreeThreads = 256;
+
+// LDS of a block, by the call's largest tree.
+template <int KIND, int V, typename QT>
 struct TreeLds {
-    static constexpr bool DELTA = KIND != SKSSM_MAMBA2;
-    static constexpr bool KDA = KIND == SKSSM_KDA;
-    static constexpr int NT = 16 * MT, L = 16 + NT;
-    static constexpr int LP = L + 4;   // row of P; 4 rows apart in the banks
+    static constexpr bool DELTA = KIND != SKSSM_MAMBA2, KDA = KIND == SKSSM_KDA;
     static constexpr int XS = kK + 4;  // row of x
-    static constexpr int kKeyBytes = kK * Vec8<QT>::kElemBytes;
-    // what the walk uses, then the waves' sums over it
-    static constexpr int keys = 0;
-    static constexpr int dec = keys + (DELTA ? L * kKeyBytes : 0);
-    static constexpr int x = dec + (KDA ? L * kK * 4 : 0);
-    static constexpr int gram = x;                                             // Mamba-2
-    static constexpr int cs = DELTA ? keys : x + NT * LP * 4;                  // coefficients of 16 ranks
-    static constexpr int cs_end = cs + 4 * 16 * 20 * 4;
-    static constexpr int x_end = x + NT * XS * 4;
-    static constexpr int walk_end = DELTA ? x_end : cs_end;
-    static constexpr int red_end = 4 * 16 * V * 4;
-    static constexpr int p = walk_end > red_end ? walk_end : red_end;
-    static constexpr int a = p + NT * LP * 4;  // decays; Mamba-2: its window's become products
-    static constexpr int beta = a + L * 4;
-    static constexpr int up = beta + L * 4;
-    static constexpr int g = up + L * 4;       // per node: Mamba-2's product of decays
-    static constexpr int flag = g + NT * 4;
-    static constexpr int bytes = flag + 16;
-    static_assert(!DELTA || cs_end <= x, "the coefficients' sums fit the keys' place");
+    static constexpr int CS = 20;      // row of a sketch's coefficients
+    static constexpr int kKey = kK * Vec8<QT>::kElemBytes;
+    static constexpr int kCoef = 4 * 16 * CS * 4;
+    static constexpr int kRed = 2 * 2 * Cols<V>::C * 64 * 8;
+    int rows;  // window slots and nodes, a multiple of 4
+    int lp;    // row of P, 4 apart in the banks from the next one
+    int gp;    // row of a Mamba-2 tree's decays
+    int keys, dec, x, red, cs, p, g, info, node, win, anc, flag, bytes;
+
+    __host__ __device__ __forceinline__ TreeLds(int max_nodes, bool sketch) {
+        rows = 16 + (max_nodes + 3) / 4 * 4;
+        lp = 16 + (max_nodes + 15) / 16 * 16 + 4;
+        gp = rows - 16 + 1;
+        keys = 0;
+        dec = keys + (DELTA ? (rows + 1) * kKey : 0);
+        x = dec + (KDA ? (rows + 1) * kK * 4 : 0);
+        red = x + (DELTA && !KDA ? 16 * XS * 4 : 0);  // KDA: the sums take x's place
+        cs = red + (KDA && 16 * XS * 4 > kRed ? 16 * XS * 4 : kRed);
+        p = cs + (sketch ? kCoef : 0);
+        g = p + (16 * lp + 4) * 4;
+        info = g + (DELTA ? 0 : (rows - 16) * gp * 4 + 15) / 16 * 16;
+        node = info + (rows + 2) * int(sizeof(RowInfo));  // Mamba-2: a node's product of decays to the tree's root
+        win = node + (rows - 16) * 4;                     // and from each window slot to its end
+        anc = (win + 16 * 4 + 15) / 16 * 16;
+        flag = anc + (rows - 16) * 8;
+        bytes = flag + 16;
+    }
 };
 
 }  // namespace
 
-// A block per (sequence, head), MT tiles of 16 nodes; dense heads first.
+// A block per (sequence, head), heads first.  Nodes go in tiles of 16; the state stays in
+// registers from tile to tile.
 template <int KIND, int V, typename QT, int MT>
-__global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(MT == 1 ? (V <= 96 ? 4 : 3) : 2)))
-void tree_kernel(TreeArgs A, HeadTable T) {
-    typedef TreeLds<KIND, V, QT, MT> Lds;
+__global__ __launch_bounds__(kTreeThreads) __attribute__((amdgpu_waves_per_eu(4)))
+void tree_kernel(TreeArgs A, HeadTable T, int sketch_lds) {
+    typedef TreeLds<KIND, V, QT> Lds;
+    typedef Cols<V> Co;
+    typedef typename Vec8<QT>::raw_t Raw;
     constexpr bool DELTA = Lds::DELTA, KDA = Lds::KDA;
-    constexpr int CT = V / 16, R = CT - 4, E = Vec8<QT>::kElemBytes;
-    constexpr int L = Lds::L, LP = Lds::LP, XS = Lds::XS, NT = Lds::NT;
+    constexpr int C = Co::C, E = Vec8<QT>::kElemBytes, XS = Lds::XS, CS = Lds::CS, NTH = kTreeThreads;
     extern __shared__ __align__(16) char lds[];
-    float* red = reinterpret_cast<float*>(lds);
-    float* xs = reinterpret_cast<float*>(lds + Lds::x);
-    float* gram = reinterpret_cast<float*>(lds + Lds::gram);
-    float* ps = reinterpret_cast<float*>(lds + Lds::p);
-    float* as = reinterpret_cast<float*>(lds + Lds::a);
-    float* bs = reinterpret_cast<float*>(lds + Lds::beta);
-    int* up = reinterpret_cast<int*>(lds + Lds::up);
-    float* gs = reinterpret_cast<float*>(lds + Lds::g);
-    int* flag = reinterpret_cast<int*>(lds + Lds::flag);
+    const Lds Y(A.max_nodes, sketch_lds);
+    float* xs = reinterpret_cast<float*>(lds + Y.x);
+    float* ps = reinterpret_cast<float*>(lds + Y.p);
+    RowInfo* info = reinterpret_cast<RowInfo*>(lds + Y.info);
+    int* flag = reinterpret_cast<int*>(lds + Y.flag);
+    float* gn = reinterpret_cast<float*>(lds + Y.g);     // Mamba-2: decays between a node and its ancestors
+    float* gs = reinterpret_cast<float*>(lds + Y.node);  // and between it and the root
+    float* ws = reinterpret_cast<float*>(lds + Y.win);   // behind each window slot
+    // a node's path, a bit per node in two words (a 64-bit shift by a lane's amount reads a
+    // wrong register where that amount sits in the last one of the wave); 0: none
+    uint2* anc = reinterpret_cast<uint2*>(lds + Y.anc);
+    const int LP = Y.lp;
 
-    const int seq = blockIdx.x % A.n_seqs, at = blockIdx.x / A.n_seqs;
-    const int h = T.head[at], rank = T.rank[at], hk = h / A.share;
+    const int seq = blockIdx.x / A.H, at = blockIdx.x % A.H;
+    const int h = T.head[at], rank = T.rank[at], hk = int(uint32_t(h) * A.per_share >> 16);
     const TreeSpan sp = tree_span(A, seq);
     if (!sp.live) return;
-    const int tid = threadIdx.x, lane = tid & 63, w = tid >> 6;
+    const int tid = threadIdx.x, lane = tid & 63, w = __builtin_amdgcn_readfirstlane(tid >> 6);
     const int j = lane & 15, kk = lane >> 4;
+    const int wk = w & 1, wc = w >> 1;
     const int rrow = tid >> 4, l = tid & 15;
 
-    // ---- loads, in the order of their use --------------------------------------
-    const size_t win = size_t(h) * A.B + sp.row, wslot = size_t(A.H) * A.B;  // an item's window entry, a slot
-    const size_t node = size_t(sp.t0) * A.H + h;
-    const size_t kwin = size_t(hk) * A.B + sp.row, kslot = size_t(A.Hk) * A.B;
-    const size_t knode = size_t(sp.t0) * A.Hk + hk;
-    float a_r = 1.f, b_r = 1.f;
-    int up_r = kNoRow;
-    if (tid < 16) {
-        if (tid < sp.p) {
-            if (!KDA) a_r = A.abuf[win + tid * wslot];
-            if (DELTA) b_r = A.bbuf[win + tid * wslot];
-            up_r = tid - 1;
+    // ---- tokens to LDS ---------------------------------------------------------------
+    // bases of this item's window entries and nodes, which all lanes share, and the
+    // 32-bit strides of a slot and a node (a window array is below 2^32 bytes for every shape)
+    const size_t win = size_t(h) * A.B + sp.row, kwin = size_t(hk) * A.B + sp.row;
+    const size_t node = size_t(sp.t0) * A.H + h, knode = size_t(sp.t0) * A.Hk + hk;
+    const uint32_t slot = uint32_t(A.H) * A.B, kslot = uint32_t(A.Hk) * A.B, step = A.H, kstep = A.Hk;
+    const auto at_elem = [](const void* p, size_t e, int bytes) -> const void* {
+        return static_cast<const char*>(p) + e * bytes;
+    };
+    const bool held = sp.p > 0;  // without a window its loads read the first node's
+    const void* k_n = at_elem(A.k, knode * kK, E);
+    const void* q_n = at_elem(A.q, knode * kK, E);
+    const void* v_n = at_elem(A.v, node * V, E);
+    const void* k_w = held ? at_elem(A.kbuf, kwin * kK, E) : k_n;
+    const void* v_w = held ? at_elem(A.vbuf, win * V, E) : v_n;
+    const float* a_n = A.a + node * (KDA ? kK : 1);
+    const float* a_w = held ? A.abuf + win * (KDA ? kK : 1) : a_n;
+    float s[16][C];  // keys 64 wk + 8 kk + (t < 8 ? t : 24 + t)
+    {
+        RowInfo in = {Y.rows + 1, 1.f, 1.f, 0};
+        const int in_n = max(min(tid - 16, sp.len - 1), 0);
+        const uint32_t in_off = 4 * (tid < 16 ? min(tid, max(sp.p - 1, 0)) * slot : in_n * step);
+        const int par = load_at<int>(A.parents + sp.t0, 4 * in_n);
+        const bool first16 = tid < 16 && held;
+        if constexpr (!KDA) in.a = load_at<float>(first16 ? a_w : a_n, in_off);
+        if constexpr (DELTA) in.beta = load_at<float>(first16 ? A.bbuf + win : A.beta + node, in_off);
+        RowRegs<kK * E / 16, MT, NTH> kr;
+        RowRegs<kK * 4 / 16, MT, NTH> ar;
+        if constexpr (DELTA) {
+            kr.load(k_n, kstep * kK * E, sp.len, k_w, kslot * kK * E, sp.p);
+            if constexpr (KDA) ar.load(a_n, step * kK * 4, sp.len, a_w, slot * kK * 4, sp.p);
         }
-    } else if (tid < L && tid - 16 < sp.len) {
-        const int n = tid - 16;
-        if (!KDA) a_r = A.a[node + size_t(n) * A.H];
-        if (DELTA) b_r = A.beta[node + size_t(n) * A.H];
-        const int up = A.parents[sp.t0 + n];
-        up_r = up >= n || up < -1 ? kNoRow : up < 0 ? sp.p - 1 : 16 + up;
-    }
-    RowRegs<kK * E / 16, MT> kr;
-    RowRegs<kK * 4 / 16, MT> ar;
-    typename Vec8<QT>::raw_t qr[MT];
-    if constexpr (DELTA) {
-        kr.load(static_cast<const char*>(A.kbuf) + kwin * kK * E, kslot * kK * E, sp.p,
-                static_cast<const char*>(A.k) + knode * kK * E, size_t(A.Hk) * kK * E, sp.len);
-        if constexpr (KDA)
-            ar.load(reinterpret_cast<const char*>(A.abuf) + win * kK * 4, wslot * kK * 4, sp.p,
-                    reinterpret_cast<const char*>(A.a) + node * kK * 4, size_t(A.H) * kK * 4, sp.len);
+        // the state is on its way while the first tile's queries are carried back
+        if (rank == 0) {
+            const __amdgpu_buffer_rsrc_t rs = buffer_rsrc(A.S + (size_t(sp.row) * A.H + h) * (kK * V), kK * V * 4);
+            const int voff = ((64 * wk + 8 * kk) * V + Co::first(wc, j)) * 4;
 #pragma unroll
-        for (int m = 0; m < MT; ++m)
-            if (16 * m < sp.len)
-                qr[m] = Vec8<QT>::load(A.q, (knode + size_t(min(16 * m + rrow, sp.len - 1)) * A.Hk) * kK + 8 * l);
-    }
-    // values: of each 16 rows this wave takes 4
-    ValueCols<V, QT> vr[1 + MT];
-#pragma unroll
-    for (int u = 0; u <= MT; ++u) {
-        const int row = 4 * w + kk + 16 * (u > 0 ? u - 1 : 0);
-        const bool on = row < (u ? sp.len : sp.p);
-        vr[u].zero();
-        if (on)
-            vr[u].load(u ? A.v : A.vbuf, (u ? node + size_t(row) * A.H : win + row * wslot) * V, j);
-    }
-    float s[8][CT];
-    if (rank == 0) {
-        const float* S = A.S + (size_t(sp.row) * A.H + h) * (kK * V) + (32 * w + 8 * kk) * V;
-#pragma unroll
-        for (int t = 0; t < 8; ++t) load_cols<V>(S + t * V, j, s[t]);
-    }
-    __builtin_amdgcn_sched_barrier(0);
-
-    // ---- to LDS --------------------------------------------------------------------
-    if (tid < L) {
-        as[tid] = a_r;
-        bs[tid] = b_r;
-        up[tid] = up_r;
-    }
-    if (tid == 0) *flag = 0;
-    for (int i = tid; i < NT * LP; i += 256) ps[i] = 0.f;
-    if constexpr (DELTA) {
-        kr.store(lds + Lds::keys);
-        if constexpr (KDA) ar.store(lds + Lds::dec);
-    } else {  // products q k of all nodes and rows
-        for (int tile = w; tile < MT * (1 + MT); tile += 4) {
-            const int m = tile / (1 + MT), u = tile % (1 + MT);
-            if (16 * m >= sp.len || (u ? 16 * (u - 1) >= sp.len : sp.p == 0)) continue;
-            const size_t qe = (knode + size_t(min(16 * m + j, sp.len - 1)) * A.Hk) * kK + 8 * kk;
-            const void* kb = u ? A.k : A.kbuf;
-            const size_t ke = (u ? knode + size_t(min(16 * (u - 1) + j, sp.len - 1)) * A.Hk
-                                 : kwin + min(j, sp.p - 1) * kslot) * kK + 8 * kk;
-            f32x4 d = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-            for (int c = 0; c < 4; ++c) {
-                const auto qv = Vec8<QT>::load(A.q, qe + 32 * c);
-                const auto kv = Vec8<QT>::load(kb, ke + 32 * c);
-                if constexpr (E == 2) {
-                    typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
-                    d = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, qv.w),
-                                                                __builtin_bit_cast(bf16x8, kv.w), d, 0, 0, 0);
-                } else {
-                    float qf[8], kf[8];
-                    Vec8<QT>::unpack(qv, qf);
-                    Vec8<QT>::unpack(kv, kf);
-#pragma unroll
-                    for (int e = 0; e < 8; ++e) d = mfma_16x16x4(qf[e], kf[e], d);
-                }
+            for (int t = 0; t < 16; ++t) Co::load_buf(rs, voff, (t < 8 ? t : 24 + t) * V * 4, s[t]);
+        }
+        __builtin_amdgcn_sched_barrier(0);
+        if (tid < Y.rows + 2) {
+            // paths end behind slot 0, or at once without a window
+            if (tid < 16) in.up = tid > 0 ? tid - 1 : Y.rows;
+            else if (tid < Y.rows)
+                in.up = par >= in_n || par < -1 ? Y.rows + 1 : par >= 0 ? 16 + par : held ? sp.p - 1 : Y.rows;
+            else in = {tid, 0.f, 1.f, 0};
+            info[tid] = in;
+        }
+        if (tid == 0) *flag = 0;
+        if constexpr (DELTA) {
+            kr.store(lds + Y.keys, Y.rows);
+            if (tid < Lds::kKey / 16)
+                *reinterpret_cast<u32x4*>(lds + Y.keys + Y.rows * Lds::kKey + 16 * tid) = u32x4{0u, 0u, 0u, 0u};
+            if constexpr (KDA) {
+                ar.store(lds + Y.dec, Y.rows);
+                if (tid < kK) reinterpret_cast<float*>(lds + Y.dec)[Y.rows * kK + tid] = 1.f;
             }
-#pragma unroll
-            for (int i = 0; i < 4; ++i) gram[(16 * m + 4 * kk + i) * LP + 16 * u + j] = d[i];
         }
     }
     __syncthreads();
-
-    // a value that is no number must not meet the zeros of other nodes' rows: it is
-    // left out of the products and joins the nodes below it at the end
-    bool odd = false;
-#pragma unroll
-    for (int u = 0; u <= MT; ++u)
-#pragma unroll
-        for (int c = 0; c < CT; ++c)
-            if (!isfinite(vr[u].get(c))) {
-                odd = true;
-                vr[u].drop(c);
-            }
-    if (odd) *flag = 1;
-
-    // ---- the walk --------------------------------------------------------------------
-    bool ok[MT];
-    if constexpr (DELTA) {
-#pragma unroll
-        for (int m = 0; m < MT; ++m) {
-            const int n = 16 * m + rrow;
-            ok[m] = false;
-            if (n < sp.len) {
-                float x[8], g = 1.f;
-                Vec8<QT>::unpack(qr[m], x);
-                int row = 16 + n;
-                while (row >= 0) {
-                    float kf[8];
-                    Vec8<QT>::unpack(Vec8<QT>::load(lds + Lds::keys, row * kK + 8 * l), kf);
-                    const float c = bs[row] * row_sum16(dot8(kf, x));
-#pragma unroll
-                    for (int e = 0; e < 8; ++e) x[e] = fmaf(-c, kf[e], x[e]);
-                    if constexpr (KDA) {
-                        float af[8];
-                        load8f(reinterpret_cast<const float*>(lds + Lds::dec) + row * kK + 8 * l, af);
-#pragma unroll
-                        for (int e = 0; e < 8; ++e) x[e] *= af[e];
-                    }
-                    if (l == 0) ps[n * LP + row] = g * c;
-                    if constexpr (!KDA) g *= as[row];
-                    row = up[row];
-                }
-                ok[m] = row == -1;
-                if constexpr (!KDA) {
-#pragma unroll
-                    for (int e = 0; e < 8; ++e) x[e] *= g;
-                }
-                store8f(xs + n * XS + 8 * l, x);
-            }
-        }
-    } else {
-        if (tid < sp.len) {  // the nodes of the path
+    float all = 1.f;  // Mamba-2: the whole window's decays
+    if constexpr (!DELTA) {
+        if (tid < sp.len) {
             float g = 1.f;
+            uint2 path = make_uint2(0u, 0u);
             int row = 16 + tid;
-            while (row >= 16) {
-                ps[tid * LP + row] = g * gram[tid * LP + row];
-                g *= as[row];
-                row = up[row];
+            while (row >= 16 && row < Y.rows) {
+                gn[tid * Y.gp + row - 16] = g;
+                const uint32_t bit = 1u << (row - 16 & 31);
+                path.x |= row < 48 ? bit : 0u;
+                path.y |= row < 48 ? 0u : bit;
+                g *= info[row].a;
+                row = info[row].up;
             }
             gs[tid] = g;
-            if (row == kNoRow) up[16 + tid] = kNoRow;  // (a walk that meets this entry meets the other one too)
+            anc[tid] = row == Y.rows + 1 ? make_uint2(0u, 0u) : path;
         }
-    }
-    __syncthreads();
-    f32x4 d[MT][CT];
-    if constexpr (!DELTA) {
-#pragma unroll
-        for (int m = 0; m < MT; ++m) ok[m] = 16 * m + rrow < sp.len && up[16 + 16 * m + rrow] != kNoRow;
-    }
-    // products of the decays from each slot's successor to the window's end
-    float after = 1.f, all = 1.f;
-    if constexpr (!DELTA) {
         for (int i = sp.p - 1; i >= 0; --i) {
-            if (i == 4 * w + kk) after = all;
-            all *= as[i];
+            if (tid == 64) ws[i] = all;
+            all *= info[i].a;
         }
+        __syncthreads();
     }
 
-    // ---- the state, or the sketch ----------------------------------------------------
-#pragma unroll
-    for (int m = 0; m < MT; ++m)
-#pragma unroll
-        for (int c = 0; c < CT; ++c) d[m][c] = f32x4{0.f, 0.f, 0.f, 0.f};
-    auto x_of = [&](int m, float (&x)[8]) {  // node 16 m + j, key elements 32 w + 8 kk ..
-        if constexpr (DELTA) load8f(xs + (16 * m + j) * XS + 32 * w + 8 * kk, x);
-        else Vec8<QT>::unpack(Vec8<QT>::load(A.q, (knode + size_t(min(16 * m + j, sp.len - 1)) * A.Hk) * kK + 32 * w + 8 * kk), x);
-    };
-    if (rank == 0) {
-#pragma unroll
-        for (int m = 0; m < MT; ++m) {
-            if (16 * m >= sp.len) continue;
-            float x[8];
-            x_of(m, x);
-#pragma unroll
-            for (int t = 0; t < 8; ++t)
-#pragma unroll
-                for (int c = 0; c < CT; ++c) d[m][c] = mfma_16x16x4(x[t], s[t][c], d[m][c]);
-        }
-    } else {
-        const float* F = A.frames + size_t(T.frow[at]) * kK;
-        const float* Z = A.Z + (size_t(T.zrow[at]) * A.B + size_t(sp.row) * rank) * V;
-        f32x4 c[MT];
+    const int j_lane = j, kk_lane = kk;
 #pragma unroll 1
-        for (int r0 = 0; r0 < rank; r0 += 16) {
-            float f[8], z[CT];
-            load8f(F + min(r0 + j, rank - 1) * kK + 32 * w + 8 * kk, f);
-#pragma unroll
-            for (int i = 0; i < CT; ++i) z[i] = 0.f;
-            if (r0 + 4 * w + kk < rank) load_cols<V>(Z + (r0 + 4 * w + kk) * V, j, z);
-#pragma unroll
-            for (int m = 0; m < MT; ++m) {
-                c[m] = f32x4{0.f, 0.f, 0.f, 0.f};
-                if (16 * m >= sp.len) continue;
-                float x[8];
-                x_of(m, x);
-#pragma unroll
-                for (int t = 0; t < 8; ++t) c[m] = mfma_16x16x4(x[t], f[t], c[m]);
-            }
-            // c's sums over the waves' keys
-            float* cs = reinterpret_cast<float*>(lds + Lds::cs);
-#pragma unroll
-            for (int m = 0; m < MT; ++m) {
-                if (16 * m >= sp.len) break;
-                __syncthreads();
-#pragma unroll
-                for (int i = 0; i < 4; ++i) cs[(w * 16 + 4 * kk + i) * 20 + j] = c[m][i];
-                __syncthreads();
-                float y = 0.f;
-#pragma unroll
-                for (int i = 0; i < 4; ++i) y += cs[(i * 16 + j) * 20 + 4 * w + kk];
-                if (r0 + 4 * w + kk >= rank) y = 0.f;
-#pragma unroll
-                for (int i = 0; i < CT; ++i) d[m][i] = mfma_16x16x4(y, z[i], d[m][i]);
-            }
-        }
-    }
-
-    // ---- the path's values, the waves' sums ---------------------------------------
-#pragma unroll
     for (int m = 0; m < MT; ++m) {
         if (16 * m >= sp.len) break;
+        const int n0 = 16 * m, left = sp.len - n0;
+        // a tile's addresses are formed anew: kept from tile to tile they take the registers
+        // of another wave
+        int j = j_lane, kk = kk_lane;
+        if constexpr (MT > 1) asm volatile("" : "+v"(j), "+v"(kk));
+        Raw qx[2];  // Mamba-2: this wave's keys of node n0 + j's query
+        if constexpr (DELTA) {
+            // ---- the walk: 16 lanes a node, a wave's four until the last one ends --------
+            const int n = n0 + min(rrow, left - 1), end = Y.rows;
+            float x[8], g = 1.f;
+            Vec8<QT>::unpack(load_at<Raw>(q_n, (n * kstep * kK + 8 * l) * E), x);
+            float* pr = ps + rrow * LP;
+            for (int i = l; i < LP; i += 16) pr[i] = 0.f;
+            // a row's operands are read while the one before is in use; the rows that end
+            // paths have the key 0 and lead to themselves
+            struct Step {
+                RowInfo in;
+                Raw k;
+                float a[8];
+            };
+            auto read = [&](Step& t, int row) {
+                const int r = min(row, end);
+                t.in = info[row];
+                t.k = Vec8<QT>::load(lds + Y.keys, r * kK + 8 * l);
+                if constexpr (KDA) load8f(reinterpret_cast<const float*>(lds + Y.dec) + r * kK + 8 * l, t.a);
+            };
+            auto take = [&](const Step& t, int row) {
+                float k[8];
+                Vec8<QT>::unpack(t.k, k);
+                const bool on = row < end;
+                const float c = on ? t.in.beta * row_sum16(dot8(k, x)) : 0.f;
+#pragma unroll
+                for (int e = 0; e < 8; ++e) {
+                    x[e] = fmaf(-c, k[e], x[e]);
+                    if constexpr (KDA) x[e] *= t.a[e];
+                }
+                // lane 0 notes the product; the others, and ended paths, write behind P
+                ps[on && l == 0 ? rrow * LP + row : 16 * LP] = g * c;
+                if constexpr (!KDA) g *= t.in.a;
+            };
+            int row = rrow < left ? 16 + n : end;
+            Step s0, s1;
+            read(s0, row);
+            while (__any(row < end)) {
+                const int r1 = s0.in.up;
+                read(s1, r1);
+                take(s0, row);
+                row = s1.in.up;
+                read(s0, row);
+                take(s1, r1);
+            }
+            if (l == 0 && rrow < left) anc[n] = make_uint2(row == end, 0u);
+            if constexpr (!KDA) {
+#pragma unroll
+                for (int e = 0; e < 8; ++e) x[e] *= g;
+            }
+            store8f(xs + rrow * XS + 8 * l, x);
+        } else {
+            // ---- products q k, each with the decays between its tokens -------------------
+            const uint32_t qe = (uint32_t(n0 + min(j, left - 1)) * kstep * kK + 8 * kk) * E;
+            Raw qf[4];
+#pragma unroll
+            for (int c = 0; c < 4; ++c) qf[c] = load_at<Raw>(q_n, qe + 32 * E * c);
+            qx[0] = load_at<Raw>(q_n, qe + E * (rank ? 32 * w : 64 * wk));
+            qx[1] = load_at<Raw>(q_n, qe + E * (rank ? 32 * w : 64 * wk + 32));
+            for (int u = w; u <= m + 1; u += 4) {
+                if (u == 0 && !held) continue;
+                const uint32_t ke = ((u ? min(16 * (u - 1) + j, sp.len - 1) * kstep : min(j, sp.p - 1) * kslot) * kK +
+                                     8 * kk) * E;
+                Raw kf[4];
+#pragma unroll
+                for (int c = 0; c < 4; ++c) kf[c] = load_at<Raw>(u ? k_n : k_w, ke + 32 * E * c);
+                f32x4 d = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+                for (int c = 0; c < 4; ++c) {
+                    if constexpr (E == 2) {
+                        typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
+                        d = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, qf[c].w),
+                                                                    __builtin_bit_cast(bf16x8, kf[c].w), d, 0, 0, 0);
+                    } else {
+                        float x[8], k[8];
+                        Vec8<QT>::unpack(qf[c], x);
+                        Vec8<QT>::unpack(kf[c], k);
+#pragma unroll
+                        for (int e = 0; e < 8; ++e) d = mfma_16x16x4(x[e], k[e], d);
+                    }
+                }
+                const int r = 16 * (u - 1) + j;
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    const int rn = 4 * kk + i, n = n0 + min(rn, left - 1);
+                    float f;
+                    if (u == 0) {
+                        f = gs[n] * ws[j] * d[i];
+                        f = j < sp.p ? f : 0.f;
+                    } else {
+                        const uint2 path = anc[n];
+                        f = gn[n * Y.gp + min(r, sp.len - 1)] * d[i];
+                        f = r < sp.len && ((r < 32 ? path.x : path.y) >> (r & 31) & 1u) ? f : 0.f;
+                    }
+                    ps[rn * LP + 16 * u + j] = f;
+                }
+            }
+        }
+        __syncthreads();
+
+        // ---- values: of each 16 rows 8 wk + 4 i + kk, i = 0, 1; NB groups on their way ---
+        constexpr int NB = 2;
+        ValueCols<V, QT> vr[NB][2];
+        auto load_values = [&](int u) {
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+                const int row = 8 * wk + 4 * i + kk;
+                if (u == 0) vr[u % NB][i].load(v_w, max(min(row, sp.p - 1), 0) * (slot * V), wc, j);
+                else vr[u % NB][i].load(v_n, min(16 * (u - 1) + row, sp.len - 1) * (step * V), wc, j);
+            }
+        };
+#pragma unroll
+        for (int u = 0; u < NB; ++u) load_values(u);
+
+        // ---- the state, or the sketch ------------------------------------------------
+        f32x4 d[C];
+#pragma unroll
+        for (int c = 0; c < C; ++c) d[c] = f32x4{0.f, 0.f, 0.f, 0.f};
+        if (rank == 0) {
+#pragma unroll
+            for (int t8 = 0; t8 < 2; ++t8) {
+                float x[8];
+                if constexpr (DELTA) load8f(xs + j * XS + 64 * wk + 32 * t8 + 8 * kk, x);
+                else Vec8<QT>::unpack(qx[t8], x);
+#pragma unroll
+                for (int t = 0; t < 8; ++t)
+#pragma unroll
+                    for (int c = 0; c < C; ++c) d[c] = mfma_16x16x4(x[t], s[8 * t8 + t][c], d[c]);
+            }
+        } else {
+            const float* F = A.frames + size_t(T.frow[at]) * kK;
+            const float* Z = A.Z + (size_t(T.zrow[at]) * A.B + size_t(sp.row) * rank) * V;
+            float x[8];  // node n0 + j, key elements 32 w + 8 kk ..
+            if constexpr (DELTA) load8f(xs + j * XS + 32 * w + 8 * kk, x);
+            else Vec8<QT>::unpack(qx[0], x);
+            float* cs = reinterpret_cast<float*>(lds + Y.cs);
+#pragma unroll 1
+            for (int r0 = 0; r0 < rank; r0 += 16) {
+                float z[2][C];
+                const uint32_t fe = 4 * (min(r0 + j, rank - 1) * kK + 32 * w + 8 * kk);
+                const f32x4 f0 = load_at<f32x4>(F, fe), f1 = load_at<f32x4>(F, fe + 16);
+#pragma unroll
+                for (int i = 0; i < 2; ++i) Co::load(Z, min(r0 + 8 * wk + 4 * i + kk, rank - 1) * V, wc, j, z[i]);
+                f32x4 q = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+                for (int t = 0; t < 8; ++t) q = mfma_16x16x4(x[t], t < 4 ? f0[t & 3] : f1[t & 3], q);
+                if (r0) __syncthreads();  // the coefficients before are read
+#pragma unroll
+                for (int i = 0; i < 4; ++i) cs[(w * 16 + 4 * kk + i) * CS + j] = q[i];
+                __syncthreads();
+#pragma unroll
+                for (int i = 0; i < 2; ++i) {
+                    const int r = 8 * wk + 4 * i + kk;
+                    float y = 0.f;
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) y += cs[(e * 16 + j) * CS + r];
+                    const bool on = r0 + r < rank;
+                    y = on ? y : 0.f;
+#pragma unroll
+                    for (int c = 0; c < C; ++c) d[c] = mfma_16x16x4(y, on ? z[i][c] : 0.f, d[c]);
+                }
+            }
+        }
+
+        // ---- the path's values ---------------------------------------------------------
+        // a value that is no number must not meet the zeros of other nodes' rows: it is
+        // left out of the products and joins the nodes below it at the end
         if constexpr (!DELTA) {  // what the state gave decays over the whole path
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
-                const float g = all * gs[16 * m + 4 * kk + i];
+                const float g = all * gs[n0 + min(4 * kk + i, left - 1)];
 #pragma unroll
-                for (int c = 0; c < CT; ++c) d[m][c][i] *= g;
+                for (int c = 0; c < C; ++c) d[c][i] *= g;
             }
         }
+        bool odd = false;
 #pragma unroll
         for (int u = 0; u <= MT; ++u) {
-            if (u ? 16 * (u - 1) >= sp.len : sp.p == 0) continue;
-            const int n = 16 * m + j, row = 16 * u + 4 * w + kk;
-            float pv;
-            if (!DELTA && u == 0) {
-                pv = row < sp.p && n < sp.len ? gs[n] * after * gram[n * LP + row] : 0.f;
-                ps[n * LP + row] = pv;
-            } else {
-                pv = ps[n * LP + row];
+            if (u > m + 1) break;
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+                ValueCols<V, QT>& vu = vr[u % NB][i];
+                vu.keep(8 * wk + 4 * i + kk + 16 * (u ? u - 1 : 0) < (u ? sp.len : sp.p));
+#pragma unroll
+                for (int c = 0; c < C; ++c)
+                    if (!isfinite(vu.get(c))) {
+                        odd = true;
+                        vu.drop(c);
+                    }
+                const float pv = u || held ? ps[j * LP + 16 * u + 8 * wk + 4 * i + kk] : 0.f;
+#pragma unroll
+                for (int c = 0; c < C; ++c) d[c] = mfma_16x16x4(pv, vu.get(c), d[c]);
             }
-#pragma unroll
-            for (int c = 0; c < CT; ++c) d[m][c] = mfma_16x16x4(pv, vr[u].get(c), d[m][c]);
+            if (u + NB <= MT && u + NB <= m + 1) load_values(u + NB);
         }
-    }
+        if (odd) *flag = 1;
+        // ---- the two halves of the keys: each wave keeps nodes 4 kk + 2 wk + i -------
+        if constexpr (KDA) __syncthreads();  // x is read
+        float* red = reinterpret_cast<float*>(lds + Y.red) + wc * (2 * C * 64 * 2) + 2 * lane;
 #pragma unroll
-    for (int m = 0; m < MT; ++m) {
-        if (16 * m >= sp.len) break;
+        for (int c = 0; c < C; ++c)
+            *reinterpret_cast<float2*>(red + (wk * C + c) * 128) =
+                wk ? make_float2(d[c][0], d[c][1]) : make_float2(d[c][2], d[c][3]);
         __syncthreads();
+        float y[2][C];
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            float* to = red + (w * 16 + 4 * kk + i) * V;
-            *reinterpret_cast<float4*>(to + 4 * j) = make_float4(d[m][0][i], d[m][1][i], d[m][2][i], d[m][3][i]);
-#pragma unroll
-            for (int c = 0; c < R; ++c) to[64 + R * j + c] = d[m][4 + c][i];
+        for (int c = 0; c < C; ++c) {
+            const float2 o = *reinterpret_cast<const float2*>(red + ((1 - wk) * C + c) * 128);
+            y[0][c] = (wk ? d[c][2] : d[c][0]) + o.x;
+            y[1][c] = (wk ? d[c][3] : d[c][1]) + o.y;
         }
-        __syncthreads();
-        if (ok[m] && l < V / 8) {
-            const int n = 16 * m + rrow;
-            float y[8];
-            load8f(red + rrow * V + 8 * l, y);
+        const bool fix = *flag;
 #pragma unroll
-            for (int u = 1; u < 4; ++u) {
-                float f[8];
-                load8f(red + (u * 16 + rrow) * V + 8 * l, f);
+        for (int i = 0; i < 2; ++i) {
+            const int rn = 4 * kk + 2 * wk + i, n = n0 + rn;
+            if (rn < left && (anc[n].x | anc[n].y)) {
+                if (fix) {
+                    for (int row = 16 + n; row < Y.rows; row = info[row].up) {
+                        ValueCols<V, QT> f;
+                        f.load(row < 16 ? v_w : v_n, (row < 16 ? row * slot : (row - 16) * step) * V, wc, j);
 #pragma unroll
-                for (int e = 0; e < 8; ++e) y[e] += f[e];
-            }
-            if (*flag) {
-                for (int row = 16 + n; row >= 0; row = up[row]) {
-                    float f[8];
-                    Vec8<QT>::unpack(row < 16 ? Vec8<QT>::load(A.vbuf, (win + row * wslot) * V + 8 * l)
-                                              : Vec8<QT>::load(A.v, (node + size_t(row - 16) * A.H) * V + 8 * l), f);
-#pragma unroll
-                    for (int e = 0; e < 8; ++e)
-                        if (!isfinite(f[e])) y[e] = fmaf(ps[n * LP + row], f[e], y[e]);
+                        for (int c = 0; c < C; ++c)
+                            if (!isfinite(f.get(c))) y[i][c] = fmaf(ps[rn * LP + row], f.get(c), y[i][c]);
+                    }
                 }
+                Co::store(A.y + (node + size_t(n) * A.H) * V, wc, j, y[i]);
             }
-            store8f(A.y + (node + size_t(n) * A.H) * V + 8 * l, y);
         }
+        // KDA: the next x takes the sums' place; all: P is read above
+        if (KDA || fix) __syncthreads();
     }
 }
 
@@ -615,14 +719,16 @@ namespace {
 
 template <int KIND, int V, typename QT, int MT>
 hipError_t launch_tree_m(const TreeArgs& a, const HeadTable& t, hipStream_t s) {
-    constexpr int bytes = TreeLds<KIND, V, QT, MT>::bytes;
-    if (!launch_fits(double(a.n_seqs) * a.H, 256)) return hipErrorInvalidConfiguration;
+    const bool sketch = a.n_dense < a.H;
+    const int bytes = TreeLds<KIND, V, QT>(a.max_nodes, sketch).bytes;
+    if (!launch_fits(double(a.n_seqs) * a.H, kTreeThreads)) return hipErrorInvalidConfiguration;
     if (bytes > 65536) {
         const hipError_t e = hipFuncSetAttribute(reinterpret_cast<const void*>(tree_kernel<KIND, V, QT, MT>),
                                                  hipFuncAttributeMaxDynamicSharedMemorySize, bytes);
         if (e != hipSuccess) return e;
     }
-    hipLaunchKernelGGL((tree_kernel<KIND, V, QT, MT>), dim3(a.n_seqs * a.H), dim3(256), bytes, s, a, t);
+    hipLaunchKernelGGL((tree_kernel<KIND, V, QT, MT>), dim3(a.n_seqs * a.H), dim3(kTreeThreads), bytes, s, a, t,
+                       int(sketch));
     return hipGetLastError();
 }
 
@@ -707,7 +813,8 @@ extern "C" sketchssm_status sketchssm_tree_read(const sketchssm_plan* plan, cons
     A.max_nodes = max_nodes;
     A.H = sh.H;
     A.Hk = kq_heads_of(sh);
-    A.share = sh.H / A.Hk;
+    const uint32_t share = uint32_t(sh.H / A.Hk);
+    A.per_share = (65536 + share - 1) / share;
     A.n_dense = plan->n_dense;
     hipStream_t s = static_cast<hipStream_t>(stream);
     const hipError_t e = sh.qkv == SKSSM_BF16 ? launch_tree<Bf16Tag>(sh.kind, sh.V, A, plan->table, s)
