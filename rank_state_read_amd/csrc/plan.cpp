@@ -121,6 +121,15 @@ static sketchssm_status make_plan(const sketchssm_shape* shape, const int32_t* r
             p->table.frow[i] = rank[h] ? static_cast<uint32_t>(p->frame_row_off[p->frame_index[h]]) : 0u;
             p->table.zrow[i] = static_cast<uint32_t>(p->z_row_off[h]);
         }
+        std::memset(&p->by_head, 0, sizeof(p->by_head));
+        for (int i = 0; i < H; ++i) {
+            const int h = p->order[i];
+            p->by_head.head[h] = p->table.head[i];
+            p->by_head.rank[h] = p->table.rank[i];
+            p->by_head.group[h] = p->table.group[i];
+            p->by_head.frow[h] = p->table.frow[i];
+            p->by_head.zrow[h] = p->table.zrow[i];
+        }
     } catch (...) {
         delete p;
         return SKSSM_ENOMEM;

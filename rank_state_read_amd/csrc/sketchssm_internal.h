@@ -51,4 +51,5 @@ struct sketchssm_plan {
     size_t z_elems = 0;
     size_t frame_elems = 0;
     skssm::HeadTable table;
+    skssm::HeadTable by_head;  // the same entries, that of head h at h
 };

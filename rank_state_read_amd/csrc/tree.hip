@@ -137,16 +137,16 @@ struct Cols {
     // from a buffer whose reads past the end give 0
     __device__ static __forceinline__ void load_buf(__amdgpu_buffer_rsrc_t rs, int voff, int soff, float (&f)[C]) {
         if constexpr (C == 4) {
-            const uint4 v = buffer_load_u4(rs, voff, soff);
+            const uint4 v = buffer_load_u4_nt(rs, voff, soff);
             f[0] = __uint_as_float(v.x); f[1] = __uint_as_float(v.y);
             f[2] = __uint_as_float(v.z); f[3] = __uint_as_float(v.w);
         } else if constexpr (C == 3) {
             typedef unsigned u32x3 __attribute__((ext_vector_type(3)));
-            const u32x3 v = __builtin_bit_cast(u32x3, __builtin_amdgcn_raw_buffer_load_b96(rs, voff, soff, 0));
+            const u32x3 v = __builtin_bit_cast(u32x3, __builtin_amdgcn_raw_buffer_load_b96(rs, voff, soff, 2));
             f[0] = __uint_as_float(v.x); f[1] = __uint_as_float(v.y); f[2] = __uint_as_float(v.z);
         } else {
             typedef unsigned u32x2 __attribute__((ext_vector_type(2)));
-            const u32x2 v = __builtin_bit_cast(u32x2, __builtin_amdgcn_raw_buffer_load_b64(rs, voff, soff, 0));
+            const u32x2 v = __builtin_bit_cast(u32x2, __builtin_amdgcn_raw_buffer_load_b64(rs, voff, soff, 2));
             f[0] = __uint_as_float(v.x); f[1] = __uint_as_float(v.y);
         }
     }
@@ -252,7 +252,7 @@ struct TreeLds {
 // A block per (sequence, head), heads first.  Nodes go in tiles of 16; the state stays in
 // registers from tile to tile.
 template <int KIND, int V, typename QT, int MT>
-__global__ __launch_bounds__(kTreeThreads) __attribute__((amdgpu_waves_per_eu(4)))
+__global__ __launch_bounds__(kTreeThreads) __attribute__((amdgpu_waves_per_eu(3)))
 void tree_kernel(TreeArgs A, HeadTable T, int sketch_lds) {
     typedef TreeLds<KIND, V, QT> Lds;
     typedef Cols<V> Co;
@@ -609,6 +609,376 @@ void tree_kernel(TreeArgs A, HeadTable T, int sketch_lds) {
     }
 }
 
+// ---------------------------------------------------------------------------
+// Mamba-2: a wave per (sequence, head), up to 16 MT nodes.  Queries are not changed on
+// the way but for the decays, so there is no walk over keys: y = g (q S) + P v with P the
+// products q k times the decays between two tokens of a path.  Nothing is shared by the
+// waves of a block.
+// ---------------------------------------------------------------------------
+namespace {
+
+// What this lane wrote to LDS may be read by the wave's other lanes.
+__device__ __forceinline__ void wave_lds() {
+    __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+    __builtin_amdgcn_wave_barrier();
+}
+
+typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
+
+// Eight floats as three vectors of bf16 whose sum they are: the first 8 bits of each, the
+// next 8 and the rest.  Products with bf16 numbers are then exact before they are summed.
+__device__ __forceinline__ void split3(const float (&f)[8], bf16x8 (&out)[3]) {
+    uint32_t u[3][4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        uint32_t a[2][3];
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+            const float x = f[2 * i + e];
+            a[e][0] = __float_as_uint(x);
+            const float r = x - __uint_as_float(a[e][0] & 0xffff0000u);
+            a[e][1] = __float_as_uint(r);
+            a[e][2] = __float_as_uint(r - __uint_as_float(a[e][1] & 0xffff0000u));
+        }
+#pragma unroll
+        for (int s = 0; s < 3; ++s) u[s][i] = __builtin_amdgcn_perm(a[1][s], a[0][s], 0x07060302u);  // the upper halves
+    }
+#pragma unroll
+    for (int s = 0; s < 3; ++s) out[s] = __builtin_bit_cast(bf16x8, (u32x4{u[s][0], u[s][1], u[s][2], u[s][3]}));
+}
+
+// All V columns of a row for 16 lanes: lane j has 4j .. 4j+3 (tiles 0 .. 3) and, of those
+// past 64, R j .. R j + R-1 (tiles 4 ..).
+template <int V>
+struct AllCols {
+    static constexpr int CT = V / 16, R = CT - 4;
+    __device__ static __forceinline__ void load(const float* base, uint32_t e, int j, float (&f)[CT]) {
+        const f32x4 c = load_at<f32x4>(base, 4 * (e + 4 * j));
+#pragma unroll
+        for (int i = 0; i < 4; ++i) f[i] = c[i];
+        if constexpr (R == 4) {
+            const f32x4 d = load_at<f32x4>(base, 4 * (e + 64 + 4 * j));
+#pragma unroll
+            for (int i = 0; i < 4; ++i) f[4 + i] = d[i];
+        } else {
+#pragma unroll
+            for (int i = 0; i < R; ++i) f[4 + i] = load_at<float>(base, 4 * (e + 64 + R * j + i));
+        }
+    }
+    __device__ static __forceinline__ void load(const uint16_t* base, uint32_t e, int j, float (&f)[CT]) {
+        const uint2 c = load_at<uint2>(base, 2 * (e + 4 * j));
+        const uint32_t u[2] = {c.x, c.y};
+#pragma unroll
+        for (int i = 0; i < 4; ++i) f[i] = __uint_as_float(i % 2 ? u[i / 2] & 0xffff0000u : u[i / 2] << 16);
+        if constexpr (R == 4) {
+            const uint2 d = load_at<uint2>(base, 2 * (e + 64 + 4 * j));
+            const uint32_t v[2] = {d.x, d.y};
+#pragma unroll
+            for (int i = 0; i < 4; ++i) f[4 + i] = __uint_as_float(i % 2 ? v[i / 2] & 0xffff0000u : v[i / 2] << 16);
+        } else {
+#pragma unroll
+            for (int i = 0; i < R; ++i)
+                f[4 + i] = __uint_as_float(uint32_t(load_at<uint16_t>(base, 2 * (e + 64 + R * j + i))) << 16);
+        }
+    }
+    __device__ static __forceinline__ void store(float* p, int j, const float (&f)[CT]) {
+        *reinterpret_cast<float4*>(p + 4 * j) = make_float4(f[0], f[1], f[2], f[3]);
+        if constexpr (R == 4) {
+            *reinterpret_cast<float4*>(p + 64 + 4 * j) = make_float4(f[4], f[5], f[6], f[7]);
+        } else {
+#pragma unroll
+            for (int i = 0; i < R; ++i) p[64 + R * j + i] = f[4 + i];
+        }
+    }
+};
+
+// LDS of one wave.
+template <int MT>
+struct ScanLds {
+    static constexpr int ROWS = 16 + 16 * MT;
+    static constexpr int LP = ROWS + 4;  // row of P, 4 apart in the banks from the next one
+    static constexpr int CS = 20;        // row of a sketch's coefficients
+    float p[16 * LP];
+    float c[16 * CS];
+    float a[ROWS];
+    int up[ROWS];  // the row before on a path: -1 none, -2 no path
+    float ws[16];  // decays behind each window slot
+    float gs[16];  // a node's decays to the tree's root
+    uint2 path[16];
+};
+
+}  // namespace
+
+template <int V, typename QT, int MT>
+__global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(MT == 1 ? 4 : MT == 2 ? 3 : 2)))
+void tree_scan_kernel(TreeArgs A, HeadTable T) {
+    typedef AllCols<V> Co;
+    typedef typename Vec8<QT>::raw_t Raw;
+    typedef typename std::conditional<std::is_same<QT, Bf16Tag>::value, uint16_t, float>::type Elem;
+    constexpr int CT = Co::CT, E = Vec8<QT>::kElemBytes, LP = ScanLds<MT>::LP, CS = ScanLds<MT>::CS;
+    constexpr bool BF = E == 2;
+    __shared__ __align__(16) ScanLds<MT> lds[4];
+    const int tid = threadIdx.x, lane = tid & 63, w = __builtin_amdgcn_readfirstlane(tid >> 6);
+    ScanLds<MT>& Y = lds[w];
+    const int item = blockIdx.x * 4 + w;
+    const int seq = item / A.H, h = item - seq * A.H;
+    if (seq >= A.n_seqs) return;
+    const TreeSpan sp = tree_span(A, seq);
+    if (!sp.live) return;
+    const int rank = T.rank[h], hk = int(uint32_t(h) * A.per_share >> 16);
+    const int j = lane & 15, kk = lane >> 4;
+    const bool held = sp.p > 0;
+    const uint32_t slot = uint32_t(A.H) * A.B, kslot = uint32_t(A.Hk) * A.B, step = A.H, kstep = A.Hk;
+    const size_t win = size_t(h) * A.B + sp.row, node = size_t(sp.t0) * A.H + h;
+    const size_t kwin = size_t(hk) * A.B + sp.row, knode = size_t(sp.t0) * A.Hk + hk;
+    const char* q_n = static_cast<const char*>(A.q) + knode * kK * E;
+    const char* k_n = static_cast<const char*>(A.k) + knode * kK * E;
+    const char* k_w = held ? static_cast<const char*>(A.kbuf) + kwin * kK * E : k_n;
+    const Elem* v_n = static_cast<const Elem*>(A.v) + node * V;
+    const Elem* v_w = held ? static_cast<const Elem*>(A.vbuf) + win * V : v_n;
+
+    // ---- rows: decays, and which one stands before --------------------------------------
+#pragma unroll
+    for (int r0 = 0; r0 < 16 * (1 + MT); r0 += 64) {
+        const int r = r0 + lane;
+        const int n = max(min(r - 16, sp.len - 1), 0);
+        const bool in_w = r < 16 && held;
+        const float a = load_at<float>(in_w ? A.abuf + win : A.a + node,
+                                       4 * (r < 16 ? min(r, max(sp.p - 1, 0)) * slot : n * step));
+        const int par = load_at<int>(A.parents + sp.t0, 4 * n);
+        if (r < 16 * (1 + MT)) {
+            Y.a[r] = a;
+            Y.up[r] = par >= n || par < -1 ? -2 : par < 0 ? -1 : 16 + par;
+        }
+    }
+
+    // ---- q times the state, or the sketch ----------------------------------------------
+    f32x4 d[MT][CT];
+#pragma unroll
+    for (int m = 0; m < MT; ++m)
+#pragma unroll
+        for (int c = 0; c < CT; ++c) d[m][c] = f32x4{0.f, 0.f, 0.f, 0.f};
+    auto q_at = [&](int m, int key) {  // node 16 m + j, key elements key + 8 kk ..
+        return load_at<Raw>(q_n, (uint32_t(min(16 * m + j, sp.len - 1)) * kstep * kK + key + 8 * kk) * E);
+    };
+    // d += q f^T over 32 keys
+    auto multiply = [&](const Raw& q, const float (&f)[8], f32x4 d) {
+        if constexpr (BF) {
+            bf16x8 t[3];
+            split3(f, t);
+#pragma unroll
+            for (int s = 0; s < 3; ++s)
+                d = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, q.w), t[s], d, 0, 0, 0);
+        } else {
+            float x[8];
+            Vec8<QT>::unpack(q, x);
+#pragma unroll
+            for (int t = 0; t < 8; ++t) d = mfma_16x16x4(x[t], f[t], d);
+        }
+        return d;
+    };
+    if (rank == 0) {
+        const float* S = A.S + (size_t(sp.row) * A.H + h) * (kK * V);
+#pragma unroll 1
+        for (int b = 0; b < 4; ++b) {
+            float s[8][CT];
+#pragma unroll
+            for (int t = 0; t < 8; ++t) Co::load(S, (32 * b + 8 * kk + t) * V, j, s[t]);
+            Raw q[MT];
+#pragma unroll
+            for (int m = 0; m < MT; ++m) q[m] = q_at(m, 32 * b);
+            __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+            for (int c = 0; c < CT; ++c) {  // one column tile's terms at a time
+                float f[8];
+#pragma unroll
+                for (int t = 0; t < 8; ++t) f[t] = s[t][c];
+                if constexpr (BF) {
+                    bf16x8 t[3];
+                    split3(f, t);
+#pragma unroll
+                    for (int m = 0; m < MT; ++m)
+                        if (16 * m < sp.len)
+#pragma unroll
+                            for (int e = 0; e < 3; ++e)
+                                d[m][c] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, q[m].w), t[e],
+                                                                                  d[m][c], 0, 0, 0);
+                } else {
+#pragma unroll
+                    for (int m = 0; m < MT; ++m)
+                        if (16 * m < sp.len) d[m][c] = multiply(q[m], f, d[m][c]);
+                }
+                __builtin_amdgcn_sched_barrier(0);
+            }
+        }
+    } else {
+        const float* F = A.frames + size_t(T.frow[h]) * kK;
+        const float* Z = A.Z + (size_t(T.zrow[h]) * A.B + size_t(sp.row) * rank) * V;
+#pragma unroll 1
+        for (int r0 = 0; r0 < rank; r0 += 16) {
+            float f[4][8], z[4][CT];
+            const uint32_t fe = 4 * (min(r0 + j, rank - 1) * kK + 8 * kk);
+#pragma unroll
+            for (int b = 0; b < 4; ++b) {
+                const f32x4 f0 = load_at<f32x4>(F, fe + 128 * b), f1 = load_at<f32x4>(F, fe + 128 * b + 16);
+#pragma unroll
+                for (int t = 0; t < 8; ++t) f[b][t] = t < 4 ? f0[t & 3] : f1[t & 3];
+            }
+#pragma unroll
+            for (int s = 0; s < 4; ++s) Co::load(Z, min(r0 + 4 * s + kk, rank - 1) * V, j, z[s]);
+#pragma unroll
+            for (int m = 0; m < MT; ++m) {
+                if (16 * m >= sp.len) continue;
+                __builtin_amdgcn_sched_barrier(0);
+                f32x4 c = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+                for (int b = 0; b < 4; ++b) {
+                    c = multiply(q_at(m, 32 * b), f[b], c);
+                    __builtin_amdgcn_sched_barrier(0);
+                }
+                wave_lds();
+#pragma unroll
+                for (int i = 0; i < 4; ++i) Y.c[(4 * kk + i) * CS + j] = c[i];
+                wave_lds();
+#pragma unroll
+                for (int s = 0; s < 4; ++s) {
+                    if (r0 + 4 * s >= rank) continue;
+                    const bool on = r0 + 4 * s + kk < rank;
+                    const float y = on ? Y.c[j * CS + 4 * s + kk] : 0.f;
+#pragma unroll
+                    for (int t = 0; t < CT; ++t) d[m][t] = mfma_16x16x4(y, on ? z[s][t] : 0.f, d[m][t]);
+                }
+            }
+        }
+    }
+
+    // ---- decays behind each window slot, and of the whole window ------------------------
+    wave_lds();
+    float all = 1.f;
+    for (int i = sp.p - 1; i >= 0; --i) {
+        if (lane == 0) Y.ws[i] = all;
+        all *= Y.a[i];
+    }
+
+#pragma unroll
+    for (int m = 0; m < MT; ++m) {
+        const int n0 = 16 * m, left = sp.len - n0;
+        if (left <= 0) break;
+        wave_lds();
+        // ---- decays between a tile's nodes and their ancestors ----------------------------
+        if (lane < 16) {
+            const int n = n0 + min(lane, left - 1);
+            float g = 1.f;
+            uint2 path = make_uint2(0u, 0u);
+            int row = 16 + n;
+            while (row >= 0) {
+                Y.p[lane * LP + row] = g;
+                const uint32_t bit = 1u << (row - 16 & 31);
+                path.x |= row < 48 ? bit : 0u;
+                path.y |= row < 48 ? 0u : bit;
+                g *= Y.a[row];
+                row = Y.up[row];
+            }
+            Y.gs[lane] = g;
+            Y.path[lane] = row == -1 ? path : make_uint2(0u, 0u);
+        }
+        wave_lds();
+        float gr[4];
+        uint2 pa[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            gr[i] = Y.gs[4 * kk + i];
+            pa[i] = Y.path[4 * kk + i];
+            const float g = all * gr[i];
+#pragma unroll
+            for (int c = 0; c < CT; ++c) d[m][c][i] *= g;
+        }
+        // ---- P: products q k, each with the decays between its tokens -----------------------
+        Raw qf[4];
+#pragma unroll
+        for (int c = 0; c < 4; ++c) qf[c] = q_at(m, 32 * c);
+        bool odd = false;
+#pragma unroll
+        for (int u = 0; u <= m + 1; ++u) {
+            if (u == 0 && !held) continue;
+            __builtin_amdgcn_sched_barrier(0);
+            const int rows = u ? min(16, sp.len - 16 * (u - 1)) : sp.p;
+            const uint32_t ke = ((u ? min(16 * (u - 1) + j, sp.len - 1) * kstep : min(j, sp.p - 1) * kslot) * kK + 8 * kk) * E;
+            Raw kf[4];
+#pragma unroll
+            for (int c = 0; c < 4; ++c) kf[c] = load_at<Raw>(u ? k_n : k_w, ke + 32 * E * c);
+            float v[4][CT];
+#pragma unroll
+            for (int s = 0; s < 4; ++s) {
+                const int r = min(4 * s + kk, rows - 1);
+                if (u) Co::load(v_n, (16 * (u - 1) + r) * (step * V), j, v[s]);
+                else Co::load(v_w, r * (slot * V), j, v[s]);
+            }
+            f32x4 g = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+            for (int c = 0; c < 4; ++c) {
+                if constexpr (BF) {
+                    g = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, qf[c].w),
+                                                                __builtin_bit_cast(bf16x8, kf[c].w), g, 0, 0, 0);
+                } else {
+                    float k[8];
+                    Vec8<QT>::unpack(kf[c], k);
+                    g = multiply(qf[c], k, g);
+                }
+            }
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                float& p = Y.p[(4 * kk + i) * LP + 16 * u + j];
+                if (u == 0) {
+                    const float f = gr[i] * Y.ws[j] * g[i];
+                    p = j < sp.p ? f : 0.f;
+                } else {
+                    const int r = 16 * (u - 1) + j;
+                    const float f = p * g[i];
+                    p = (r < 32 ? pa[i].x : pa[i].y) >> (r & 31) & 1u ? f : 0.f;
+                }
+            }
+            wave_lds();
+            // ---- times the values; one that is no number must not meet the zeros of other
+            // nodes' rows: it is left out here and joins the nodes below it afterwards
+#pragma unroll
+            for (int s = 0; s < 4; ++s) {
+                if (4 * s >= rows) continue;
+                const bool on = 4 * s + kk < rows;
+                const float pv = Y.p[j * LP + 16 * u + 4 * s + kk];
+#pragma unroll
+                for (int c = 0; c < CT; ++c) {
+                    const bool fin = isfinite(v[s][c]);
+                    odd = odd || !fin;
+                    d[m][c] = mfma_16x16x4(pv, on && fin ? v[s][c] : 0.f, d[m][c]);
+                }
+            }
+        }
+        const bool fix = __any(odd);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const int rn = 4 * kk + i, n = n0 + rn;
+            if (rn >= left || !(pa[i].x | pa[i].y)) continue;
+            float y[CT];
+#pragma unroll
+            for (int c = 0; c < CT; ++c) y[c] = d[m][c][i];
+            if (fix) {
+                auto join = [&](int row) {
+                    float f[CT];
+                    if (row < 16) Co::load(v_w, row * (slot * V), j, f);
+                    else Co::load(v_n, (row - 16) * (step * V), j, f);
+#pragma unroll
+                    for (int c = 0; c < CT; ++c)
+                        if (!isfinite(f[c])) y[c] = fmaf(Y.p[rn * LP + row], f[c], y[c]);
+                };
+                for (int row = 16 + n; row >= 0; row = Y.up[row]) join(row);
+                for (int row = 0; row < sp.p; ++row) join(row);
+            }
+            Co::store(A.y + (node + size_t(n) * A.H) * V, j, y);
+        }
+    }
+}
+
 // The path to each sequence's accepted node, its tokens to the row's next window
 // slots.  A block takes one sequence and some heads; the last block writes the new
 // positions.
@@ -732,11 +1102,25 @@ hipError_t launch_tree_m(const TreeArgs& a, const HeadTable& t, hipStream_t s) {
     return hipGetLastError();
 }
 
+template <int V, typename QT, int MT>
+hipError_t launch_scan_m(const TreeArgs& a, const HeadTable& t, hipStream_t s) {
+    const double blocks = (double(a.n_seqs) * a.H + 3) / 4;
+    if (!launch_fits(blocks, 256)) return hipErrorInvalidConfiguration;
+    hipLaunchKernelGGL((tree_scan_kernel<V, QT, MT>), dim3(uint32_t(blocks)), dim3(256), 0, s, a, t);
+    return hipGetLastError();
+}
+
 template <int KIND, int V, typename QT>
 hipError_t launch_tree_t(const TreeArgs& a, const HeadTable& t, hipStream_t s) {
+    if constexpr (KIND == SKSSM_MAMBA2) {
+        if (a.max_nodes <= 16) return launch_scan_m<V, QT, 1>(a, t, s);
+        if (a.max_nodes <= 32) return launch_scan_m<V, QT, 2>(a, t, s);
+        return launch_scan_m<V, QT, 4>(a, t, s);
+    } else {
     if (a.max_nodes <= 16) return launch_tree_m<KIND, V, QT, 1>(a, t, s);
     if (a.max_nodes <= 32) return launch_tree_m<KIND, V, QT, 2>(a, t, s);
     return launch_tree_m<KIND, V, QT, 4>(a, t, s);
+    }
 }
 
 template <int KIND, typename QT>
@@ -817,8 +1201,9 @@ extern "C" sketchssm_status sketchssm_tree_read(const sketchssm_plan* plan, cons
     A.per_share = (65536 + share - 1) / share;
     A.n_dense = plan->n_dense;
     hipStream_t s = static_cast<hipStream_t>(stream);
-    const hipError_t e = sh.qkv == SKSSM_BF16 ? launch_tree<Bf16Tag>(sh.kind, sh.V, A, plan->table, s)
-                                              : launch_tree<F32Tag>(sh.kind, sh.V, A, plan->table, s);
+    const HeadTable& table = sh.kind == SKSSM_MAMBA2 ? plan->by_head : plan->table;
+    const hipError_t e = sh.qkv == SKSSM_BF16 ? launch_tree<Bf16Tag>(sh.kind, sh.V, A, table, s)
+                                              : launch_tree<F32Tag>(sh.kind, sh.V, A, table, s);
     if (e == hipErrorInvalidConfiguration) return SKSSM_ESHAPE;  // more threads than a launch takes
     return e == hipSuccess ? SKSSM_OK : SKSSM_ELAUNCH;
 }
