@@ -151,6 +151,7 @@ class Plan:
         self.handle = h.value
         self.rank = r.copy()
         self.group = g.copy()
+        self._elems = int(lib().sketchssm_z_elems(self.handle)), int(lib().sketchssm_frame_elems(self.handle))
 
     def __del__(self):
         h = getattr(self, "handle", None)
@@ -160,11 +161,11 @@ class Plan:
 
     @property
     def z_elems(self) -> int:
-        return int(lib().sketchssm_z_elems(self.handle))
+        return self._elems[0]
 
     @property
     def frame_elems(self) -> int:
-        return int(lib().sketchssm_frame_elems(self.handle))
+        return self._elems[1]
 
     def export(self) -> dict:
         H = self.shape.H

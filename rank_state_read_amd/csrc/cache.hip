@@ -69,82 +69,114 @@ __device__ __forceinline__ int code_i8(float x, float s, float inv) {
 
 }  // namespace
 
+// A team of 16 lanes takes kRows key rows: lane l has values 4 l .. 4 l + 3 and, where the row
+// is longer, 64 + 4 l .. 64 + 4 l + 3, so that a row's load and store cover whole lines.
+constexpr int kRows = 4;
+
 template <int V, int FMT>
 __global__ __launch_bounds__(256) void cache_store_kernel(CacheArgs A) {
     const int l = threadIdx.x & 15;
-    const uint32_t kr = blockIdx.x * 16 + (threadIdx.x >> 4);  // key row of the call
+    const uint32_t first = (blockIdx.x * 16 + (threadIdx.x >> 4)) * kRows;  // key row of the call
     const uint32_t per = uint32_t(A.H) * kK;
-    const uint32_t i = kr / per;
+    const uint32_t i = first / per;
     if (i >= uint32_t(A.n)) return;
     const int row = A.rows ? A.rows[i] : int(i), slot = A.slots ? A.slots[i] : int(i);
     if (row < 0 || row >= A.B || slot < 0 || slot >= A.n_slots) return;
-    const uint32_t hk = kr - i * per;
-    const bool on = l < V / 8;
-    float x[8];
-    load8f(A.S + (size_t(row) * per + hk) * V + (on ? 8 * l : 0), x);
-    uint32_t top = 0;
+    const uint32_t hk = first - i * per;
+    const bool more = 64 + 4 * l < V;
+    const float* S = A.S + (size_t(row) * per + hk) * V + 4 * l;
+    float4 x[kRows][2];
 #pragma unroll
-    for (int e = 0; e < 8; ++e) top = max(top, __float_as_uint(x[e]) & 0x7fffffffu);
-    top = row_max16(top);
-    const bool finite = top < 0x7f800000u;
-    const uint32_t sb = finite ? scale_bits<FMT>(__uint_as_float(top)) : 0x7fc00000u;
+    for (int r = 0; r < kRows; ++r) {
+        x[r][0] = ldnt_f4(S + r * V);
+        x[r][1] = make_float4(0.f, 0.f, 0.f, 0.f);
+    }
+    if (more)
+#pragma unroll
+        for (int r = 0; r < kRows; ++r) x[r][1] = ldnt_f4(S + r * V + 64);
     const size_t at = size_t(slot) * per + hk;
-    if (l == 0) A.scales[at] = uint16_t(sb >> 16);
-    const float s = __uint_as_float(sb), inv = 1.f / s;
-    uint32_t c[2] = {0u, 0u};
-    if (finite) {
+    uint8_t* codes = static_cast<uint8_t*>(A.codes) + at * V + 4 * l;
+#pragma unroll
+    for (int r = 0; r < kRows; ++r) {
+        const float f[8] = {x[r][0].x, x[r][0].y, x[r][0].z, x[r][0].w, x[r][1].x, x[r][1].y, x[r][1].z, x[r][1].w};
+        uint32_t top = 0;
+#pragma unroll
+        for (int e = 0; e < 8; ++e) top = max(top, __float_as_uint(f[e]) & 0x7fffffffu);
+        top = row_max16(top);
+        const bool finite = top < 0x7f800000u;
+        const uint32_t sb = finite ? scale_bits<FMT>(__uint_as_float(top)) : 0x7fc00000u;
+        if (l == r) A.scales[at + r] = uint16_t(sb >> 16);
+        const float s = __uint_as_float(sb), inv = 1.f / s;
+        uint32_t c[2] = {0u, 0u};
         if constexpr (FMT == SKSSM_CACHE_I8) {
 #pragma unroll
-            for (int e = 0; e < 8; ++e) c[e / 4] |= (uint32_t(code_i8(x[e], s, inv)) & 0xffu) << (8 * (e % 4));
+            for (int e = 0; e < 8; ++e) c[e / 4] |= (uint32_t(code_i8(f[e], s, inv)) & 0xffu) << (8 * (e % 4));
         } else {
 #pragma unroll
             for (int e = 0; e < 2; ++e) {
-                int u = __builtin_amdgcn_cvt_pk_fp8_f32(x[4 * e] * inv, x[4 * e + 1] * inv, 0, false);
-                c[e] = uint32_t(__builtin_amdgcn_cvt_pk_fp8_f32(x[4 * e + 2] * inv, x[4 * e + 3] * inv, u, true));
+                const int u = __builtin_amdgcn_cvt_pk_fp8_f32(f[4 * e] * inv, f[4 * e + 1] * inv, 0, false);
+                c[e] = uint32_t(__builtin_amdgcn_cvt_pk_fp8_f32(f[4 * e + 2] * inv, f[4 * e + 3] * inv, u, true));
             }
         }
+        *reinterpret_cast<uint32_t*>(codes + r * V) = finite ? c[0] : 0u;
+        if (more) *reinterpret_cast<uint32_t*>(codes + r * V + 64) = finite ? c[1] : 0u;
     }
-    if (on) *reinterpret_cast<uint2*>(static_cast<uint8_t*>(A.codes) + at * V + 8 * l) = make_uint2(c[0], c[1]);
+}
+
+template <int FMT>
+__device__ __forceinline__ f32x4 values_of(uint32_t c, float s) {
+    f32x4 x;
+    if constexpr (FMT == SKSSM_CACHE_I8) {
+#pragma unroll
+        for (int e = 0; e < 4; ++e) x[e] = float(int8_t(c >> (8 * e)));
+    } else {
+        const auto lo = __builtin_amdgcn_cvt_pk_f32_fp8(int(c), false);
+        const auto hi = __builtin_amdgcn_cvt_pk_f32_fp8(int(c), true);
+        x = f32x4{lo[0], lo[1], hi[0], hi[1]};
+    }
+#pragma unroll
+    for (int e = 0; e < 4; ++e) x[e] *= s;
+    return x;
 }
 
 template <int V, int FMT>
 __global__ __launch_bounds__(256) void cache_load_kernel(CacheArgs A) {
     const int l = threadIdx.x & 15;
-    const uint32_t kr = blockIdx.x * 16 + (threadIdx.x >> 4);
+    const uint32_t first = (blockIdx.x * 16 + (threadIdx.x >> 4)) * kRows;
     const uint32_t per = uint32_t(A.H) * kK;
-    const uint32_t i = kr / per;
-    if (i >= uint32_t(A.n) || l >= V / 8) return;
+    const uint32_t i = first / per;
+    if (i >= uint32_t(A.n)) return;
     const int row = A.rows ? A.rows[i] : int(i), slot = A.slots ? A.slots[i] : int(i);
     if (row < 0 || row >= A.B || slot >= A.n_slots) return;
-    const uint32_t hk = kr - i * per;
-    float x[8];
-    if (slot < 0) {
+    const uint32_t hk = first - i * per;
+    const bool more = 64 + 4 * l < V;
+    f32x4 x[kRows][2];
 #pragma unroll
-        for (int e = 0; e < 8; ++e) x[e] = 0.f;
-    } else {
+    for (int r = 0; r < kRows; ++r) x[r][0] = x[r][1] = f32x4{0.f, 0.f, 0.f, 0.f};
+    if (slot >= 0) {
         const size_t at = size_t(slot) * per + hk;
-        const float s = __uint_as_float(uint32_t(A.scales[at]) << 16);
-        const uint2 c = *reinterpret_cast<const uint2*>(static_cast<const uint8_t*>(A.codes) + at * V + 8 * l);
-        const uint32_t cc[2] = {c.x, c.y};
+        const uint8_t* codes = static_cast<const uint8_t*>(A.codes) + at * V + 4 * l;
+        const uint2 sc = *reinterpret_cast<const uint2*>(A.scales + at);  // four of them
+        uint32_t c[kRows][2];
 #pragma unroll
-        for (int e = 0; e < 8; ++e) {
-            if constexpr (FMT == SKSSM_CACHE_I8) x[e] = float(int8_t(cc[e / 4] >> (8 * (e % 4))));
-        }
-        if constexpr (FMT == SKSSM_CACHE_E4M3) {
-#pragma unroll
-            for (int e = 0; e < 2; ++e) {
-                const auto lo = __builtin_amdgcn_cvt_pk_f32_fp8(int(cc[e]), false);
-                const auto hi = __builtin_amdgcn_cvt_pk_f32_fp8(int(cc[e]), true);
-                x[4 * e] = lo[0];
-                x[4 * e + 1] = lo[1];
-                x[4 * e + 2] = hi[0];
-                x[4 * e + 3] = hi[1];
-            }
+        for (int r = 0; r < kRows; ++r) {
+            c[r][0] = *reinterpret_cast<const uint32_t*>(codes + r * V);
+            c[r][1] = more ? *reinterpret_cast<const uint32_t*>(codes + r * V + 64) : 0u;
         }
 #pragma unroll
-        for (int e = 0; e < 8; ++e) x[e] *= s;
+        for (int r = 0; r < kRows; ++r) {
+            const uint32_t b = r < 2 ? sc.x : sc.y;
+            const float s = __uint_as_float(r % 2 ? b & 0xffff0000u : b << 16);
+            x[r][0] = values_of<FMT>(c[r][0], s);
+            x[r][1] = values_of<FMT>(c[r][1], s);
+        }
     }
-    store8f(A.out + (size_t(row) * per + hk) * V + 8 * l, x);
+    float* S = A.out + (size_t(row) * per + hk) * V + 4 * l;
+#pragma unroll
+    for (int r = 0; r < kRows; ++r) __builtin_nontemporal_store(x[r][0], reinterpret_cast<f32x4*>(S + r * V));
+    if (more)
+#pragma unroll
+        for (int r = 0; r < kRows; ++r) __builtin_nontemporal_store(x[r][1], reinterpret_cast<f32x4*>(S + r * V + 64));
 }
 
 namespace {
@@ -176,8 +208,8 @@ sketchssm_status cache_call(bool store, const sketchssm_shape* shape, const Cach
         if (ptr && !aligned16(ptr)) return SKSSM_EALIGN;
     A.B = shape->B;
     A.H = shape->H;
-    // key rows of a call are counted in 32 bits
-    const double blocks = double(A.n) * A.H * (kK / 16);
+    // a call's key rows, kRows of them to 16 lanes, are counted in 32 bits
+    const double blocks = (double(A.n) * A.H * (kK / kRows) + 15) / 16;
     if (!launch_fits(blocks, 256)) return SKSSM_ESHAPE;
     if (A.n == 0) return SKSSM_OK;
     hipStream_t s = static_cast<hipStream_t>(stream);

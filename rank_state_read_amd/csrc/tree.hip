@@ -38,7 +38,7 @@ struct TreeArgs {
     int B, n_seqs, total, max_nodes;
     int H, Hk;
     uint32_t per_share;  // 2^16 / (heads of a key head), rounded up: h / share is h per_share >> 16 below 256
-    int n_dense;  // dense heads lead the head table
+    bool sketch;  // whether any head has one
 };
 
 // A sequence of the call; what the lists hold is checked here.
@@ -69,6 +69,10 @@ struct __align__(16) RowInfo {
     int pad;
 };
 
+// The delta rule's blocks: four waves, two by two, wave (wk, wc) with keys 64 wk .. 64 wk + 63
+// and half wc of the columns.
+constexpr int kTreeThreads = 256;
+
 // A load at a per-lane 32-bit byte offset from a base that all lanes share.
 template <typename T>
 __device__ __forceinline__ T load_at(const void* base, uint32_t off) {
@@ -78,10 +82,10 @@ __device__ __forceinline__ T load_at(const void* base, uint32_t off) {
 // A block's rows of CH 16-byte chunks, through registers to LDS.  All loads are made,
 // without a branch to wait behind: rows behind the window's or the tree's last one
 // repeat it, and nothing points to them.
-template <int CH, int MT, int NTH>
+template <int CH, int MT>
 struct RowRegs {
-    static constexpr int PER = NTH / CH;  // rows per load of the block
-    static constexpr int W = 16 / PER > 0 ? 16 / PER : 1, N = (16 * (1 + MT) + PER - 1) / PER;
+    static constexpr int PER = kTreeThreads / CH;  // rows per load of the block
+    static constexpr int W = 16 / PER, N = W * (1 + MT);
     u32x4 r[N];
 
     __device__ __forceinline__ void load(const void* node, uint32_t nstep, int len, const void* win, uint32_t wstep,
@@ -90,22 +94,15 @@ struct RowRegs {
         const uint32_t c = 16 * (threadIdx.x % CH);
 #pragma unroll
         for (int i = 0; i < N; ++i) {
-            if constexpr (PER <= 16) {
-                if (i < W) r[i] = load_at<u32x4>(win, max(min(i * PER + row, p - 1), 0) * wstep + c);
-                else r[i] = load_at<u32x4>(node, min(i * PER - 16 + row, len - 1) * nstep + c);
-            } else {  // the first load's threads take both
-                const int at = i * PER + row;
-                const bool w = i == 0 && row < 16;
-                r[i] = load_at<u32x4>(w ? win : node,
-                                      (w ? max(min(at, p - 1), 0) * wstep : min(at - 16, len - 1) * nstep) + c);
-            }
+            if (i < W) r[i] = load_at<u32x4>(win, max(min(i * PER + row, p - 1), 0) * wstep + c);
+            else r[i] = load_at<u32x4>(node, min(i * PER - 16 + row, len - 1) * nstep + c);
         }
     }
     __device__ __forceinline__ void store(char* lds, int rows) const {
 #pragma unroll
         for (int i = 0; i < N; ++i)
             if (int(i * PER + threadIdx.x / CH) < rows)
-                *reinterpret_cast<u32x4*>(lds + (i * NTH + threadIdx.x) * 16) = r[i];
+                *reinterpret_cast<u32x4*>(lds + (i * kTreeThreads + threadIdx.x) * 16) = r[i];
     }
 };
 
@@ -209,14 +206,10 @@ struct ValueCols<V, Bf16Tag> {
     __device__ __forceinline__ void drop(int c) { u[c / 2] &= c % 2 ? 0xffffu : 0xffff0000u; }
 };
 
-// Four waves a block, two by two: wave (wk, wc) has keys 64 wk .. 64 wk + 63 and half wc of
-// the columns.
-constexpr int kTreeThreads = 256;
-
 // LDS of a block, by the call's largest tree.
 template <int KIND, int V, typename QT>
 struct TreeLds {
-    static constexpr bool DELTA = KIND != SKSSM_MAMBA2, KDA = KIND == SKSSM_KDA;
+    static constexpr bool KDA = KIND == SKSSM_KDA;
     static constexpr int XS = kK + 4;  // row of x
     static constexpr int CS = 20;      // row of a sketch's coefficients
     static constexpr int kKey = kK * Vec8<QT>::kElemBytes;
@@ -224,25 +217,20 @@ struct TreeLds {
     static constexpr int kRed = 2 * 2 * Cols<V>::C * 64 * 8;
     int rows;  // window slots and nodes, a multiple of 4
     int lp;    // row of P, 4 apart in the banks from the next one
-    int gp;    // row of a Mamba-2 tree's decays
-    int keys, dec, x, red, cs, p, g, info, node, win, anc, flag, bytes;
+    int keys, dec, x, red, cs, p, info, good, flag, bytes;
 
     __host__ __device__ __forceinline__ TreeLds(int max_nodes, bool sketch) {
         rows = 16 + (max_nodes + 3) / 4 * 4;
         lp = 16 + (max_nodes + 15) / 16 * 16 + 4;
-        gp = rows - 16 + 1;
         keys = 0;
-        dec = keys + (DELTA ? (rows + 1) * kKey : 0);
+        dec = keys + (rows + 1) * kKey;
         x = dec + (KDA ? (rows + 1) * kK * 4 : 0);
-        red = x + (DELTA && !KDA ? 16 * XS * 4 : 0);  // KDA: the sums take x's place
+        red = x + (KDA ? 0 : 16 * XS * 4);  // KDA: the sums take x's place
         cs = red + (KDA && 16 * XS * 4 > kRed ? 16 * XS * 4 : kRed);
         p = cs + (sketch ? kCoef : 0);
-        g = p + (16 * lp + 4) * 4;
-        info = g + (DELTA ? 0 : (rows - 16) * gp * 4 + 15) / 16 * 16;
-        node = info + (rows + 2) * int(sizeof(RowInfo));  // Mamba-2: a node's product of decays to the tree's root
-        win = node + (rows - 16) * 4;                     // and from each window slot to its end
-        anc = (win + 16 * 4 + 15) / 16 * 16;
-        flag = anc + (rows - 16) * 8;
+        info = p + (16 * lp + 4) * 4;
+        good = info + (rows + 2) * int(sizeof(RowInfo));
+        flag = good + (rows - 16) * 4;
         bytes = flag + 16;
     }
 };
@@ -253,28 +241,23 @@ struct TreeLds {
 // registers from tile to tile.
 template <int KIND, int V, typename QT, int MT>
 __global__ __launch_bounds__(kTreeThreads) __attribute__((amdgpu_waves_per_eu(3)))
-void tree_kernel(TreeArgs A, HeadTable T, int sketch_lds) {
+void tree_kernel(TreeArgs A, HeadTable T) {
     typedef TreeLds<KIND, V, QT> Lds;
     typedef Cols<V> Co;
     typedef typename Vec8<QT>::raw_t Raw;
-    constexpr bool DELTA = Lds::DELTA, KDA = Lds::KDA;
-    constexpr int C = Co::C, E = Vec8<QT>::kElemBytes, XS = Lds::XS, CS = Lds::CS, NTH = kTreeThreads;
+    constexpr bool KDA = Lds::KDA;
+    constexpr int C = Co::C, E = Vec8<QT>::kElemBytes, XS = Lds::XS, CS = Lds::CS;
     extern __shared__ __align__(16) char lds[];
-    const Lds Y(A.max_nodes, sketch_lds);
+    const Lds Y(A.max_nodes, A.sketch);
     float* xs = reinterpret_cast<float*>(lds + Y.x);
     float* ps = reinterpret_cast<float*>(lds + Y.p);
     RowInfo* info = reinterpret_cast<RowInfo*>(lds + Y.info);
     int* flag = reinterpret_cast<int*>(lds + Y.flag);
-    float* gn = reinterpret_cast<float*>(lds + Y.g);     // Mamba-2: decays between a node and its ancestors
-    float* gs = reinterpret_cast<float*>(lds + Y.node);  // and between it and the root
-    float* ws = reinterpret_cast<float*>(lds + Y.win);   // behind each window slot
-    // a node's path, a bit per node in two words (a 64-bit shift by a lane's amount reads a
-    // wrong register where that amount sits in the last one of the wave); 0: none
-    uint2* anc = reinterpret_cast<uint2*>(lds + Y.anc);
+    int* good = reinterpret_cast<int*>(lds + Y.good);  // whether a node has a path
     const int LP = Y.lp;
 
-    const int seq = blockIdx.x / A.H, at = blockIdx.x % A.H;
-    const int h = T.head[at], rank = T.rank[at], hk = int(uint32_t(h) * A.per_share >> 16);
+    const int seq = blockIdx.x / A.H, h = blockIdx.x % A.H;
+    const int rank = T.rank[h], hk = int(uint32_t(h) * A.per_share >> 16);
     const TreeSpan sp = tree_span(A, seq);
     if (!sp.live) return;
     const int tid = threadIdx.x, lane = tid & 63, w = __builtin_amdgcn_readfirstlane(tid >> 6);
@@ -307,13 +290,11 @@ void tree_kernel(TreeArgs A, HeadTable T, int sketch_lds) {
         const int par = load_at<int>(A.parents + sp.t0, 4 * in_n);
         const bool first16 = tid < 16 && held;
         if constexpr (!KDA) in.a = load_at<float>(first16 ? a_w : a_n, in_off);
-        if constexpr (DELTA) in.beta = load_at<float>(first16 ? A.bbuf + win : A.beta + node, in_off);
-        RowRegs<kK * E / 16, MT, NTH> kr;
-        RowRegs<kK * 4 / 16, MT, NTH> ar;
-        if constexpr (DELTA) {
-            kr.load(k_n, kstep * kK * E, sp.len, k_w, kslot * kK * E, sp.p);
-            if constexpr (KDA) ar.load(a_n, step * kK * 4, sp.len, a_w, slot * kK * 4, sp.p);
-        }
+        in.beta = load_at<float>(first16 ? A.bbuf + win : A.beta + node, in_off);
+        RowRegs<kK * E / 16, MT> kr;
+        RowRegs<kK * 4 / 16, MT> ar;
+        kr.load(k_n, kstep * kK * E, sp.len, k_w, kslot * kK * E, sp.p);
+        if constexpr (KDA) ar.load(a_n, step * kK * 4, sp.len, a_w, slot * kK * 4, sp.p);
         // the state is on its way while the first tile's queries are carried back
         if (rank == 0) {
             const __amdgpu_buffer_rsrc_t rs = buffer_rsrc(A.S + (size_t(sp.row) * A.H + h) * (kK * V), kK * V * 4);
@@ -331,40 +312,15 @@ void tree_kernel(TreeArgs A, HeadTable T, int sketch_lds) {
             info[tid] = in;
         }
         if (tid == 0) *flag = 0;
-        if constexpr (DELTA) {
-            kr.store(lds + Y.keys, Y.rows);
-            if (tid < Lds::kKey / 16)
-                *reinterpret_cast<u32x4*>(lds + Y.keys + Y.rows * Lds::kKey + 16 * tid) = u32x4{0u, 0u, 0u, 0u};
-            if constexpr (KDA) {
-                ar.store(lds + Y.dec, Y.rows);
-                if (tid < kK) reinterpret_cast<float*>(lds + Y.dec)[Y.rows * kK + tid] = 1.f;
-            }
+        kr.store(lds + Y.keys, Y.rows);
+        if (tid < Lds::kKey / 16)
+            *reinterpret_cast<u32x4*>(lds + Y.keys + Y.rows * Lds::kKey + 16 * tid) = u32x4{0u, 0u, 0u, 0u};
+        if constexpr (KDA) {
+            ar.store(lds + Y.dec, Y.rows);
+            if (tid < kK) reinterpret_cast<float*>(lds + Y.dec)[Y.rows * kK + tid] = 1.f;
         }
     }
     __syncthreads();
-    float all = 1.f;  // Mamba-2: the whole window's decays
-    if constexpr (!DELTA) {
-        if (tid < sp.len) {
-            float g = 1.f;
-            uint2 path = make_uint2(0u, 0u);
-            int row = 16 + tid;
-            while (row >= 16 && row < Y.rows) {
-                gn[tid * Y.gp + row - 16] = g;
-                const uint32_t bit = 1u << (row - 16 & 31);
-                path.x |= row < 48 ? bit : 0u;
-                path.y |= row < 48 ? 0u : bit;
-                g *= info[row].a;
-                row = info[row].up;
-            }
-            gs[tid] = g;
-            anc[tid] = row == Y.rows + 1 ? make_uint2(0u, 0u) : path;
-        }
-        for (int i = sp.p - 1; i >= 0; --i) {
-            if (tid == 64) ws[i] = all;
-            all *= info[i].a;
-        }
-        __syncthreads();
-    }
 
     const int j_lane = j, kk_lane = kk;
 #pragma unroll 1
@@ -375,8 +331,7 @@ void tree_kernel(TreeArgs A, HeadTable T, int sketch_lds) {
         // of another wave
         int j = j_lane, kk = kk_lane;
         if constexpr (MT > 1) asm volatile("" : "+v"(j), "+v"(kk));
-        Raw qx[2];  // Mamba-2: this wave's keys of node n0 + j's query
-        if constexpr (DELTA) {
+        {
             // ---- the walk: 16 lanes a node, a wave's four until the last one ends --------
             const int n = n0 + min(rrow, left - 1), end = Y.rows;
             float x[8], g = 1.f;
@@ -421,58 +376,12 @@ void tree_kernel(TreeArgs A, HeadTable T, int sketch_lds) {
                 read(s0, row);
                 take(s1, r1);
             }
-            if (l == 0 && rrow < left) anc[n] = make_uint2(row == end, 0u);
+            if (l == 0 && rrow < left) good[n] = row == end;
             if constexpr (!KDA) {
 #pragma unroll
                 for (int e = 0; e < 8; ++e) x[e] *= g;
             }
             store8f(xs + rrow * XS + 8 * l, x);
-        } else {
-            // ---- products q k, each with the decays between its tokens -------------------
-            const uint32_t qe = (uint32_t(n0 + min(j, left - 1)) * kstep * kK + 8 * kk) * E;
-            Raw qf[4];
-#pragma unroll
-            for (int c = 0; c < 4; ++c) qf[c] = load_at<Raw>(q_n, qe + 32 * E * c);
-            qx[0] = load_at<Raw>(q_n, qe + E * (rank ? 32 * w : 64 * wk));
-            qx[1] = load_at<Raw>(q_n, qe + E * (rank ? 32 * w : 64 * wk + 32));
-            for (int u = w; u <= m + 1; u += 4) {
-                if (u == 0 && !held) continue;
-                const uint32_t ke = ((u ? min(16 * (u - 1) + j, sp.len - 1) * kstep : min(j, sp.p - 1) * kslot) * kK +
-                                     8 * kk) * E;
-                Raw kf[4];
-#pragma unroll
-                for (int c = 0; c < 4; ++c) kf[c] = load_at<Raw>(u ? k_n : k_w, ke + 32 * E * c);
-                f32x4 d = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-                for (int c = 0; c < 4; ++c) {
-                    if constexpr (E == 2) {
-                        typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
-                        d = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, qf[c].w),
-                                                                    __builtin_bit_cast(bf16x8, kf[c].w), d, 0, 0, 0);
-                    } else {
-                        float x[8], k[8];
-                        Vec8<QT>::unpack(qf[c], x);
-                        Vec8<QT>::unpack(kf[c], k);
-#pragma unroll
-                        for (int e = 0; e < 8; ++e) d = mfma_16x16x4(x[e], k[e], d);
-                    }
-                }
-                const int r = 16 * (u - 1) + j;
-#pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    const int rn = 4 * kk + i, n = n0 + min(rn, left - 1);
-                    float f;
-                    if (u == 0) {
-                        f = gs[n] * ws[j] * d[i];
-                        f = j < sp.p ? f : 0.f;
-                    } else {
-                        const uint2 path = anc[n];
-                        f = gn[n * Y.gp + min(r, sp.len - 1)] * d[i];
-                        f = r < sp.len && ((r < 32 ? path.x : path.y) >> (r & 31) & 1u) ? f : 0.f;
-                    }
-                    ps[rn * LP + 16 * u + j] = f;
-                }
-            }
         }
         __syncthreads();
 
@@ -498,19 +407,17 @@ void tree_kernel(TreeArgs A, HeadTable T, int sketch_lds) {
 #pragma unroll
             for (int t8 = 0; t8 < 2; ++t8) {
                 float x[8];
-                if constexpr (DELTA) load8f(xs + j * XS + 64 * wk + 32 * t8 + 8 * kk, x);
-                else Vec8<QT>::unpack(qx[t8], x);
+                load8f(xs + j * XS + 64 * wk + 32 * t8 + 8 * kk, x);
 #pragma unroll
                 for (int t = 0; t < 8; ++t)
 #pragma unroll
                     for (int c = 0; c < C; ++c) d[c] = mfma_16x16x4(x[t], s[8 * t8 + t][c], d[c]);
             }
         } else {
-            const float* F = A.frames + size_t(T.frow[at]) * kK;
-            const float* Z = A.Z + (size_t(T.zrow[at]) * A.B + size_t(sp.row) * rank) * V;
+            const float* F = A.frames + size_t(T.frow[h]) * kK;
+            const float* Z = A.Z + (size_t(T.zrow[h]) * A.B + size_t(sp.row) * rank) * V;
             float x[8];  // node n0 + j, key elements 32 w + 8 kk ..
-            if constexpr (DELTA) load8f(xs + j * XS + 32 * w + 8 * kk, x);
-            else Vec8<QT>::unpack(qx[0], x);
+            load8f(xs + j * XS + 32 * w + 8 * kk, x);
             float* cs = reinterpret_cast<float*>(lds + Y.cs);
 #pragma unroll 1
             for (int r0 = 0; r0 < rank; r0 += 16) {
@@ -543,14 +450,6 @@ void tree_kernel(TreeArgs A, HeadTable T, int sketch_lds) {
         // ---- the path's values ---------------------------------------------------------
         // a value that is no number must not meet the zeros of other nodes' rows: it is
         // left out of the products and joins the nodes below it at the end
-        if constexpr (!DELTA) {  // what the state gave decays over the whole path
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                const float g = all * gs[n0 + min(4 * kk + i, left - 1)];
-#pragma unroll
-                for (int c = 0; c < C; ++c) d[c][i] *= g;
-            }
-        }
         bool odd = false;
 #pragma unroll
         for (int u = 0; u <= MT; ++u) {
@@ -591,7 +490,7 @@ void tree_kernel(TreeArgs A, HeadTable T, int sketch_lds) {
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
             const int rn = 4 * kk + 2 * wk + i, n = n0 + rn;
-            if (rn < left && (anc[n].x | anc[n].y)) {
+            if (rn < left && good[n]) {
                 if (fix) {
                     for (int row = 16 + n; row < Y.rows; row = info[row].up) {
                         ValueCols<V, QT> f;
@@ -1089,16 +988,14 @@ namespace {
 
 template <int KIND, int V, typename QT, int MT>
 hipError_t launch_tree_m(const TreeArgs& a, const HeadTable& t, hipStream_t s) {
-    const bool sketch = a.n_dense < a.H;
-    const int bytes = TreeLds<KIND, V, QT>(a.max_nodes, sketch).bytes;
+    const int bytes = TreeLds<KIND, V, QT>(a.max_nodes, a.sketch).bytes;
     if (!launch_fits(double(a.n_seqs) * a.H, kTreeThreads)) return hipErrorInvalidConfiguration;
     if (bytes > 65536) {
         const hipError_t e = hipFuncSetAttribute(reinterpret_cast<const void*>(tree_kernel<KIND, V, QT, MT>),
                                                  hipFuncAttributeMaxDynamicSharedMemorySize, bytes);
         if (e != hipSuccess) return e;
     }
-    hipLaunchKernelGGL((tree_kernel<KIND, V, QT, MT>), dim3(a.n_seqs * a.H), dim3(kTreeThreads), bytes, s, a, t,
-                       int(sketch));
+    hipLaunchKernelGGL((tree_kernel<KIND, V, QT, MT>), dim3(a.n_seqs * a.H), dim3(kTreeThreads), bytes, s, a, t);
     return hipGetLastError();
 }
 
@@ -1199,11 +1096,10 @@ extern "C" sketchssm_status sketchssm_tree_read(const sketchssm_plan* plan, cons
     A.Hk = kq_heads_of(sh);
     const uint32_t share = uint32_t(sh.H / A.Hk);
     A.per_share = (65536 + share - 1) / share;
-    A.n_dense = plan->n_dense;
+    A.sketch = plan->n_dense < sh.H;
     hipStream_t s = static_cast<hipStream_t>(stream);
-    const HeadTable& table = sh.kind == SKSSM_MAMBA2 ? plan->by_head : plan->table;
-    const hipError_t e = sh.qkv == SKSSM_BF16 ? launch_tree<Bf16Tag>(sh.kind, sh.V, A, table, s)
-                                              : launch_tree<F32Tag>(sh.kind, sh.V, A, table, s);
+    const hipError_t e = sh.qkv == SKSSM_BF16 ? launch_tree<Bf16Tag>(sh.kind, sh.V, A, plan->by_head, s)
+                                              : launch_tree<F32Tag>(sh.kind, sh.V, A, plan->by_head, s);
     if (e == hipErrorInvalidConfiguration) return SKSSM_ESHAPE;  // more threads than a launch takes
     return e == hipSuccess ? SKSSM_OK : SKSSM_ELAUNCH;
 }
