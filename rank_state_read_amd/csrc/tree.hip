@@ -879,8 +879,8 @@ void tree_scan_kernel(TreeArgs A, HeadTable T) {
 }
 
 // The path to each sequence's accepted node, its tokens to the row's next window
-// slots.  A block takes one sequence and some heads; the last block writes the new
-// positions.
+// slots.  A block takes one sequence and some heads; the first one, whose paths take longest,
+// writes the new positions.
 namespace {
 
 struct AcceptArgs {
@@ -903,84 +903,96 @@ struct AcceptArgs {
 };
 
 constexpr int kAcceptHeads = 8;
+constexpr int kStaged = 256;  // parents of a tree's first nodes, in LDS
 
-// The path of sequence i from its first token on, and its length; 0 where nothing
-// is accepted or anything is out of range.
-__device__ __forceinline__ int accept_path(const AcceptArgs& A, int i, int& row, int& t0, int (&path)[kW]) {
-    const int t1 = A.offsets[i + 1];
-    t0 = A.offsets[i];
-    row = A.rows ? A.rows[i] : i;
-    if (!(t0 >= 0 && t1 > t0 && t1 <= A.total && row >= 0 && row < A.B)) return 0;
-    const int p = A.pos[row];
-    int m = A.accepted[i];
-    if (p < 0 || p > kW || m >= t1 - t0) return 0;
+// The path to accepted node m of a tree of len nodes, last node first, and its length; 0 where
+// nothing is accepted, anything is out of range or the window has no room behind p tokens.
+template <typename Parent>
+__device__ __forceinline__ int accept_path(int m, int len, int p, Parent&& parent, int* path) {
+    if (p < 0 || p > kW || m >= len) return 0;
     int n = 0;
     while (m >= 0) {
         if (p + n >= kW) return 0;
-        path[n++] = m;
-        const int up = A.parents[t0 + m];
+        if (path) path[n] = m;
+        ++n;
+        const int up = parent(m);
         if (up >= m || up < -1) return 0;
         m = up;
     }
     return n;
 }
 
+struct AcceptSpan {
+    int row, t0, len;  // len 0: idle
+};
+
+__device__ __forceinline__ AcceptSpan accept_span(const AcceptArgs& A, int i) {
+    AcceptSpan s;
+    const int t1 = A.offsets[i + 1];
+    s.t0 = A.offsets[i];
+    s.row = A.rows ? A.rows[i] : i;
+    s.len = s.t0 >= 0 && t1 > s.t0 && t1 <= A.total && s.row >= 0 && s.row < A.B ? t1 - s.t0 : 0;
+    return s;
+}
+
 }  // namespace
 
+// Bound by latency: the path has to be known before its tokens can be read.  A tree's parents
+// come to LDS in one load, and a block's threads take all tokens of its heads at once.
 template <typename QT>
 __global__ __launch_bounds__(256) void tree_accept_kernel(AcceptArgs A, int groups) {
-    __shared__ int path[kW], info[3];
-    const int seq = blockIdx.x / groups, group = blockIdx.x % groups;
-    if (seq == A.n_seqs) {  // positions: every row's old one, then those that grew
-        for (int b = threadIdx.x; b < A.B; b += 256) A.new_pos[b] = A.pos[b];
+    __shared__ int path[kW], staged[kStaged], n_path;
+    const int tid = threadIdx.x;
+    if (blockIdx.x == 0) {  // positions: every row's old one, then those that grew
+        for (int b = tid; b < A.B; b += 256) A.new_pos[b] = A.pos[b];
         __syncthreads();
-        for (int i = threadIdx.x; i < A.n_seqs; i += 256) {
-            int pt[kW], row, t0;
-            const int n = accept_path(A, i, row, t0, pt);
-            if (n) A.new_pos[row] = A.pos[row] + n;
+        for (int i = tid; i < A.n_seqs; i += 256) {
+            const AcceptSpan sp = accept_span(A, i);
+            if (!sp.len) continue;
+            const int n = accept_path(A.accepted[i], sp.len, A.pos[sp.row],
+                                      [&](int m) { return A.parents[sp.t0 + m]; }, nullptr);
+            if (n) A.new_pos[sp.row] = A.pos[sp.row] + n;
         }
         return;
     }
-    if (threadIdx.x == 0) {
-        int pt[kW], row, t0;
-        const int n = accept_path(A, seq, row, t0, pt);
-        for (int i = 0; i < n; ++i) path[i] = pt[n - 1 - i];
-        info[0] = n;
-        info[1] = row;
-        info[2] = t0;
-    }
+    const int seq = (blockIdx.x - 1) / groups, group = (blockIdx.x - 1) % groups;
+    const AcceptSpan sp = accept_span(A, seq);
+    if (!sp.len) return;
+    const int row = sp.row, p = A.pos[row], last = A.accepted[seq];
+    if (tid < sp.len) staged[tid] = A.parents[sp.t0 + tid];
     __syncthreads();
-    const int n = info[0], row = info[1];
-    const int h0 = group * kAcceptHeads, nh = min(kAcceptHeads, A.H - h0);
+    if (tid == 0)
+        n_path = accept_path(last, sp.len, p, [&](int m) { return m < kStaged ? staged[m] : A.parents[sp.t0 + m]; }, path);
+    __syncthreads();
+    const int n = n_path;
     if (n == 0) return;
-    const int p = A.pos[row];
+    const int h0 = group * kAcceptHeads, nh = min(kAcceptHeads, A.H - h0);
+    const auto token = [&](int i) { return size_t(sp.t0) + path[n - 1 - i]; };  // the path's i-th from the root
     const int VC = A.V / 8, KC = kK / 8;
-    for (int i = 0; i < n; ++i) {
-        const size_t t = size_t(info[2]) + path[i];
-        const size_t slot = size_t(p + i);
-        for (int e = threadIdx.x; e < nh * VC; e += 256) {
-            const int h = h0 + e / VC, c = 8 * (e % VC);
-            Vec8<QT>::store(A.vbuf, ((slot * A.H + h) * A.B + row) * A.V + c,
-                            Vec8<QT>::load(A.v, (t * A.H + h) * A.V + c));
+    for (int e = tid; e < n * nh * VC; e += 256) {
+        const int i = e / (nh * VC), r = e - i * (nh * VC), h = h0 + r / VC, c = 8 * (r % VC);
+        Vec8<QT>::store(A.vbuf, ((size_t(p + i) * A.H + h) * A.B + row) * A.V + c,
+                        Vec8<QT>::load(A.v, (token(i) * A.H + h) * A.V + c));
+    }
+    for (int e = tid; e < n * nh * KC; e += 256) {
+        const int i = e / (nh * KC), r = e - i * (nh * KC), h = h0 + r / KC, c = 8 * (r % KC);
+        const size_t t = token(i), slot = size_t(p + i);
+        if (h % A.share == 0) {
+            const int hk = h / A.share;
+            Vec8<QT>::store(A.kbuf, ((slot * A.Hk + hk) * A.B + row) * kK + c,
+                            Vec8<QT>::load(A.k, (t * A.Hk + hk) * kK + c));
         }
-        for (int e = threadIdx.x; e < nh * KC; e += 256) {
-            const int h = h0 + e / KC, c = 8 * (e % KC);
-            if (h % A.share == 0) {
-                const int hk = h / A.share;
-                Vec8<QT>::store(A.kbuf, ((slot * A.Hk + hk) * A.B + row) * kK + c,
-                                Vec8<QT>::load(A.k, (t * A.Hk + hk) * kK + c));
-            }
-            if (A.kda) {
-                float f[8];
-                load8f(A.a + (t * A.H + h) * kK + c, f);
-                store8f(A.abuf + ((slot * A.H + h) * A.B + row) * kK + c, f);
-            }
+        if (A.kda) {
+            float f[8];
+            load8f(A.a + (t * A.H + h) * kK + c, f);
+            store8f(A.abuf + ((slot * A.H + h) * A.B + row) * kK + c, f);
         }
-        for (int e = threadIdx.x; e < nh; e += 256) {
-            const size_t to = (slot * A.H + h0 + e) * A.B + row, from = t * A.H + h0 + e;
-            if (!A.kda) A.abuf[to] = A.a[from];
-            if (A.bbuf) A.bbuf[to] = A.beta[from];
-        }
+    }
+    for (int e = tid; e < n * nh; e += 256) {
+        const int i = e / nh, h = h0 + e - i * nh;
+        const size_t to = (size_t(p + i) * A.H + h) * A.B + row, from = token(i) * A.H + h;
+        if (!A.kda) A.abuf[to] = A.a[from];
+        if (A.bbuf) A.bbuf[to] = A.beta[from];
     }
 }
 
@@ -1147,7 +1159,7 @@ extern "C" sketchssm_status sketchssm_tree_accept(const sketchssm_shape* shape, 
     A.V = shape->V;
     A.kda = shape->kind == SKSSM_KDA;
     hipStream_t s = static_cast<hipStream_t>(stream);
-    const dim3 grid(A.n_seqs * groups + 1);  // the last block: positions
+    const dim3 grid(A.n_seqs * groups + 1);  // the first block: positions
     if (shape->qkv == SKSSM_BF16) hipLaunchKernelGGL((tree_accept_kernel<Bf16Tag>), grid, dim3(256), 0, s, A, groups);
     else hipLaunchKernelGGL((tree_accept_kernel<F32Tag>), grid, dim3(256), 0, s, A, groups);
     return hipGetLastError() == hipSuccess ? SKSSM_OK : SKSSM_ELAUNCH;
