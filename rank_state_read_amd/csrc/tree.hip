@@ -591,35 +591,77 @@ struct AllCols {
     }
 };
 
+// The same columns of a row of bf16 values, as they are stored.
+template <int V>
+struct PackedCols {
+    static constexpr int CT = V / 16, R = CT - 4;
+    static constexpr bool kPairs = R % 2 == 0;
+    static constexpr int X = kPairs ? R / 2 : R;
+    uint32_t w[2], x[X > 0 ? X : 1];
+    __device__ __forceinline__ void load(const uint16_t* base, uint32_t e, int j) {
+        const uint2 c = load_at<uint2>(base, 2 * (e + 4 * j));
+        w[0] = c.x;
+        w[1] = c.y;
+        const uint32_t at = 2 * (e + 64 + R * j);
+        if constexpr (R == 4) {
+            const uint2 d = load_at<uint2>(base, at);
+            x[0] = d.x;
+            x[1] = d.y;
+        } else if constexpr (R == 2) {
+            x[0] = load_at<uint32_t>(base, at);
+        } else {
+#pragma unroll
+            for (int i = 0; i < R; ++i) x[i] = load_at<uint16_t>(base, at + 2 * i);
+        }
+    }
+    __device__ __forceinline__ void clear() {
+        w[0] = w[1] = 0u;
+#pragma unroll
+        for (int i = 0; i < X; ++i) x[i] = 0u;
+    }
+    // column tile c of two rows, the first one's in the lower half
+    __device__ static __forceinline__ uint32_t pair(const PackedCols& a, const PackedCols& b, int c) {
+        const bool tail = c >= 4;
+        const int i = tail ? (kPairs ? (c - 4) / 2 : c - 4) : c / 2;
+        const bool upper = tail && !kPairs ? false : c % 2 != 0;
+        return __builtin_amdgcn_perm(tail ? b.x[i] : b.w[i], tail ? a.x[i] : a.w[i], upper ? 0x07060302 : 0x05040100);
+    }
+};
+
 // LDS of one wave.
 template <int MT>
 struct ScanLds {
     static constexpr int ROWS = 16 + 16 * MT;
-    static constexpr int LP = ROWS + 4;  // row of P, 4 apart in the banks from the next one
-    static constexpr int CS = 20;        // row of a sketch's coefficients
-    float p[16 * LP];
+    static constexpr int CS = 20;  // row of a sketch's coefficients
+    // P of tile m: its 16 nodes by the window and the nodes of tiles 0 .. m; rows 4 apart in the banks
+    __host__ __device__ static constexpr int row_p(int m) { return 16 * m + 36; }
+    __host__ __device__ static constexpr int tile_p(int m) { return 128 * m * (m - 1) + 576 * m; }
+    float p[tile_p(MT)];
     float c[16 * CS];
     float a[ROWS];
     int up[ROWS];  // the row before on a path: -1 none, -2 no path
     float ws[16];  // decays behind each window slot
-    float gs[16];  // a node's decays to the tree's root
-    uint2 path[16];
+    float gs[16 * MT];  // a node's decays to the tree's root
+    uint2 path[16 * MT];
 };
 
 }  // namespace
 
+// Waves of a block: their LDS stays below 64 KB.
+__host__ __device__ constexpr int scan_waves(int MT) { return MT == 4 ? 2 : 4; }
+
 template <int V, typename QT, int MT>
-__global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(MT == 1 ? 4 : MT == 2 ? 3 : 2)))
+__global__ __launch_bounds__(64 * scan_waves(MT)) __attribute__((amdgpu_waves_per_eu(MT == 1 ? 4 : MT == 2 ? 3 : 2)))
 void tree_scan_kernel(TreeArgs A, HeadTable T) {
     typedef AllCols<V> Co;
     typedef typename Vec8<QT>::raw_t Raw;
     typedef typename std::conditional<std::is_same<QT, Bf16Tag>::value, uint16_t, float>::type Elem;
-    constexpr int CT = Co::CT, E = Vec8<QT>::kElemBytes, LP = ScanLds<MT>::LP, CS = ScanLds<MT>::CS;
+    constexpr int CT = Co::CT, E = Vec8<QT>::kElemBytes, CS = ScanLds<MT>::CS;
     constexpr bool BF = E == 2;
-    __shared__ __align__(16) ScanLds<MT> lds[4];
+    __shared__ __align__(16) ScanLds<MT> lds[scan_waves(MT)];
     const int tid = threadIdx.x, lane = tid & 63, w = __builtin_amdgcn_readfirstlane(tid >> 6);
     ScanLds<MT>& Y = lds[w];
-    const int item = blockIdx.x * 4 + w;
+    const int item = blockIdx.x * scan_waves(MT) + w;
     const int seq = item / A.H, h = item - seq * A.H;
     if (seq >= A.n_seqs) return;
     const TreeSpan sp = tree_span(A, seq);
@@ -636,6 +678,12 @@ void tree_scan_kernel(TreeArgs A, HeadTable T) {
     const Elem* v_n = static_cast<const Elem*>(A.v) + node * V;
     const Elem* v_w = held ? static_cast<const Elem*>(A.vbuf) + win * V : v_n;
 
+    Raw q0[4];  // the first tile's queries
+    if constexpr (MT == 1) {
+#pragma unroll
+        for (int c = 0; c < 4; ++c)
+            q0[c] = load_at<Raw>(q_n, (uint32_t(min(j, sp.len - 1)) * kstep * kK + 32 * c + 8 * kk) * E);
+    }
     // ---- rows: decays, and which one stands before --------------------------------------
 #pragma unroll
     for (int r0 = 0; r0 < 16 * (1 + MT); r0 += 64) {
@@ -649,6 +697,31 @@ void tree_scan_kernel(TreeArgs A, HeadTable T) {
             Y.a[r] = a;
             Y.up[r] = par >= n || par < -1 ? -2 : par < 0 ? -1 : 16 + par;
         }
+    }
+
+    // ---- decays behind each window slot and of the whole window; between a node, a lane
+    // each, and its ancestors ------------------------------------------------------------
+    wave_lds();
+    float all = 1.f;
+    for (int i = sp.p - 1; i >= 0; --i) {
+        if (lane == 0) Y.ws[i] = all;
+        all *= Y.a[i];
+    }
+    if (lane < 16 * MT) {
+        float* pr = Y.p + ScanLds<MT>::tile_p(lane >> 4) + j * ScanLds<MT>::row_p(lane >> 4);
+        float g = 1.f;
+        uint2 path = make_uint2(0u, 0u);
+        int row = lane < sp.len ? 16 + lane : -2;
+        while (row >= 0) {
+            pr[row] = g;
+            const uint32_t bit = 1u << (row - 16 & 31);
+            path.x |= row < 48 ? bit : 0u;
+            path.y |= row < 48 ? 0u : bit;
+            g *= Y.a[row];
+            row = Y.up[row];
+        }
+        Y.gs[lane] = g;
+        Y.path[lane] = row == -1 ? path : make_uint2(0u, 0u);
     }
 
     // ---- q times the state, or the sketch ----------------------------------------------
@@ -732,7 +805,7 @@ void tree_scan_kernel(TreeArgs A, HeadTable T) {
                 f32x4 c = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
                 for (int b = 0; b < 4; ++b) {
-                    c = multiply(q_at(m, 32 * b), f[b], c);
+                    c = multiply(MT == 1 ? q0[b] : q_at(m, 32 * b), f[b], c);
                     __builtin_amdgcn_sched_barrier(0);
                 }
                 wave_lds();
@@ -751,43 +824,19 @@ void tree_scan_kernel(TreeArgs A, HeadTable T) {
         }
     }
 
-    // ---- decays behind each window slot, and of the whole window ------------------------
-    wave_lds();
-    float all = 1.f;
-    for (int i = sp.p - 1; i >= 0; --i) {
-        if (lane == 0) Y.ws[i] = all;
-        all *= Y.a[i];
-    }
-
 #pragma unroll
     for (int m = 0; m < MT; ++m) {
         const int n0 = 16 * m, left = sp.len - n0;
         if (left <= 0) break;
-        wave_lds();
-        // ---- decays between a tile's nodes and their ancestors ----------------------------
-        if (lane < 16) {
-            const int n = n0 + min(lane, left - 1);
-            float g = 1.f;
-            uint2 path = make_uint2(0u, 0u);
-            int row = 16 + n;
-            while (row >= 0) {
-                Y.p[lane * LP + row] = g;
-                const uint32_t bit = 1u << (row - 16 & 31);
-                path.x |= row < 48 ? bit : 0u;
-                path.y |= row < 48 ? 0u : bit;
-                g *= Y.a[row];
-                row = Y.up[row];
-            }
-            Y.gs[lane] = g;
-            Y.path[lane] = row == -1 ? path : make_uint2(0u, 0u);
-        }
+        float* pt = Y.p + ScanLds<MT>::tile_p(m);
+        const int LP = ScanLds<MT>::row_p(m);
         wave_lds();
         float gr[4];
         uint2 pa[4];
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-            gr[i] = Y.gs[4 * kk + i];
-            pa[i] = Y.path[4 * kk + i];
+            gr[i] = Y.gs[n0 + 4 * kk + i];
+            pa[i] = Y.path[n0 + 4 * kk + i];
             const float g = all * gr[i];
 #pragma unroll
             for (int c = 0; c < CT; ++c) d[m][c][i] *= g;
@@ -795,61 +844,127 @@ void tree_scan_kernel(TreeArgs A, HeadTable T) {
         // ---- P: products q k, each with the decays between its tokens -----------------------
         Raw qf[4];
 #pragma unroll
-        for (int c = 0; c < 4; ++c) qf[c] = q_at(m, 32 * c);
-        bool odd = false;
+        for (int c = 0; c < 4; ++c) qf[c] = MT == 1 ? q0[c] : q_at(m, 32 * c);
+        // group u: the window's slots, then the tiles' nodes
+        auto k_at = [&](int u, int c) {
+            const uint32_t r = u ? min(16 * (u - 1) + j, sp.len - 1) * kstep : max(min(j, sp.p - 1), 0) * kslot;
+            return load_at<Raw>(u ? k_n : k_w, (r * kK + 32 * c + 8 * kk) * E);
+        };
+        auto note = [&](int u, const f32x4& g) {
 #pragma unroll
-        for (int u = 0; u <= m + 1; ++u) {
-            if (u == 0 && !held) continue;
-            __builtin_amdgcn_sched_barrier(0);
-            const int rows = u ? min(16, sp.len - 16 * (u - 1)) : sp.p;
-            const uint32_t ke = ((u ? min(16 * (u - 1) + j, sp.len - 1) * kstep : min(j, sp.p - 1) * kslot) * kK + 8 * kk) * E;
-            Raw kf[4];
-#pragma unroll
-            for (int c = 0; c < 4; ++c) kf[c] = load_at<Raw>(u ? k_n : k_w, ke + 32 * E * c);
-            float v[4][CT];
-#pragma unroll
-            for (int s = 0; s < 4; ++s) {
-                const int r = min(4 * s + kk, rows - 1);
-                if (u) Co::load(v_n, (16 * (u - 1) + r) * (step * V), j, v[s]);
-                else Co::load(v_w, r * (slot * V), j, v[s]);
+            for (int i = 0; i < 4; ++i) {
+                float& p = pt[(4 * kk + i) * LP + 16 * u + j];
+                const int r = 16 * (u - 1) + j;
+                const float f = u ? p * g[i] : gr[i] * Y.ws[j] * g[i];
+                p = (u == 0 ? j < sp.p : ((r < 32 ? pa[i].x : pa[i].y) >> (r & 31) & 1u) != 0u) ? f : 0.f;
             }
-            f32x4 g = {0.f, 0.f, 0.f, 0.f};
+        };
+        // ... and times the values.  One that is no number must not meet the zeros of other
+        // nodes' rows: it is left out here and joins the nodes below it afterwards
+        bool odd = false;
+        if constexpr (BF) {
+            // two groups at a time: their 32 rows are one product's, with P in three terms
 #pragma unroll
-            for (int c = 0; c < 4; ++c) {
-                if constexpr (BF) {
-                    g = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, qf[c].w),
-                                                                __builtin_bit_cast(bf16x8, kf[c].w), g, 0, 0, 0);
-                } else {
+            for (int s = 0; s < (MT + 2) / 2; ++s) {
+                if (2 * s > m + 1) break;
+                const bool two = 2 * s < m + 1;
+                __builtin_amdgcn_sched_barrier(0);
+                Raw kf[2][4];
+                PackedCols<V> v[8];
+#pragma unroll
+                for (int e = 0; e < 2; ++e)
+#pragma unroll
+                    for (int c = 0; c < 4; ++c)
+                        if (!e || two) kf[e][c] = k_at(2 * s + e, c);
+#pragma unroll
+                for (int t = 0; t < 8; ++t) {
+                    const int u = 2 * s + t / 4, r = 4 * kk + t % 4;
+                    if (t >= 4 && !two) v[t].clear();
+                    else if (u) v[t].load(v_n, min(16 * (u - 1) + r, sp.len - 1) * (step * V), j);
+                    else v[t].load(v_w, max(min(r, sp.p - 1), 0) * (slot * V), j);
+                }
+#pragma unroll
+                for (int e = 0; e < 2; ++e) {
+                    if (e && !two) continue;
+                    f32x4 g = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+                    for (int c = 0; c < 4; ++c)
+                        g = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, qf[c].w),
+                                                                    __builtin_bit_cast(bf16x8, kf[e][c].w), g, 0, 0, 0);
+                    note(2 * s + e, g);
+                }
+                wave_lds();
+                const float* pr = pt + j * LP + 32 * s + 4 * kk;
+                const f32x4 p0 = *reinterpret_cast<const f32x4*>(pr);
+                const f32x4 p1 = two ? *reinterpret_cast<const f32x4*>(pr + 16) : f32x4{0.f, 0.f, 0.f, 0.f};
+                const float pv[8] = {p0[0], p0[1], p0[2], p0[3], p1[0], p1[1], p1[2], p1[3]};
+                bf16x8 a[3];
+                split3(pv, a);
+                u32x4 b[CT];
+#pragma unroll
+                for (int c = 0; c < CT; ++c)
+#pragma unroll
+                    for (int t = 0; t < 4; ++t) b[c][t] = PackedCols<V>::pair(v[2 * t], v[2 * t + 1], c);
+                // times zeros they add up to no number if any is none
+                f32x4 nul = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+                for (int c = 0; c < CT; ++c)
+                    nul = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, (u32x4{0u, 0u, 0u, 0u})),
+                                                                  __builtin_bit_cast(bf16x8, b[c]), nul, 0, 0, 0);
+                if (__any(!(nul[0] == 0.f))) {
+                    odd = true;
+#pragma unroll
+                    for (int c = 0; c < CT; ++c)
+#pragma unroll
+                        for (int t = 0; t < 4; ++t) {
+                            const uint32_t u = b[c][t];
+                            b[c][t] = ((u & 0x7f80u) == 0x7f80u ? 0u : u & 0xffffu) |
+                                      ((u & 0x7f800000u) == 0x7f800000u ? 0u : u & 0xffff0000u);
+                        }
+                }
+#pragma unroll
+                for (int c = 0; c < CT; ++c)
+#pragma unroll
+                    for (int e = 0; e < 3; ++e)
+                        d[m][c] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(a[e], __builtin_bit_cast(bf16x8, b[c]), d[m][c],
+                                                                          0, 0, 0);
+            }
+        } else {
+#pragma unroll
+            for (int u = 0; u <= m + 1; ++u) {
+                if (u == 0 && !held) continue;
+                __builtin_amdgcn_sched_barrier(0);
+                const int rows = u ? min(16, sp.len - 16 * (u - 1)) : sp.p;
+                Raw kf[4];
+#pragma unroll
+                for (int c = 0; c < 4; ++c) kf[c] = k_at(u, c);
+                float v[4][CT];
+#pragma unroll
+                for (int s = 0; s < 4; ++s) {
+                    const int r = min(4 * s + kk, rows - 1);
+                    if (u) Co::load(v_n, (16 * (u - 1) + r) * (step * V), j, v[s]);
+                    else Co::load(v_w, r * (slot * V), j, v[s]);
+                }
+                f32x4 g = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+                for (int c = 0; c < 4; ++c) {
                     float k[8];
                     Vec8<QT>::unpack(kf[c], k);
                     g = multiply(qf[c], k, g);
                 }
-            }
+                note(u, g);
+                wave_lds();
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                float& p = Y.p[(4 * kk + i) * LP + 16 * u + j];
-                if (u == 0) {
-                    const float f = gr[i] * Y.ws[j] * g[i];
-                    p = j < sp.p ? f : 0.f;
-                } else {
-                    const int r = 16 * (u - 1) + j;
-                    const float f = p * g[i];
-                    p = (r < 32 ? pa[i].x : pa[i].y) >> (r & 31) & 1u ? f : 0.f;
-                }
-            }
-            wave_lds();
-            // ---- times the values; one that is no number must not meet the zeros of other
-            // nodes' rows: it is left out here and joins the nodes below it afterwards
+                for (int s = 0; s < 4; ++s) {
+                    if (4 * s >= rows) continue;
+                    const bool on = 4 * s + kk < rows;
+                    const float pv = pt[j * LP + 16 * u + 4 * s + kk];
 #pragma unroll
-            for (int s = 0; s < 4; ++s) {
-                if (4 * s >= rows) continue;
-                const bool on = 4 * s + kk < rows;
-                const float pv = Y.p[j * LP + 16 * u + 4 * s + kk];
-#pragma unroll
-                for (int c = 0; c < CT; ++c) {
-                    const bool fin = isfinite(v[s][c]);
-                    odd = odd || !fin;
-                    d[m][c] = mfma_16x16x4(pv, on && fin ? v[s][c] : 0.f, d[m][c]);
+                    for (int c = 0; c < CT; ++c) {
+                        const bool fin = isfinite(v[s][c]);
+                        odd = odd || !fin;
+                        d[m][c] = mfma_16x16x4(pv, on && fin ? v[s][c] : 0.f, d[m][c]);
+                    }
                 }
             }
         }
@@ -868,7 +983,7 @@ void tree_scan_kernel(TreeArgs A, HeadTable T) {
                     else Co::load(v_n, (row - 16) * (step * V), j, f);
 #pragma unroll
                     for (int c = 0; c < CT; ++c)
-                        if (!isfinite(f[c])) y[c] = fmaf(Y.p[rn * LP + row], f[c], y[c]);
+                        if (!isfinite(f[c])) y[c] = fmaf(pt[rn * LP + row], f[c], y[c]);
                 };
                 for (int row = 16 + n; row >= 0; row = Y.up[row]) join(row);
                 for (int row = 0; row < sp.p; ++row) join(row);
@@ -1013,9 +1128,10 @@ hipError_t launch_tree_m(const TreeArgs& a, const HeadTable& t, hipStream_t s) {
 
 template <int V, typename QT, int MT>
 hipError_t launch_scan_m(const TreeArgs& a, const HeadTable& t, hipStream_t s) {
-    const double blocks = (double(a.n_seqs) * a.H + 3) / 4;
-    if (!launch_fits(blocks, 256)) return hipErrorInvalidConfiguration;
-    hipLaunchKernelGGL((tree_scan_kernel<V, QT, MT>), dim3(uint32_t(blocks)), dim3(256), 0, s, a, t);
+    constexpr int waves = scan_waves(MT);
+    const double blocks = (double(a.n_seqs) * a.H + waves - 1) / waves;
+    if (!launch_fits(blocks, 64 * waves)) return hipErrorInvalidConfiguration;
+    hipLaunchKernelGGL((tree_scan_kernel<V, QT, MT>), dim3(uint32_t(blocks)), dim3(64 * waves), 0, s, a, t);
     return hipGetLastError();
 }
 
