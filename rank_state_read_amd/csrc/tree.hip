@@ -650,8 +650,16 @@ struct ScanLds {
 // Waves of a block: their LDS stays below 64 KB.
 __host__ __device__ constexpr int scan_waves(int MT) { return MT == 4 ? 2 : 4; }
 
+// Waves per SIMD the registers are made for: the sums take MT V / 4 of them and the loads in flight
+// V / 2 more.  One wave fewer where that would spill, measured with 64 heads in bf16 (us, more | fewer waves):
+// 12 nodes on the sketch V = 128 67 | 47, V = 112 81 | 52, V = 96 40 | 40, V = 80 38 | 41; 31 nodes on the state V = 128
+// 121 | 77, V = 96 78 | 53, V = 80 44.5 | 46; 64 nodes V = 128 140 | 124, V = 112 154 | 123, V = 96 95 | 105.
+__host__ __device__ constexpr int scan_per_simd(int V, int MT) {
+    return MT == 1 ? (V <= 96 ? 4 : 3) : MT == 2 ? (V <= 80 ? 3 : 2) : V <= 96 ? 2 : 1;
+}
+
 template <int V, typename QT, int MT>
-__global__ __launch_bounds__(64 * scan_waves(MT)) __attribute__((amdgpu_waves_per_eu(MT == 1 ? 4 : MT == 2 ? 3 : 2)))
+__global__ __launch_bounds__(64 * scan_waves(MT)) __attribute__((amdgpu_waves_per_eu(scan_per_simd(V, MT))))
 void tree_scan_kernel(TreeArgs A, HeadTable T) {
     typedef AllCols<V> Co;
     typedef typename Vec8<QT>::raw_t Raw;
