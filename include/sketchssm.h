@@ -37,7 +37,8 @@
  *     status is returned; nothing throws across this boundary;
  *   - a call that would take 2^32 GPU threads or more gives SKSSM_ESHAPE (the ragged
  *     calls from an n_seqs H V of about 2^30 on or, in chunks, a total_tokens H of
- *     2^30; the gated norm from 2^28 norms over one head on);
+ *     2^30; the gated norm from 2^28 norms over one head on; trees from an n_seqs H of
+ *     2^24 on; cached states from an n H of 2^23 on);
  *   - all arrays are dense row-major with the layouts written beside them.
  * Supported shapes: K = 128, W = 16, V a multiple of 16 from 64 to 128 (the
  * Nano layer's 80, GDN/KDA's 128), 1 <= H <= 256,
@@ -442,13 +443,16 @@ sketchssm_status sketchssm_gated_norm(const sketchssm_shape* shape, const float*
  *   q, k    device [total_nodes,Hk,K] qkv dtype;  v device [total_nodes,H,V]
  *   a       device [total_nodes,H] fp32 (Mamba-2, GDN) or [total_nodes,H,K] (KDA)
  *   beta    device [total_nodes,H] fp32 (GDN, KDA); NULL for Mamba-2
- *   y       device [total_nodes,H,V] fp32, out
+ *   y       device [total_nodes,H,V] fp32, out; overlaps none of q, k, v, a, beta
+ *           (SKSSM_EINVAL)
  * The lists are read on the device, so bad values are not reported: a sequence
  * whose row is outside 0 .. B-1, whose pos is outside 0 .. W, whose offsets
  * decrease or leave 0 .. total_nodes or whose tree has more than max_nodes nodes is
  * idle, and so is a node on whose path a parent is not below its child or below -1
  * (its y is left as it was).  Values of tokens that are not on a node's path, an
  * infinity or NaN among them, do not reach it, nor do window slots from pos on.
+ * Sequences that share nodes have no defined results.  Where an infinity enters a
+ * sum, from the state, the window or the node's own path, y may be a NaN instead.
  */
 sketchssm_status sketchssm_tree_read(const sketchssm_plan* plan, const float* S, const float* Z,
                                      const float* frames, const void* kbuf, const void* vbuf,
@@ -465,8 +469,8 @@ sketchssm_status sketchssm_tree_read(const sketchssm_plan* plan, const float* S,
  * number.  A row must have room: flush it before (sketchssm_flush_seq with its
  * pos[row] tokens, then pos[row] = 0) where pos + the path could exceed W.
  *   kbuf, vbuf, abuf, bbuf   the window, in/out
- *   pos     device [B] int32; new_pos device [B] int32, out, another array: also the
- *           entries of rows that no sequence names are copied
+ *   pos     device [B] int32; new_pos device [B] int32, out, no part of pos
+ *           (SKSSM_EINVAL): also the entries of rows that no sequence names are copied
  *   rows    device [n_seqs] int32, each row at most once per call; NULL: sequence i
  *           is row i
  *   accepted  device [n_seqs] int32

@@ -1121,6 +1121,11 @@ __global__ __launch_bounds__(256) void tree_accept_kernel(AcceptArgs A, int grou
 
 namespace {
 
+bool overlap(const void* a, size_t na, const void* b, size_t nb) {
+    const uintptr_t x = reinterpret_cast<uintptr_t>(a), y = reinterpret_cast<uintptr_t>(b);
+    return na && nb && x < y + nb && y < x + na;
+}
+
 template <int KIND, int V, typename QT, int MT>
 hipError_t launch_tree_m(const TreeArgs& a, const HeadTable& t, hipStream_t s) {
     const int bytes = TreeLds<KIND, V, QT>(a.max_nodes, a.sketch).bytes;
@@ -1206,6 +1211,13 @@ extern "C" sketchssm_status sketchssm_tree_read(const sketchssm_plan* plan, cons
         if (ptr && !aligned16(ptr)) return SKSSM_EALIGN;
     if (double(n_seqs) * sh.H * 4 >= 2147483648.0) return SKSSM_ESHAPE;  // block indices stay below 2^31
     if (n_seqs == 0 || total_nodes == 0 || max_nodes == 0) return SKSSM_OK;
+    // a node's y may be written before another one's inputs are read
+    const size_t T = total_nodes, elem = sh.qkv == SKSSM_BF16 ? 2 : 4, y_bytes = T * sh.H * sh.V * 4;
+    const size_t k_bytes = T * kq_heads_of(sh) * kK * elem, a_elems = T * sh.H * (sh.kind == SKSSM_KDA ? kK : 1);
+    if (overlap(y, y_bytes, q, k_bytes) || overlap(y, y_bytes, k, k_bytes) ||
+        overlap(y, y_bytes, v, T * sh.H * sh.V * elem) || overlap(y, y_bytes, a, a_elems * 4) ||
+        overlap(y, y_bytes, beta, beta ? T * sh.H * 4 : 0))
+        return SKSSM_EINVAL;
     TreeArgs A;
     A.S = S;
     A.Z = Z;
@@ -1250,13 +1262,14 @@ extern "C" sketchssm_status sketchssm_tree_accept(const sketchssm_shape* shape, 
     if (st != SKSSM_OK) return st;
     const bool delta = shape->kind != SKSSM_MAMBA2;
     if (n_seqs < 0 || total_nodes < 0) return SKSSM_EINVAL;
-    if (!kbuf || !vbuf || !abuf || !pos || !new_pos || pos == new_pos || !offsets) return SKSSM_EINVAL;
+    if (!kbuf || !vbuf || !abuf || !pos || !new_pos || !offsets) return SKSSM_EINVAL;
     if (delta != (bbuf != nullptr)) return SKSSM_EINVAL;
     if (n_seqs > 0 && !accepted) return SKSSM_EINVAL;
     if (total_nodes > 0 && (!parents || !k || !v || !a || delta != (beta != nullptr))) return SKSSM_EINVAL;
     const void* ptrs[] = {kbuf, vbuf, abuf, bbuf, pos, new_pos, rows, offsets, parents, accepted, k, v, a, beta};
     for (const void* ptr : ptrs)
         if (ptr && !aligned16(ptr)) return SKSSM_EALIGN;
+    if (overlap(pos, size_t(shape->B) * 4, new_pos, size_t(shape->B) * 4)) return SKSSM_EINVAL;
     const int groups = (shape->H + kAcceptHeads - 1) / kAcceptHeads;
     if (!launch_fits((double(n_seqs) + 1) * groups, 256)) return SKSSM_ESHAPE;
     AcceptArgs A;

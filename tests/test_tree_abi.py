@@ -158,3 +158,15 @@ def test_state_cache_object():
     assert c.scales.shape == (3, 2, 128) and c.scales.dtype == torch.bfloat16
     with pytest.raises(KeyError):
         StateCache(3, 2, 128, 64, "fp8", device="cpu")
+
+
+def test_outputs_apart_from_inputs():
+    """y may not overlap a node's inputs, new_pos not pos: other blocks still read them."""
+    plan = _plan()
+    far = {n: (i + 1) << 30 for i, n in enumerate(READ) if n not in NUMBERS}
+    nbytes = {"q": 10 * 8 * 128 * 2, "k": 10 * 8 * 128 * 2, "v": 10 * 8 * 80 * 2, "a": 10 * 8 * 4, "beta": 10 * 8 * 4}
+    for key, n in nbytes.items():
+        for y in (far[key], far[key] + n - 16, far[key] - 10 * 8 * 80 * 4 + 16):
+            assert _read(plan, **dict(far, y=y)) == 1, key
+    for new in (FAKE, FAKE + 16, FAKE - 16):
+        assert _accept(_shape(B=8), new_pos=new) == 1
