@@ -6,6 +6,10 @@
 // both with ties to even and without any rounding before that one, so that a code
 // does not depend on how it is computed.  A row that holds an infinity or a NaN gets
 // the scale NaN and reads back as NaN.
+//
+// Bound by memory.  48 states of 128 heads of 128 x 80 in whole numbers: stored in 67 us (316 MB,
+// 4.7 TB/s, most of it reads), loaded in 54 (5.8 TB/s, most of it writes); 96 of 32 heads of 128 x 128 in
+// e4m3 loaded in 36 (5.6 TB/s).
 #include <hip/hip_runtime.h>
 
 #include <type_traits>
@@ -70,7 +74,8 @@ __device__ __forceinline__ int code_i8(float x, float s, float inv) {
 }  // namespace
 
 // A team of 16 lanes takes kRows key rows: lane l has values 4 l .. 4 l + 3 and, where the row
-// is longer, 64 + 4 l .. 64 + 4 l + 3, so that a row's load and store cover whole lines.
+// is longer, 64 + 4 l .. 64 + 4 l + 3, so that a row's load and store cover whole lines (one row a team, 8
+// values a lane: 170 us for the 120 of the store and the load above).
 constexpr int kRows = 4;
 
 template <int V, int FMT>

@@ -5,7 +5,17 @@
 //     s = k . x,  acc += beta s v,  x <- M^T x          (x = q_n at the start)
 //   y = acc + S^T x (dense head)  |  acc + Z^T (F x) (sketch head)
 // with Mamba-2 M = a I (beta = 1), GDN M = a (I - beta k k^T),
-// KDA M = (I - beta k k^T) diag(a).
+// KDA M = (I - beta k k^T) diag(a).  The products beta s make a matrix P, nodes by
+// rows (window slots and nodes, 0 off a node's path), so that acc = P v is a matrix
+// product, as is the state's or the sketch's part.
+//
+// Every float32 operand keeps its 24 bits: products are fp32, or bf16 with the
+// float32 factor in three terms.  All sums are fp32.  y is within 1.3e-7 of the same sums in 64
+// bits, relative to a call's largest y.
+//
+// Two kernels: the delta rule changes x at every token, so GDN and KDA walk
+// (tree_kernel); Mamba-2 only scales it, so that s = decays times (q k) and all of it is
+// products (tree_scan_kernel).
 #include <hip/hip_runtime.h>
 
 #include <type_traits>
@@ -237,8 +247,22 @@ struct TreeLds {
 
 }  // namespace
 
-// A block per (sequence, head), heads first.  Nodes go in tiles of 16; the state stays in
-// registers from tile to tile.
+// GDN and KDA: a block per (sequence, head), the heads of a sequence in turn, so that heads that
+// share keys run side by side.  Per tile of 16 nodes: the walk, 16 lanes a node with 8 of the 128
+// key elements each, its tokens from LDS; then x S (or F x, Z^T) and P v on the fp32 matrix units, keys
+// halved over two waves and columns over the other two, the halves joined through LDS.
+//   The state is read once, with streaming loads that are made before the walk and stay in
+// registers over all tiles; three waves per SIMD hold it (plain loads and two waves: 102 us for the first
+// call below, then 99.5).  Behind the walk, with four waves, they make no call faster.
+//   Values go to P v behind the walk, two groups of 16 rows on their way.  Any that is no number is
+// zeroed there and joins the nodes below it at the end, since 0 times it would not be 0.
+//   Measured (one call, bf16 but where named): gdn, 128 trees of 16 nodes, 32 heads of 128 on the
+// state: 92 us, 3.8 TB/s (loads of the state alone 51 us, everything but them 59: they overlap
+// little, a block's loads and its walk take turns at three blocks per CU); kda, 160 trees of 10 nodes on
+// sketches of rank 10: 80 us, 2.3 TB/s, of which the walk's vector and LDS instructions take about 50
+// (vector units busy 38%, LDS 25%); float32 chains of 8, 40 x 32 heads of 96: 23.5 us, 3.8 TB/s.
+//   Without gain: eight waves a block, several heads a block with the next one's loads in flight (137 us
+// for the gdn call), fp32 keys in LDS, blocks of a head on one XCD.
 template <int KIND, int V, typename QT, int MT>
 __global__ __launch_bounds__(kTreeThreads) __attribute__((amdgpu_waves_per_eu(3)))
 void tree_kernel(TreeArgs A, HeadTable T) {
@@ -511,8 +535,17 @@ void tree_kernel(TreeArgs A, HeadTable T) {
 // ---------------------------------------------------------------------------
 // Mamba-2: a wave per (sequence, head), up to 16 MT nodes.  Queries are not changed on
 // the way but for the decays, so there is no walk over keys: y = g (q S) + P v with P the
-// products q k times the decays between two tokens of a path.  Nothing is shared by the
-// waves of a block.
+// products q k times the decays between two tokens of a path, one path to a lane.  Nothing is
+// shared by the waves of a block, so that none waits for another.
+//   bf16 activations: q S, q F^T and P v are bf16 products of 32 keys or rows (16 cycles) with S, F
+// and P in three terms (fp32 products take 32 cycles for 4 keys); Z, float32 on both sides, and
+// float32 activations take the fp32 ones.
+//   Bound by the latency of four loads that follow each other (lists, decays and frame, keys and values)
+// at four waves per SIMD, beside vector units that are busy 40% of the time.  Measured: 192 trees
+// of 8 nodes, 128 heads of 80 on sketches of rank 6: 83 us, 2.3 TB/s (68 us with its operands in the
+// last-level cache); 64 trees of 47 nodes on the state: 161 us, 3.4 TB/s.
+// A block per head as for the delta rule took 210 and 285 us; three waves with the keys loaded ahead of the
+// sketch 106 where four without took 89.
 // ---------------------------------------------------------------------------
 namespace {
 
@@ -642,6 +675,8 @@ struct ScanLds {
     int up[ROWS];  // the row before on a path: -1 none, -2 no path
     float ws[16];  // decays behind each window slot
     float gs[16 * MT];  // a node's decays to the tree's root
+    // the nodes of its path.  Two words, and 32-bit shifts wherever they are read: a 64-bit shift
+    // by a lane's amount that lay in the wave's last vector register has shifted by another one.
     uint2 path[16 * MT];
 };
 
@@ -1001,9 +1036,9 @@ void tree_scan_kernel(TreeArgs A, HeadTable T) {
     }
 }
 
-// The path to each sequence's accepted node, its tokens to the row's next window
-// slots.  A block takes one sequence and some heads; the first one, whose paths take longest,
-// writes the new positions.
+// The path to each sequence's accepted node, its tokens to the row's next window slots: copies,
+// exact.  A block takes one sequence and 8 heads; the first block, whose paths take longest, writes the
+// new positions.
 namespace {
 
 struct AcceptArgs {
@@ -1061,7 +1096,9 @@ __device__ __forceinline__ AcceptSpan accept_span(const AcceptArgs& A, int i) {
 }  // namespace
 
 // Bound by latency: the path has to be known before its tokens can be read.  A tree's parents
-// come to LDS in one load, and a block's threads take all tokens of its heads at once.
+// come to LDS in one load, and a block's threads take all tokens of its heads at once.  192 sequences, 128 heads of
+// 80, 4 of 8 tokens each (17 MB): 9.9 us on the GPU, one sequence of 32 KDA heads 3.4 us.  Heads a block, for
+// those two: 4 10.6 and 3.4, 8 9.9 and 3.4, 16 9.2 and 4.1.
 template <typename QT>
 __global__ __launch_bounds__(256) void tree_accept_kernel(AcceptArgs A, int groups) {
     __shared__ int path[kW], staged[kStaged], n_path;
@@ -1148,6 +1185,10 @@ hipError_t launch_scan_m(const TreeArgs& a, const HeadTable& t, hipStream_t s) {
     return hipGetLastError();
 }
 
+// Forms for up to 16, 32 and 64 nodes, by the caller's bound: registers and LDS go by it.  What a bound
+// above the largest tree costs (us by bound): Mamba-2 sketch, 12 nodes, 16 66, 32 84, 64 112; KDA sketch, 17 nodes,
+// 17 78, 32 94, 64 161 (tokens in LDS); GDN chains of 12, 16 24.8, 32 27.4, 64 31.6; GDN on the state, 25
+// nodes, 32 98, 64 98.
 template <int KIND, int V, typename QT>
 hipError_t launch_tree_t(const TreeArgs& a, const HeadTable& t, hipStream_t s) {
     if constexpr (KIND == SKSSM_MAMBA2) {
@@ -1155,9 +1196,9 @@ hipError_t launch_tree_t(const TreeArgs& a, const HeadTable& t, hipStream_t s) {
         if (a.max_nodes <= 32) return launch_scan_m<V, QT, 2>(a, t, s);
         return launch_scan_m<V, QT, 4>(a, t, s);
     } else {
-    if (a.max_nodes <= 16) return launch_tree_m<KIND, V, QT, 1>(a, t, s);
-    if (a.max_nodes <= 32) return launch_tree_m<KIND, V, QT, 2>(a, t, s);
-    return launch_tree_m<KIND, V, QT, 4>(a, t, s);
+        if (a.max_nodes <= 16) return launch_tree_m<KIND, V, QT, 1>(a, t, s);
+        if (a.max_nodes <= 32) return launch_tree_m<KIND, V, QT, 2>(a, t, s);
+        return launch_tree_m<KIND, V, QT, 4>(a, t, s);
     }
 }
 
