@@ -29,14 +29,21 @@ def bf16_tensor(bits: np.ndarray, device) -> torch.Tensor:
 
 class StateCache:
     """Slots for 8-bit copies of a layer's states (``sketchssm_cache_store``): ``codes`` [n_slots, H, K, V] and
-    ``scales`` [n_slots, H, K]; ``format`` is a key of ``binding.CACHE``."""
+    ``scales`` [n_slots, H, K]; ``format`` is a key of ``binding.CACHE``.  A slot that nothing was stored to holds the
+    zero state.  The memory belongs to ``stream`` (None: the current one).  The zeros are there when the cache is, so
+    that a store on any stream comes after them."""
 
-    def __init__(self, n_slots: int, H: int, K: int, V: int, format: str = "i8", device="cuda"):
+    def __init__(self, n_slots: int, H: int, K: int, V: int, format: str = "i8", device="cuda", stream=None):
         _b.CACHE[format]  # a name it does not know is refused here
         kind = torch.int8 if format == "i8" else torch.float8_e4m3fn
         self.format = format
-        self.codes = torch.zeros((n_slots, H, K, V), dtype=torch.int8, device=device).view(kind)
-        self.scales = torch.zeros((n_slots, H, K), dtype=torch.bfloat16, device=device)
+        device = torch.device(device)
+        with _b.owned_by(stream, device):
+            self.codes = torch.zeros((n_slots, H, K, V), dtype=torch.int8, device=device).view(kind)
+            self.scales = torch.zeros((n_slots, H, K), dtype=torch.bfloat16, device=device)
+            # (a stream that records a graph cannot be waited for)
+            if device.type == "cuda" and not torch.cuda.is_current_stream_capturing():
+                torch.cuda.current_stream(self.codes.device).synchronize()
 
 
 class SketchLayer:
@@ -202,9 +209,9 @@ class SketchLayer:
                                 parents, accepted, k, v, a, beta, stream)
         return new_pos
 
-    def new_cache(self, n_slots: int, format: str = "i8") -> StateCache:
-        """An empty cache of this layer's states."""
-        return StateCache(n_slots, self.H, self.K, self.V, format, self.device)
+    def new_cache(self, n_slots: int, format: str = "i8", stream=None) -> StateCache:
+        """An empty cache of this layer's states, for calls on `stream`."""
+        return StateCache(n_slots, self.H, self.K, self.V, format, self.device, stream)
 
     def cache_store(self, cache: StateCache, rows=None, slots=None, stream=None):
         """States of the listed rows (their windows flushed before) to slots of the cache."""

@@ -144,9 +144,10 @@ class SketchModel:
         for L in self.layers:
             L.flush_seq(rows, n_tokens, stream=stream)
 
-    def new_cache(self, n_slots: int, format: str = "i8") -> list:
-        """An empty cache of states per layer."""
-        return [L.new_cache(n_slots, format) for L in self.layers]
+    def new_cache(self, n_slots: int, format: str = "i8", stream=None) -> list:
+        """An empty cache of states per layer, for calls on `stream`."""
+        given = {} if stream is None else {"stream": stream}
+        return [L.new_cache(n_slots, format, **given) for L in self.layers]
 
     def cache_store(self, caches: Sequence, rows: torch.Tensor, slots: torch.Tensor, stream=None):
         """Every layer's states of the listed rows (their windows flushed before) to slots of its cache."""
