@@ -1168,8 +1168,10 @@ hipError_t launch_tree_m(const TreeArgs& a, const HeadTable& t, hipStream_t s) {
     const int bytes = TreeLds<KIND, V, QT>(a.max_nodes, a.sketch).bytes;
     if (!launch_fits(double(a.n_seqs) * a.H, kTreeThreads)) return hipErrorInvalidConfiguration;
     if (bytes > 65536) {
+        // the kernel's limit is shared with calls of other threads: the most it ever takes, so that none lowers it
         const hipError_t e = hipFuncSetAttribute(reinterpret_cast<const void*>(tree_kernel<KIND, V, QT, MT>),
-                                                 hipFuncAttributeMaxDynamicSharedMemorySize, bytes);
+                                                 hipFuncAttributeMaxDynamicSharedMemorySize,
+                                                 TreeLds<KIND, V, QT>(16 * MT, true).bytes);
         if (e != hipSuccess) return e;
     }
     hipLaunchKernelGGL((tree_kernel<KIND, V, QT, MT>), dim3(a.n_seqs * a.H), dim3(kTreeThreads), bytes, s, a, t);
