@@ -385,8 +385,8 @@ def sketchssm_tree_read(plan: Plan, S, Z, frames, kbuf, vbuf, abuf, bbuf, pos, r
     window, lists, n, T, tokens = _tree(sh, rows, offsets, parents, k, v, a, beta, kbuf, vbuf, abuf, bbuf, pos, dev)
     cache = [_arg("S", S, f32, (sh.B, sh.H, sh.K, sh.V), dev), _flat("Z", Z, plan.z_elems, dev),
              _flat("frames", frames, plan.frame_elems, dev)]
-    qq = _arg("q", q, k.dtype, k.shape, dev)
-    yy = _arg("y", y, f32, v.shape, dev)
+    qq = _arg("q", q, torch.bfloat16 if sh.qkv == 0 else f32, (T, sh.kq_heads or sh.H, sh.K), dev)
+    yy = _arg("y", y, f32, (T, sh.H, sh.V), dev)
     with _on_device(dev, stream):
         _check("sketchssm_tree_read",
                lib().sketchssm_tree_read(plan.handle, *cache, *window, *lists[:3], n, T, _int32("max_nodes", max_nodes),
@@ -425,7 +425,10 @@ def _cache(shape, S, rows, codes, scales, slots, fmt):
     f = CACHE[fmt] if isinstance(fmt, str) else _int32("format", fmt)
     n_slots, H, K, V = codes.shape[0], shape.H, shape.K, shape.V
     lists = [x for x in (rows, slots) if x is not None]
-    n = lists[0].numel() if lists else n_slots
+    sized = [x for x in lists if not isinstance(x, int)]
+    if lists and not sized:
+        raise ValueError("rows, slots: the number of pairs is that of a tensor, got addresses")
+    n = sized[0].numel() if sized else n_slots
     for name, x, most in (("rows", rows, shape.B), ("slots", slots, n_slots)):
         if x is None and n > most:
             raise ValueError(f"{name}: {n} pairs and {most} {name}")
