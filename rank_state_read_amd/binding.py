@@ -224,10 +224,11 @@ def sketchssm_decode_read_seq(plan: Plan, S, Z, frames, q, k, v, a, beta, kbuf, 
 
 def sketchssm_flush_seq(plan: Plan, S, Z, basis, kbuf, vbuf, abuf, bbuf, seqs, n_tokens, n_seqs: int,
                         stream=None):
-    _check("sketchssm_flush_seq",
-           lib().sketchssm_flush_seq(plan.handle, _ptr(S), _ptr(Z), _ptr(basis), _ptr(kbuf), _ptr(vbuf),
-                                     _ptr(abuf), _ptr(bbuf), _ptr(seqs), _ptr(n_tokens), int(n_seqs),
-                                     _stream(stream)))
+    with _AS_IS if S is None or isinstance(S, int) else _on_device(S.device, stream):
+        _check("sketchssm_flush_seq",
+               lib().sketchssm_flush_seq(plan.handle, _ptr(S), _ptr(Z), _ptr(basis), _ptr(kbuf), _ptr(vbuf),
+                                         _ptr(abuf), _ptr(bbuf), _ptr(seqs), _ptr(n_tokens), int(n_seqs),
+                                         _stream(stream)))
 
 
 def sketchssm_decode_read_flush(plan: Plan, S, Z, frames, basis, q, k, v, a, beta, kbuf, vbuf, abuf, bbuf, y,
