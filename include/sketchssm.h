@@ -502,7 +502,8 @@ typedef enum {
  * key row with an infinity or NaN gets the scale NaN and reads back as NaN; values
  * whose code s passes fp32's range (states above 3.3e38) read back as infinity.
  * The window is not stored: flush a row (sketchssm_flush_seq) before storing it.
- * After a load, form the row's sketch with sketchssm_flush_seq (0 tokens).
+ * After a load, form the row's sketch with sketchssm_flush_seq (0 tokens) and set its
+ * position to 0: the tokens that the row held back before do not follow its new state.
  *   S       device [B,H,K,V] fp32
  *   codes   device [n_slots,H,K,V], one byte each: the slots of the cache
  *   scales  device [n_slots,H,K] bf16

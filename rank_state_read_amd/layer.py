@@ -219,7 +219,8 @@ class SketchLayer:
 
     def cache_load(self, cache: StateCache, slots=None, rows=None, stream=None):
         """Slots of the cache (negative: the zero state) back to rows' states; the rows' sketches are formed by
-        ``flush_seq`` with 0 tokens."""
+        ``flush_seq`` with 0 tokens, and they hold no tokens back from here on: their positions are the caller's to set
+        to 0."""
         _b.sketchssm_cache_load(self.shape, cache.codes, cache.scales, slots, self.S, rows, cache.format, stream)
 
     def set_norm(self, weight, norm_heads: int, gate: str, eps: float = 1e-5, D=None):

@@ -157,8 +157,8 @@ class SketchModel:
             L.cache_store(c, rows, slots, stream=stream)
 
     def cache_load(self, caches: Sequence, slots: torch.Tensor, rows: torch.Tensor, stream=None):
-        """Slots (negative: the zero state) back to the listed rows of every layer, with their first sketches: the
-        rows then hold no tokens back."""
+        """Slots (negative: the zero state) back to the listed rows of every layer, with their first sketches.  The rows'
+        positions are the caller's: 0 from here on, since what a row held back before does not follow its new state."""
         if len(caches) != len(self.layers):
             raise ValueError("one cache per layer")
         none = self.layers[0].zeros_like(rows, stream)
