@@ -60,27 +60,29 @@ __device__ __forceinline__ SeqSpan seq_span_uniform(const RaggedArgs& A, int i) 
     return s;
 }
 
+// How many lanes below this one are set in a ballot's mask.  (Not by a shift of the mask by the lane's number: on
+// gfx950 a 64-bit shift has taken another amount than its own where that lay in the wave's last vector register.)
+__device__ __forceinline__ int lanes_below(unsigned long long m) {
+    return int(__builtin_amdgcn_mbcnt_hi(uint32_t(m >> 32), __builtin_amdgcn_mbcnt_lo(uint32_t(m), 0u)));
+}
+
 // The sequence that the r-th group of blocks takes where those of more than twice
 // the mean length go first, so that the last blocks to start are short ones.
 __device__ __forceinline__ int seq_long_first(const RaggedArgs& A, int r, int lane) {
     const int bar = 2 * (A.total / A.n_seqs);
-    auto longs = [&](int c) {  // of sequences c .. c + 63
-        const int i = c + lane;
+    auto is_long = [&](int i) {
         const int at = min(i, A.n_seqs - 1);
-        return __ballot(i < A.n_seqs && long(A.offsets[at + 1]) - A.offsets[at] > bar);
+        return long(A.offsets[at + 1]) - A.offsets[at] > bar;
     };
     int n = 0;
-    for (int c = 0; c < A.n_seqs; c += 64) n += __popcll(longs(c));
+    for (int c = 0; c < A.n_seqs; c += 64) n += __popcll(__ballot(c + lane < A.n_seqs && is_long(c + lane)));
     const bool first = r < n;
     if (!first) r -= n;
     for (int c = 0; c < A.n_seqs; c += 64) {
-        unsigned long long m = longs(c);
-        if (!first) m = ~m & (A.n_seqs - c < 64 ? (1ull << (A.n_seqs - c)) - 1 : ~0ull);
+        const bool in = c + lane < A.n_seqs && is_long(c + lane) == first;
+        const unsigned long long m = __ballot(in);
         n = __popcll(m);
-        if (r < n) {
-            const bool mine = (m >> lane & 1) && __popcll(m & ((1ull << lane) - 1)) == r;
-            return c + __ffsll(__ballot(mine)) - 1;
-        }
+        if (r < n) return c + __ffsll(__ballot(in && lanes_below(m) == r)) - 1;
         r -= n;
     }
     return 0;  // r >= n_seqs: no such group

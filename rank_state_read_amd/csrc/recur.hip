@@ -73,7 +73,7 @@ __device__ __forceinline__ int long_sequence(const RaggedArgs& A, int r, int lan
     for (int c = 0; c < A.n_seqs; c += 64) {
         const bool mine = c + lane < A.n_seqs && is_long(A, min(c + lane, A.n_seqs - 1));
         const unsigned long long m = __ballot(mine);
-        if (r < __popcll(m)) return c + __ffsll(__ballot(mine && __popcll(m & ((1ull << lane) - 1)) == r)) - 1;
+        if (r < __popcll(m)) return c + __ffsll(__ballot(mine && lanes_below(m) == r)) - 1;
         r -= __popcll(m);
     }
     return -1;
