@@ -191,8 +191,10 @@ class SketchLayer:
     def tree_read(self, offsets, max_nodes: int, parents, q, k, v, a, beta=None, pos=None, rows=None, y=None, plan=None,
                   stream=None) -> torch.Tensor:
         """Every node's y of the listed rows' trees, over the row's sketch (or state) and its pos[row] held-back
-        tokens (device int32 [B]; None: no row has any).  Nothing of the layer changes.  ``plan``: e.g. an all-dense
-        plan, to verify on the full state.  A y taken here holds nothing defined for nodes of no sequence."""
+        tokens (device int32 [B]; None: no row has any).  Nothing of the layer changes.  ``plan``: a plan whose ranks
+        are all 0, to verify on the full state.  A y taken here holds nothing defined for nodes of no sequence."""
+        if plan is not None and plan.z_elems:
+            raise ValueError("plan: its ranks are not all 0, and the layer's sketch is that of its own plan")
         y = self._new(v.shape, torch.float32, stream) if y is None else y
         pl = self.plan if plan is None else plan
         _b.sketchssm_tree_read(pl, self.S, self.Z if plan is None else None, self.frames if plan is None else None,
