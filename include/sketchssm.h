@@ -38,7 +38,8 @@
  *   - a call that would take 2^32 GPU threads or more gives SKSSM_ESHAPE (the ragged
  *     calls from an n_seqs H V of about 2^30 on or, in chunks, a total_tokens H of
  *     2^30; the gated norm from 2^28 norms over one head on; trees from an n_seqs H of
- *     2^24 on; cached states from an n H of 2^23 on);
+ *     2^24 on, of Mamba-2 2^26; accepted paths from an n_seqs ceil(H / 8) of about 2^24
+ *     on; cached states from an n H of 2^23 on);
  *   - all arrays are dense row-major with the layouts written beside them.
  * Supported shapes: K = 128, W = 16, V a multiple of 16 from 64 to 128 (the
  * Nano layer's 80, GDN/KDA's 128), 1 <= H <= 256,

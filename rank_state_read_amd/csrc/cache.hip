@@ -7,9 +7,11 @@
 // does not depend on how it is computed.  A row that holds an infinity or a NaN gets
 // the scale NaN and reads back as NaN.
 //
-// Bound by memory.  48 states of 128 heads of 128 x 80 in whole numbers: stored in 67 us (316 MB,
-// 4.7 TB/s, most of it reads), loaded in 54 (5.8 TB/s, most of it writes); 96 of 32 heads of 128 x 128 in
-// e4m3 loaded in 36 (5.6 TB/s).
+// 48 states of 128 heads of 128 x 80 (316 MB each way): loaded in 54 us in both formats (5.8 TB/s, most of it
+// writes), which is memory's time; stored in 68 us in whole numbers and 64 in e4m3 (4.7 and 4.9 TB/s, most of it
+// reads).  A store in whole numbers has 786 vector instructions a wave, which keep the vector units busy all along,
+// the one in e4m3 327: what the others cost beside its loads is the 4 us between them.  96 states of 32 heads of
+// 128 x 128 in e4m3 loaded in 37 (5.5 TB/s).
 #include <hip/hip_runtime.h>
 
 #include <type_traits>

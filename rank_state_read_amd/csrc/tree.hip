@@ -10,8 +10,9 @@
 // product, as is the state's or the sketch's part.
 //
 // Every float32 operand keeps its 24 bits: products are fp32, or bf16 with the
-// float32 factor in three terms.  All sums are fp32.  y is within 1.3e-7 of the same sums in 64
-// bits, relative to a call's largest y.
+// float32 factor in three terms.  All sums are fp32.  Errors of y grow with the path, as its roundings' squares
+// add up: in the 2-norm 10 of 2^-24 by that count for 80 tokens on a path, 3.9 measured.  On calls of some 10 nodes a
+// path y was within 1.3e-7 of the same sums in 64 bits, relative to a call's largest y.
 //
 // Two kernels: the delta rule changes x at every token, so GDN and KDA walk
 // (tree_kernel); Mamba-2 only scales it, so that s = decays times (q k) and all of it is
@@ -90,8 +91,9 @@ __device__ __forceinline__ T load_at(const void* base, uint32_t off) {
 }
 
 // A block's rows of CH 16-byte chunks, through registers to LDS.  All loads are made,
-// without a branch to wait behind: rows behind the window's or the tree's last one
-// repeat it, and nothing points to them.
+// without a branch to wait behind (loads of existing rows alone have not been measured
+// beside it): rows behind the window's or the tree's last one repeat it, and nothing
+// points to them.
 template <int CH, int MT>
 struct RowRegs {
     static constexpr int PER = kTreeThreads / CH;  // rows per load of the block
@@ -256,11 +258,13 @@ struct TreeLds {
 // call below, then 99.5).  Behind the walk, with four waves, they make no call faster.
 //   Values go to P v behind the walk, two groups of 16 rows on their way.  Any that is no number is
 // zeroed there and joins the nodes below it at the end, since 0 times it would not be 0.
-//   Measured (one call, bf16 but where named): gdn, 128 trees of 16 nodes, 32 heads of 128 on the
+//   Measured (calls behind each other, bf16 but where named; a kernel trace, which lets none overlap the
+// next, has the first at 98 us): gdn, 128 trees of 16 nodes, 32 heads of 128 on the
 // state: 92 us, 3.8 TB/s (loads of the state alone 51 us, everything but them 59: they overlap
-// little, a block's loads and its walk take turns at three blocks per CU); kda, 160 trees of 10 nodes on
+// little, a block's loads and its walk take turns at three blocks per CU), kda 101; kda, 160 trees of 10 nodes on
 // sketches of rank 10: 80 us, 2.3 TB/s, of which the walk's vector and LDS instructions take about 50
-// (vector units busy 38%, LDS 25%); float32 chains of 8, 40 x 32 heads of 96: 23.5 us, 3.8 TB/s.
+// (vector units busy 42%, LDS 23%), gdn 74, kda in float32 104; gdn, float32 chains of 8, 40 x 32 heads of 96: 23.5 us,
+// 3.8 TB/s.
 //   Without gain: eight waves a block, several heads a block with the next one's loads in flight (137 us
 // for the gdn call), fp32 keys in LDS, blocks of a head on one XCD.
 template <int KIND, int V, typename QT, int MT>
@@ -543,7 +547,8 @@ void tree_kernel(TreeArgs A, HeadTable T) {
 //   Bound by the latency of four loads that follow each other (lists, decays and frame, keys and values)
 // at four waves per SIMD, beside vector units that are busy 40% of the time.  Measured: 192 trees
 // of 8 nodes, 128 heads of 80 on sketches of rank 6: 83 us, 2.3 TB/s (68 us with its operands in the
-// last-level cache); 64 trees of 47 nodes on the state: 161 us, 3.4 TB/s.
+// last-level cache); 64 trees of 47 nodes on the state: 161 us, 3.4 TB/s.  The same in float32, whose products are
+// all fp32 ones: 148 and 322 us.
 // A block per head as for the delta rule took 210 and 285 us; three waves with the keys loaded ahead of the
 // sketch 106 where four without took 89.
 // ---------------------------------------------------------------------------
@@ -686,7 +691,9 @@ struct ScanLds {
 __host__ __device__ constexpr int scan_waves(int MT) { return MT == 4 ? 2 : 4; }
 
 // Waves per SIMD the registers are made for: the sums take MT V / 4 of them and the loads in flight
-// V / 2 more.  One wave fewer where that would spill, measured with 64 heads in bf16 (us, more | fewer waves):
+// V / 2 more.  Chosen by time, which is mostly, but not always, one wave fewer where that would spill: at four waves
+// and up to 16 nodes V = 80 keeps 9 registers in scratch (float32 13, and 3 at V = 96).  Measured with 64 heads in
+// bf16; float32 goes by the same rule, not measured for itself (us, more | fewer waves):
 // 12 nodes on the sketch V = 128 67 | 47, V = 112 81 | 52, V = 96 40 | 40, V = 80 38 | 41; 31 nodes on the state V = 128
 // 121 | 77, V = 96 78 | 53, V = 80 44.5 | 46; 64 nodes V = 128 140 | 124, V = 112 154 | 123, V = 96 95 | 105.
 __host__ __device__ constexpr int scan_per_simd(int V, int MT) {
@@ -1097,8 +1104,8 @@ __device__ __forceinline__ AcceptSpan accept_span(const AcceptArgs& A, int i) {
 
 // Bound by latency: the path has to be known before its tokens can be read.  A tree's parents
 // come to LDS in one load, and a block's threads take all tokens of its heads at once.  192 sequences, 128 heads of
-// 80, 4 of 8 tokens each (17 MB): 9.9 us on the GPU, one sequence of 32 KDA heads 3.4 us.  Heads a block, for
-// those two: 4 10.6 and 3.4, 8 9.9 and 3.4, 16 9.2 and 4.1.
+// 80, 4 of 8 tokens each (17 MB): 10.0 us on the GPU, one sequence of 32 KDA heads 3.9 us.  Heads a block, for
+// those two, measured beside each other on another day: 4 10.6 and 3.4, 8 9.9 and 3.4, 16 9.2 and 4.1.
 template <typename QT>
 __global__ __launch_bounds__(256) void tree_accept_kernel(AcceptArgs A, int groups) {
     __shared__ int path[kW], staged[kStaged], n_path;
